@@ -42,6 +42,17 @@ class _Desc(ctypes.Structure):
                 ("device", ctypes.c_int32), ("timeout_ms", ctypes.c_int32)]
 
 
+class _PagedDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "page_size",
+                                              "max_rows", "dtype", "device", "timeout_ms")]
+
+
+class _CacheView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("s_page", ctypes.c_int64), ("s_slot", ctypes.c_int64),
+                ("s_head", ctypes.c_int64)]
+
+
 def header_symbols() -> list[str]:
     """Names of the functions include/markov.h declares."""
     text = open(HEADER).read()
@@ -88,6 +99,19 @@ def _declare(L):
         "markov_device_math": (i32, [i32, P, P, i64, P]),
         "markov_plan_query": (i64, [P, i32]),
         "markov_plan_inject_status": (i32, [P, i32, c.c_uint32]),
+        "markov_paged_plan_create": (i32, [c.POINTER(_PagedDesc), c.POINTER(P)]),
+        "markov_paged_plan_destroy": (None, [P]),
+        "markov_paged_plan_status": (i32, [P]),
+        "markov_paged_plan_inject_status": (i32, [P, i32, c.c_uint32]),
+        "markov_paged_layout": (i32, [P, P, P, P, i32, P, i64, i32, i32, P, P, i64, P, P, P, P, P,
+                                      P, P, i32, P]),
+        "markov_paged_write": (i32, [P, P, i64, i64, P, i64, i64, c.POINTER(_CacheView),
+                                     c.POINTER(_CacheView), P, i32, P]),
+        "markov_paged_attention": (i32, [P, P, i64, i64, c.POINTER(_CacheView),
+                                         c.POINTER(_CacheView), P, i64, i32, i32, P, P, P, i32,
+                                         i32, f32, i32, i32, P, i64, i64, P, P]),
+        "markov_verify": (i32, [P, P, i32, i64, i64, P, i64, P, i32, i64, i64, P, P, i64, P, i64,
+                                P, i32, P, i64, P, P, P, P]),
         "markov_selftest_wait": (i32, [i32, i32, P]),
     }
     for name, (res, args) in sig.items():
@@ -129,6 +153,7 @@ def _dev_or_pinned(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
 
 MARKOV_BF16 = 0
 MARKOV_F32 = 1
+MARKOV_F16 = 2
 
 
 class Plan:
@@ -375,3 +400,256 @@ def markov_selftest_wait(which: int, timeout_us: int, stream=None) -> int:
     if code not in (0, 4):
         raise MarkovError(code, "markov_selftest_wait")
     return int(code)
+
+
+# ---------------------------------------------------------------- verify step
+
+class PagedPlan:
+    """What the paged calls need besides their arguments, allocated once.
+    dtype (bfloat16 or float16) is that of queries, keys, values and outputs."""
+
+    def __init__(self, q_heads: int, kv_heads: int, head_dim: int, page_size: int,
+                 dtype: torch.dtype = torch.bfloat16, max_rows: int = 256,
+                 device: int | None = None, timeout_ms: int = 0):
+        codes = {torch.bfloat16: MARKOV_BF16, torch.float16: MARKOV_F16}
+        if dtype not in codes:
+            raise TypeError("dtype must be bfloat16 or float16")
+        if device is None:
+            device = torch.cuda.current_device()
+        d = _PagedDesc(q_heads, kv_heads, head_dim, page_size, max_rows, codes[dtype], device,
+                       timeout_ms)
+        h = ctypes.c_void_p()
+        _check(lib().markov_paged_plan_create(ctypes.byref(d), ctypes.byref(h)),
+               "markov_paged_plan_create")
+        self._h = h
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
+        self.page_size, self.dtype, self.max_rows, self.device = page_size, dtype, max_rows, device
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().markov_paged_plan_destroy(self._h)
+            self._h = None
+
+    def __del__(self):  # pragma: no cover
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def markov_paged_plan_status(plan: PagedPlan) -> int:
+    """The sticky device status of the plan's calls (0 = ok); clears it."""
+    return int(lib().markov_paged_plan_status(plan.handle))
+
+
+def markov_paged_plan_inject_status(plan: PagedPlan, code: int, where: int = 0):
+    """Record a device status as a failing kernel would (test hook)."""
+    _check(lib().markov_paged_plan_inject_status(plan.handle, int(code), int(where)),
+           "markov_paged_plan_inject_status")
+
+
+def _new(stream, shape, dtype, device):
+    """An output allocated here; the allocator learns of a call's other stream."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        # its memory may still be in use by earlier work of the current stream
+        stream.wait_stream(torch.cuda.current_stream(device))
+        t.record_stream(stream)
+    return t
+
+
+def _flat(t: torch.Tensor, dtype: torch.dtype, n: int, name: str) -> int:
+    """A contiguous CUDA tensor of n elements."""
+    p = _dev(t, dtype, name)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
+    return p
+
+
+def _page_table(page_table) -> int:
+    p = _dev(page_table, torch.int32, "page_table")
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [states, pages] with contiguous rows")
+    return p
+
+
+def _table_s0(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _cache_view(plan: PagedPlan, t, name: str) -> _CacheView:
+    p = _dev(t, plan.dtype, name)
+    if t.dim() != 4 or tuple(t.shape[1:]) != (plan.page_size, plan.kv_heads, plan.head_dim):
+        raise ValueError(f"{name} must be [pages, {plan.page_size}, {plan.kv_heads}, "
+                         f"{plan.head_dim}], got {tuple(t.shape)}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    # the stride of a dimension of one element says nothing
+    return _CacheView(p, t.shape[0], s[0] if t.shape[0] > 1 else 0, s[1],
+                      s[2] if plan.kv_heads > 1 else plan.head_dim)
+
+
+def _token_rows(plan: PagedPlan, t, heads: int, name: str):
+    """(pointer, token stride, head stride) of [tokens, heads, head_dim]."""
+    p = _dev(t, plan.dtype, name)
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != plan.head_dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {plan.head_dim}], "
+                         f"got {tuple(t.shape)}")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return p, s[0] if t.shape[0] > 1 else 0, s[1] if heads > 1 else plan.head_dim
+
+
+def markov_paged_layout(plan: PagedPlan, context_lens, query_lens, row_state_idx, page_table,
+                        pages_held, free_pages, free_state, num_tokens: int, query_start=None,
+                        seq_lens=None, positions=None, slots=None, pages_held_out=None,
+                        free_state_out=None, stream=None):
+    """Give every row's new tokens pages and slots; returns (query_start,
+    seq_lens, positions, slots).  page_table [states, pages], pages_held
+    [states], the ring free_pages and its [head, count] free_state are updated
+    in place (pages_held and free_state only where no *_out is given).
+    num_tokens is the length of positions and slots, at least the rows' new
+    tokens together; what is beyond them is 0 and -1."""
+    rows = context_lens.shape[0]
+    dev = context_lens.device
+    num_tokens = int(num_tokens)
+    if query_start is None:
+        query_start = _new(stream, (rows + 1,), torch.int32, dev)
+    if seq_lens is None:
+        seq_lens = _new(stream, (rows,), torch.int32, dev)
+    if positions is None:
+        positions = _new(stream, (num_tokens,), torch.int32, dev)
+    if slots is None:
+        slots = _new(stream, (num_tokens,), torch.int64, dev)
+    if pages_held_out is None:
+        pages_held_out = pages_held
+    if free_state_out is None:
+        free_state_out = free_state
+    table = _page_table(page_table)
+    states = page_table.shape[0]
+    i32, i64 = torch.int32, torch.int64
+    code = lib().markov_paged_layout(
+        plan.handle, _flat(context_lens, i32, rows, "context_lens"),
+        _flat(query_lens, i32, rows, "query_lens"),
+        _flat(row_state_idx, i64, rows, "row_state_idx"), rows, table, _table_s0(page_table),
+        states, page_table.shape[1], _flat(pages_held, i32, states, "pages_held"),
+        _flat(free_pages, i32, free_pages.numel(), "free_pages"), free_pages.numel(),
+        _flat(free_state, i64, 2, "free_state"),
+        _flat(pages_held_out, i32, states, "pages_held_out"),
+        _flat(free_state_out, i64, 2, "free_state_out"),
+        _flat(query_start, i32, rows + 1, "query_start"), _flat(seq_lens, i32, rows, "seq_lens"),
+        _flat(positions, i32, num_tokens, "positions"), _flat(slots, i64, num_tokens, "slots"),
+        num_tokens, _stream(stream))
+    _check(code, "markov_paged_layout")
+    return query_start, seq_lens, positions, slots
+
+
+def markov_paged_write(plan: PagedPlan, key, value, k_cache, v_cache, slots, stream=None):
+    """Store key and value [tokens, kv_heads, head_dim] at their slots of the
+    caches [pages, page_size, kv_heads, head_dim] (any strides with the last
+    1, so a view of a heads-outside cache is one too); slot -1 is skipped."""
+    kp, k0, k1 = _token_rows(plan, key, plan.kv_heads, "key")
+    vp, v0, v1 = _token_rows(plan, value, plan.kv_heads, "value")
+    T = key.shape[0]
+    if value.shape[0] != T:
+        raise ValueError("key and value must have the same tokens")
+    kc, vc = _cache_view(plan, k_cache, "k_cache"), _cache_view(plan, v_cache, "v_cache")
+    code = lib().markov_paged_write(plan.handle, kp, k0, k1, vp, v0, v1, ctypes.byref(kc),
+                                    ctypes.byref(vc), _flat(slots, torch.int64, T, "slots"), T,
+                                    _stream(stream))
+    _check(code, "markov_paged_write")
+
+
+def markov_paged_attention(plan: PagedPlan, q, k_cache, v_cache, page_table, row_state_idx,
+                           query_start, seq_lens, scale: float | None = None, window: int = 0,
+                           sinks: int = 0, out=None, lse=None, stream=None):
+    """Attention of each row's new tokens q [tokens, q_heads, head_dim] over
+    its cached keys; returns (out, lse).  scale defaults to head_dim ** -0.5;
+    window 0 sees everything before a token, window w the w last keys and the
+    first `sinks`.  lse [tokens, q_heads] fp32 is computed when a tensor, or
+    True to allocate one, is given.  Tokens of padding rows are not written."""
+    rows = row_state_idx.shape[0]
+    qp, q0, q1 = _token_rows(plan, q, plan.q_heads, "q")
+    T = q.shape[0]
+    if out is None:
+        out = _new(stream, (T, plan.q_heads, plan.head_dim), plan.dtype, q.device)
+    op, o0, o1 = _token_rows(plan, out, plan.q_heads, "out")
+    if out.shape[0] != T:
+        raise ValueError("out must have q's tokens")
+    if lse is True:
+        lse = _new(stream, (T, plan.q_heads), torch.float32, q.device)
+    kc, vc = _cache_view(plan, k_cache, "k_cache"), _cache_view(plan, v_cache, "v_cache")
+    table = _page_table(page_table)
+    code = lib().markov_paged_attention(
+        plan.handle, qp, q0, q1, ctypes.byref(kc), ctypes.byref(vc), table,
+        _table_s0(page_table), page_table.shape[0], page_table.shape[1],
+        _flat(row_state_idx, torch.int64, rows, "row_state_idx"),
+        _flat(query_start, torch.int32, rows + 1, "query_start"),
+        _flat(seq_lens, torch.int32, rows, "seq_lens"), rows, T,
+        float(plan.head_dim ** -0.5 if scale is None else scale), int(window), int(sinks), op, o0,
+        o1, None if lse is None else _flat(lse, torch.float32, T * plan.q_heads, "lse"),
+        _stream(stream))
+    _check(code, "markov_paged_attention")
+    return out, lse
+
+
+def markov_verify(plan: Plan, target_logits, draft_tokens, logit_cache, temperature, uniforms,
+                  noise, row_state_idx, tokens=None, num_accepted=None, target_probs=None,
+                  draft_probs=None, stream=None):
+    """Accept a prefix of each row's drafts and draw the token after it;
+    returns (tokens [rows, N + 1], num_accepted [rows]).  target_logits is
+    [rows, N + 1, V], logit_cache the [rows, N, V] cache the drafts were drawn
+    from (either bfloat16 or float32), uniforms [rows, N] in [0, 1), noise
+    [rows, V] Gumbel noise of other seeds than the drafts' (markov_gumbel_noise
+    with one position).  target_probs and draft_probs [rows, N], given
+    together, receive each draft's probability under the two models."""
+    rows, N, V = logit_cache.shape
+    dtypes = {torch.bfloat16: MARKOV_BF16, torch.float32: MARKOV_F32}
+    if target_logits.dtype not in dtypes or logit_cache.dtype not in dtypes:
+        raise TypeError("target_logits and logit_cache must be bfloat16 or float32")
+    if (N, V) != (plan.num_steps, plan.vocab) or tuple(target_logits.shape) != (rows, N + 1, V):
+        raise ValueError(f"logit_cache must be [rows, {plan.num_steps}, {plan.vocab}] and "
+                         f"target_logits [rows, {plan.num_steps + 1}, {plan.vocab}]")
+    if target_logits.stride(2) != 1 or logit_cache.stride(2) != 1 or noise.stride(-1) != 1:
+        raise ValueError("the last dimension of target_logits, logit_cache and noise must be "
+                         "contiguous")
+    if tuple(draft_tokens.shape) != (rows, N) or tuple(uniforms.shape) != (rows, N) or \
+            tuple(noise.shape) != (rows, V):
+        raise ValueError("draft_tokens and uniforms must be [rows, N], noise [rows, V]")
+    dev = target_logits.device
+    if tokens is None:
+        tokens = _new(stream, (rows, N + 1), torch.int64, dev)
+    if num_accepted is None:
+        num_accepted = _new(stream, (rows,), torch.int32, dev)
+    if tuple(tokens.shape) != (rows, N + 1):
+        raise ValueError("tokens must be [rows, N + 1]")
+    if (N > 1 and (draft_tokens.stride(1) != 1 or uniforms.stride(1) != 1)) or tokens.stride(1) != 1:
+        raise ValueError("the last dimension of draft_tokens, uniforms and tokens must be contiguous")
+
+    def s0(t):
+        return t.stride(0) if rows > 1 else max(t.stride(0), t.shape[-1])
+
+    code = lib().markov_verify(
+        plan.handle, _dev(target_logits, target_logits.dtype, "target_logits"),
+        dtypes[target_logits.dtype], target_logits.stride(0), target_logits.stride(1),
+        _dev(draft_tokens, torch.int64, "draft_tokens"), s0(draft_tokens),
+        _dev(logit_cache, logit_cache.dtype, "logit_cache"), dtypes[logit_cache.dtype],
+        logit_cache.stride(0), logit_cache.stride(1),
+        _flat(temperature, torch.float32, rows, "temperature"),
+        _dev(uniforms, torch.float32, "uniforms"), s0(uniforms),
+        _dev(noise, torch.float32, "noise"), s0(noise),
+        _flat(row_state_idx, torch.int64, rows, "row_state_idx"), rows,
+        _dev(tokens, torch.int64, "tokens"), s0(tokens),
+        _flat(num_accepted, torch.int32, rows, "num_accepted"),
+        None if target_probs is None else _flat(target_probs, torch.float32, rows * N,
+                                                "target_probs"),
+        None if draft_probs is None else _flat(draft_probs, torch.float32, rows * N,
+                                               "draft_probs"), _stream(stream))
+    _check(code, "markov_verify")
+    return tokens, num_accepted

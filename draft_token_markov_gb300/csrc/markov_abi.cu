@@ -10,7 +10,9 @@
 #include <new>
 
 #include "../../include/markov.h"
+#include "host_util.h"
 #include "internal.h"
+#include "paged.h"
 
 using namespace dtm;
 
@@ -40,6 +42,11 @@ struct markov_plan {
     uint64_t *bwin = nullptr;
     uint32_t *bcnt = nullptr;
     bool batch_dirty = false;
+    // acceptance: softmax partials, and per row the best key and a counter
+    // (zero between calls)
+    uint4 *vpart = nullptr;
+    uint64_t *vwin = nullptr;
+    uint32_t *varr = nullptr;
     size_t tc_slots_n = 0;
     CUtensorMap tmap;
     const void *tmap_head = nullptr;
@@ -53,23 +60,6 @@ struct markov_plan {
 };
 
 namespace {
-
-// Makes the plan's device current for the duration of a call and restores
-// the caller's device afterwards.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) { ok = false; return; }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard() {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; }
 
 bool valid_rank(int r) { return r == 64 || r == 128 || r == 256; }
 
@@ -85,6 +75,9 @@ void free_plan(markov_plan *p) {
     if (p->tok_slots) cudaFree(p->tok_slots);
     if (p->win_max) cudaFree(p->win_max);
     if (p->win_cnt) cudaFree(p->win_cnt);
+    if (p->vpart) cudaFree(p->vpart);
+    if (p->vwin) cudaFree(p->vwin);
+    if (p->varr) cudaFree(p->varr);
     if (p->ev_fork) cudaEventDestroy(p->ev_fork);
     if (p->ev_noise) cudaEventDestroy(p->ev_noise);
     if (p->side) cudaStreamDestroy(p->side);
@@ -220,6 +213,11 @@ markov_status markov_plan_create(const markov_desc *desc, markov_plan **out) {
         cudaMalloc(&p->win_cnt, kWinCntN * sizeof(uint32_t)) != cudaSuccess ||
         cudaMemset(p->win_max, 0, kWinMaxN * sizeof(uint64_t)) != cudaSuccess ||
         cudaMemset(p->win_cnt, 0, kWinCntN * sizeof(uint32_t)) != cudaSuccess ||
+        cudaMalloc(&p->vpart, (size_t)d.max_rows * (2 * d.num_steps + 1) * kVerifyMaxSegs * sizeof(uint4)) != cudaSuccess ||
+        cudaMalloc(&p->vwin, d.max_rows * sizeof(uint64_t)) != cudaSuccess ||
+        cudaMalloc(&p->varr, d.max_rows * sizeof(uint32_t)) != cudaSuccess ||
+        cudaMemset(p->vwin, 0, d.max_rows * sizeof(uint64_t)) != cudaSuccess ||
+        cudaMemset(p->varr, 0, d.max_rows * sizeof(uint32_t)) != cudaSuccess ||
         cudaMalloc(&p->bwin, kBatchWinN * sizeof(uint64_t)) != cudaSuccess ||
         cudaMalloc(&p->bcnt, kBatchCntN * sizeof(uint32_t)) != cudaSuccess ||
         cudaMemset(p->bwin, 0, kBatchWinN * sizeof(uint64_t)) != cudaSuccess ||
@@ -517,6 +515,68 @@ markov_status markov_plan_inject_status(markov_plan *p, markov_status code, uint
     const uint32_t w[2] = {(uint32_t)code, where};
     if (cudaDeviceSynchronize() != cudaSuccess ||
         cudaMemcpy(p->ctrl + 2, w, sizeof(w), cudaMemcpyHostToDevice) != cudaSuccess) {
+        cudaGetLastError();
+        return MARKOV_ECUDA;
+    }
+    return MARKOV_OK;
+}
+
+markov_status markov_verify(markov_plan *p, const void *target_logits, markov_dtype target_dtype,
+                            int64_t target_s0, int64_t target_s1, const int64_t *draft_tokens,
+                            int64_t draft_s0, const void *logit_cache, markov_dtype cache_dtype,
+                            int64_t cache_s0, int64_t cache_s1, const float *temperature,
+                            const float *uniforms, int64_t uni_s0, const float *noise,
+                            int64_t noise_s0, const int64_t *row_state_idx, int32_t rows,
+                            int64_t *tokens, int64_t tok_s0, int32_t *num_accepted,
+                            float *target_probs, float *draft_probs, void *stream) {
+    if (!p) return MARKOV_EINVAL;
+    if ((target_dtype != MARKOV_BF16 && target_dtype != MARKOV_F32) ||
+        (cache_dtype != MARKOV_BF16 && cache_dtype != MARKOV_F32))
+        return MARKOV_EINVAL;
+    const int64_t te = target_dtype == MARKOV_F32 ? 4 : 2, ce = cache_dtype == MARKOV_F32 ? 4 : 2;
+    const int V = p->d.vocab, N = p->d.num_steps;
+    if (!target_logits || !draft_tokens || !logit_cache || !temperature || !uniforms || !noise ||
+        !row_state_idx || !tokens || !num_accepted || !target_probs != !draft_probs)
+        return MARKOV_EINVAL;
+    if (rows < 1 || rows > p->d.max_rows) return MARKOV_EINVAL;
+    if (target_s1 < V || target_s0 < N * target_s1 + V) return MARKOV_EINVAL;
+    if (cache_s1 < V || cache_s0 < (N - 1) * cache_s1 + V) return MARKOV_EINVAL;
+    if (draft_s0 < N || uni_s0 < N || tok_s0 < N + 1 || noise_s0 < V) return MARKOV_EINVAL;
+    if (!aligned16(target_logits) || !aligned16(logit_cache) || !aligned16(noise) ||
+        (target_s0 * te) % 16 != 0 || (target_s1 * te) % 16 != 0 || (cache_s0 * ce) % 16 != 0 ||
+        (cache_s1 * ce) % 16 != 0 || noise_s0 % 4 != 0)
+        return MARKOV_EINVAL;
+    DeviceGuard guard(p->d.device);
+    if (!guard.ok) return MARKOV_EDEVICE;
+
+    VerifyArgs a{};
+    a.target = target_logits;
+    a.target_s0 = target_s0;
+    a.target_s1 = target_s1;
+    a.draft = draft_tokens;
+    a.draft_s0 = draft_s0;
+    a.cache = logit_cache;
+    a.cache_s0 = cache_s0;
+    a.cache_s1 = cache_s1;
+    a.temperature = temperature;
+    a.uniforms = uniforms;
+    a.uni_s0 = uni_s0;
+    a.noise = noise;
+    a.noise_s0 = noise_s0;
+    a.idx = row_state_idx;
+    a.rows = rows;
+    a.N = N;
+    a.V = V;
+    a.tokens = tokens;
+    a.tok_s0 = tok_s0;
+    a.accepted = num_accepted;
+    a.p = target_probs;
+    a.q = draft_probs;
+    a.part = p->vpart;
+    a.win = p->vwin;
+    a.arrivals = p->varr;
+    a.status = p->ctrl + 2;
+    if (launch_verify(a, te == 4, ce == 4, p->sm_count, (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();
         return MARKOV_ECUDA;
     }

@@ -62,7 +62,8 @@ typedef enum markov_mode {
  * page: the chain kernel is compiled per base and cache dtype, BF16 or fp32). */
 typedef enum markov_dtype {
     MARKOV_BF16 = 0,
-    MARKOV_F32 = 1
+    MARKOV_F32 = 1,
+    MARKOV_F16 = 2              /* the paged calls only */
 } markov_dtype;
 
 typedef enum markov_path {
@@ -390,6 +391,191 @@ markov_status markov_chain_sample_sharded(markov_shard_plan *plan, const uint16_
                                           int64_t *const *draft_tokens, int64_t tok_s0,
                                           uint16_t *const *logit_caches, int64_t cache_s0,
                                           int64_t cache_s1, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The verify step: what a serving loop does with the drawn tokens.
+ *
+ * The target model runs over each request's last token and its N drafts in
+ * one pass.  markov_paged_layout gives the new tokens room in a paged
+ * key/value cache, markov_paged_write stores their keys and values there,
+ * markov_paged_attention lets them attend to the cache, and markov_verify
+ * compares the target's logits with the draft-logits cache that
+ * markov_chain_sample wrote, accepts a prefix of the drafts and draws the
+ * token after it.  No counterpart on the documentation pages, which end at
+ * the draft tokens and their logits: these are additions of this library.
+ *
+ * Common terms.  Requests have a row b of the call and a state s =
+ * row_state_idx[b] (int64, as in markov_chain_sample; < 0 marks a padding
+ * row).  State s owns row s of the page table: its key j lies at slot
+ * j % page_size of page page_table[s][j / page_size].  The new tokens of all
+ * rows are packed one after the other; row b's are [query_start[b],
+ * query_start[b + 1]).
+ *
+ * A paged plan holds what the calls need besides their arguments (partial
+ * results of split rows, counters, the status word).  Calls on one plan must
+ * not overlap on the GPU; calls that may overlap need plans of their own. */
+typedef struct markov_paged_desc {
+    int32_t q_heads;      /* a multiple of kv_heads; kv_heads <= q_heads <= 256 */
+    int32_t kv_heads;     /* >= 1 */
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t page_size;    /* a power of two, 8 .. 256 */
+    int32_t max_rows;     /* request rows of a call, 1 .. 1024 */
+    int32_t dtype;        /* of queries, keys, values and outputs: MARKOV_BF16 or MARKOV_F16 */
+    int32_t device;
+    int32_t timeout_ms;   /* bounds every in-kernel wait (0 selects 1000 ms) */
+} markov_paged_desc;
+
+typedef struct markov_paged_plan markov_paged_plan;
+
+/* Validate `desc` and allocate the plan's scratch, once (CUDA graphs keep its
+ * addresses).  EINVAL for a bad desc, EDEVICE for a bad device, EUNSUPPORTED
+ * for one the kernels are not built for; *out is NULL then. */
+markov_status markov_paged_plan_create(const markov_paged_desc *desc, markov_paged_plan **out);
+
+/* Synchronize the plan's device work and free its scratch.  NULL is a no-op. */
+void markov_paged_plan_destroy(markov_paged_plan *plan);
+
+/* Synchronize, return and clear the sticky device status, as
+ * markov_plan_status; a call made while a status is pending computes nothing. */
+markov_status markov_paged_plan_status(markov_paged_plan *plan);
+
+/* Record a device status as a failing kernel would (test hook), as
+ * markov_plan_inject_status. */
+markov_status markov_paged_plan_inject_status(markov_paged_plan *plan, markov_status code,
+                                              uint32_t where);
+
+/* Give every row's new tokens their place in the paged cache; one launch.
+ * All pointers are device memory.
+ *   context_lens  int32 [rows]: tokens the row has in the cache already.
+ *   query_lens    int32 [rows]: new tokens.
+ *   row_state_idx int64 [rows], distinct among live rows.
+ *   page_table    int32 [num_states, table_width], row stride table_s0,
+ *                 updated in place; table_width >= 1.
+ *   pages_held    int32 [num_states]: pages each state owns.
+ *   free_pages    int32 [ring_size]: a ring of free page ids, updated in
+ *                 place; its free entries are the free_state[1] ones from
+ *                 position free_state[0] on.  ring_size must be at least the
+ *                 number of pages there are.
+ *   free_state    int64 [2]: head and count of the ring.
+ * Each row ends with exactly ceil((context + query) / page_size) pages: the
+ * missing ones are taken from the ring's head, in row order, and pages it
+ * holds beyond them (rejected drafts, a row whose context was set to 0 to
+ * release it) go to the ring's tail, to be taken by later calls.
+ * Outputs:
+ *   pages_held_out int32 [num_states], written for the states of granted
+ *                 rows; free_state_out int64 [2].  Both may be the inputs.
+ *   query_start   int32 [rows + 1]: prefix sums of max(query_lens, 0), over
+ *                 padding and refused rows too.
+ *   seq_lens      int32 [rows]: context + query; 0 for padding and refused rows.
+ *   positions     int32 [num_tokens] and slots int64 [num_tokens]: each new
+ *                 token's position in its request and its slot page *
+ *                 page_size + offset; 0 and -1 for the tokens of padding and
+ *                 refused rows and past the last row's.
+ * A row is refused, its state left as it is, when its context or query
+ * length is negative, its state is not below num_states, the row's pages
+ * exceed table_width, or the pages that it and the rows before it need
+ * exceed the free count (rows after it that need none are still granted).
+ * EINVAL for bad sizes or a missing pointer. */
+markov_status markov_paged_layout(markov_paged_plan *plan, const int32_t *context_lens,
+                                  const int32_t *query_lens, const int64_t *row_state_idx,
+                                  int32_t rows, int32_t *page_table, int64_t table_s0,
+                                  int32_t num_states, int32_t table_width,
+                                  const int32_t *pages_held, int32_t *free_pages,
+                                  int64_t ring_size, const int64_t *free_state,
+                                  int32_t *pages_held_out, int64_t *free_state_out,
+                                  int32_t *query_start, int32_t *seq_lens, int32_t *positions,
+                                  int64_t *slots, int32_t num_tokens, void *stream);
+
+/* Strides of a paged cache, in elements: element (page, slot, head, d) lies
+ * at page * s_page + slot * s_slot + head * s_head + d, so the heads may be
+ * outside or inside a page's slots.  All multiples of 8, base 16-byte
+ * aligned; a page's elements must not overlap another's. */
+typedef struct markov_cache_view {
+    void *data;
+    int64_t num_pages;
+    int64_t s_page, s_slot, s_head;
+} markov_cache_view;
+
+/* Store keys and values [num_tokens, kv_heads, head_dim] at their slots.
+ * key / value: element (t, h, d) at t * s0 + h * s1 + d, strides multiples
+ * of 8, 16-byte aligned.  Tokens whose slot is negative or not below
+ * num_pages * page_size are skipped; slots are distinct. */
+markov_status markov_paged_write(markov_paged_plan *plan, const void *key, int64_t key_s0,
+                                 int64_t key_s1, const void *value, int64_t value_s0,
+                                 int64_t value_s1, const markov_cache_view *k_cache,
+                                 const markov_cache_view *v_cache, const int64_t *slots,
+                                 int32_t num_tokens, void *stream);
+
+/* Attention of each row's new tokens over its cached keys, its own included
+ * (write them first).  Token j of row b, with n = query_start[b + 1] -
+ * query_start[b] tokens, has the position p = seq_lens[b] - n + j and sees
+ * key i when 0 <= i <= p and, with window > 0, also i > p - window or i <
+ * sinks.  For each query head h, with key head h / (q_heads / kv_heads):
+ *   s_i = scale * q . k_i,  out = sum_i exp(s_i - m) v_i / sum_i exp(s_i - m),
+ *   lse = m + ln sum_i exp(s_i - m)  (m the largest s_i; natural logarithm),
+ * scores, softmax sums and outputs in fp32; the weights exp(s_i - m) are
+ * rounded to the plan's dtype for their product with the values, and the
+ * result once.  A token that sees no key gets zeros and lse = -inf.
+ *   q, out        [num_tokens, q_heads, head_dim], strides s0 (token) and s1
+ *                 (head) multiples of 8, 16-byte aligned; out != q.
+ *   lse           fp32 [num_tokens, q_heads] contiguous, or NULL.
+ *   seq_lens      int32 [rows]; at most table_width * page_size (longer ones
+ *                 see the table's keys only).
+ * Padding rows, and tokens outside every row, are not written.  Keys and
+ * values that no token of the row sees (slots past its length, before its
+ * window, foreign pages) may hold anything, NaN included, and table entries
+ * for them are not read; page ids outside [0, num_pages) read as zeros.
+ * Keys that one token of the row sees and another does not may be anything
+ * too, values there must be finite.  One launch.  EINVAL for a bad shape,
+ * stride or alignment. */
+markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int64_t q_s0,
+                                     int64_t q_s1, const markov_cache_view *k_cache,
+                                     const markov_cache_view *v_cache, const int32_t *page_table,
+                                     int64_t table_s0, int32_t num_states, int32_t table_width,
+                                     const int64_t *row_state_idx, const int32_t *query_start,
+                                     const int32_t *seq_lens, int32_t rows, int32_t num_tokens,
+                                     float scale, int32_t window, int32_t sinks, void *out,
+                                     int64_t out_s0, int64_t out_s1, float *lse, void *stream);
+
+/* Accept a prefix of each row's drafts and draw the token after it
+ * (speculative sampling: the result is distributed as the target model's).
+ * The plan gives vocab, num_steps = N and max_rows.  With T = temperature[b],
+ * p_i = softmax(target_logits[b, i] / T) for i = 0 .. N and q_i =
+ * softmax(logit_cache[b, i] / T) for i < N: draft x_i is accepted when
+ *   uniforms[b, i] * q_i(x_i) < p_i(x_i)
+ * and every draft before it was.  At the first refusal j the row's own token
+ * is the argmax over v of ln max(p_j(v) - q_j(v), 0) + noise[b, v] (of ln
+ * p_j(v) + noise where no v has p_j > q_j); with all accepted it is the
+ * argmax of ln p_N(v) + noise[b, v]; the lowest id among equals.  T <= 0 or
+ * NaN, and a position whose largest logit is NaN or infinite: the
+ * distribution is one-hot at that logit's id (the lowest NaN id, else the
+ * lowest id of the maximum, as the draft was drawn), and noise is not read
+ * where p is one-hot.
+ *   target_logits [rows, N + 1, V] of target_dtype, strides in elements;
+ *   logit_cache   [rows, N, V] of cache_dtype, as markov_chain_sample wrote
+ *                 it; both 16-byte aligned with 16-byte multiples as strides;
+ *   draft_tokens  int64 [rows, N], row stride draft_s0; an id outside
+ *                 [0, V) is refused;
+ *   uniforms      fp32 [rows, N] in [0, 1), row stride uni_s0;
+ *   noise         fp32 [rows, V] Gumbel noise (markov_gumbel_noise with one
+ *                 position), row stride noise_s0 a multiple of 4, 16-byte
+ *                 aligned;
+ *   tokens        int64 [rows, N + 1], row stride tok_s0: the accepted
+ *                 drafts, the row's own token, then -1;
+ *   num_accepted  int32 [rows]: accepted drafts, 0 .. N;
+ *   target_probs, draft_probs: fp32 [rows, N] p_i(x_i) and q_i(x_i), row
+ *                 stride N, or both NULL.
+ * Padding rows (row_state_idx[b] < 0) are not written.  Two launches.  EINVAL
+ * for a bad shape, stride, alignment or dtype. */
+markov_status markov_verify(markov_plan *plan, const void *target_logits,
+                            markov_dtype target_dtype, int64_t target_s0, int64_t target_s1,
+                            const int64_t *draft_tokens, int64_t draft_s0,
+                            const void *logit_cache, markov_dtype cache_dtype, int64_t cache_s0,
+                            int64_t cache_s1, const float *temperature, const float *uniforms,
+                            int64_t uni_s0, const float *noise, int64_t noise_s0,
+                            const int64_t *row_state_idx, int32_t rows, int64_t *tokens,
+                            int64_t tok_s0, int32_t *num_accepted, float *target_probs,
+                            float *draft_probs, void *stream);
 
 #ifdef __cplusplus
 }
