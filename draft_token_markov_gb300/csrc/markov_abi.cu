@@ -84,24 +84,11 @@ void free_plan(markov_plan *p) {
     delete p;
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
 // The head [V, r] BF16 as 2-D tiles of 128 rows x 64 elements, 128-byte
 // swizzle (the K-major MMA operand layout); rows past V read as zero.
 bool encode_head_map(CUtensorMap *m, const void *head, int V, int r) {
-    static EncodeTiledFn fn = nullptr;
-    if (!fn) {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess || !f)
-            return false;
-        fn = (EncodeTiledFn)f;
-    }
+    const EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)r, (cuuint64_t)V};
     cuuint64_t strides[1] = {(cuuint64_t)r * 2};
     cuuint32_t box[2] = {64, 128};

@@ -50,21 +50,22 @@ struct WriteArgs {
 struct AttnArgs {
     const uint16_t *q;
     int64_t q_s0, q_s1;
-    const uint16_t *k, *v;
-    int64_t k_page, k_slot, k_head, v_page, v_slot, v_head;
-    int64_t num_pages;         // of both caches
+    uint32_t q_sign;           // flips the queries' signs when the scale is negative
     const int32_t *table;
     int64_t table_s0;
-    int num_states, width, page_shift;
+    int num_states, room, page_shift;      // room: keys that a table row has pages for
     const int64_t *idx;
     const int32_t *query_start, *seq_lens;
     int rows, T, q_heads, kv_heads, group;
-    float scale;
+    float scale2;              // |scale| log2(e), not zero
     int window, sinks;
     uint16_t *out;
     int64_t out_s0, out_s1;
     float *lse;
+    float *parts;              // split items' parts: [blocks][2][2 tiles][128 (D + 2)]
+    uint32_t *arrivals;        // [blocks][2 tiles]: parts that are there; zero between calls
     uint32_t *status;
+    uint64_t timeout_ns;
 };
 
 struct VerifyArgs {
@@ -96,7 +97,10 @@ constexpr int kVerifyMaxSegs = 64;
 
 cudaError_t launch_paged_layout(const LayoutArgs &a, cudaStream_t s);
 cudaError_t launch_paged_write(const WriteArgs &a, cudaStream_t s);
-cudaError_t launch_paged_attention(const AttnArgs &a, int head_dim, bool f16, cudaStream_t s);
+cudaError_t paged_attention_prepare();
+size_t paged_attention_parts(int head_dim, int blocks);
+cudaError_t launch_paged_attention(const AttnArgs &a, const CUtensorMap &k, const CUtensorMap &v,
+                                   int head_dim, bool f16, int blocks, cudaStream_t s);
 cudaError_t launch_verify(VerifyArgs a, bool target_f32, bool cache_f32, int sms, cudaStream_t s);
 
 }  // namespace dtm

@@ -15,16 +15,21 @@ struct markov_paged_plan {
     markov_paged_desc d;
     int sm_count = 0;
     int page_shift = 0;
-    uint32_t *ctrl = nullptr;     // [0..1] status, where; [2] the layout's arrivals
+    int blocks = 0;               // of an attention launch: one a multiprocessor
+    uint32_t *ctrl = nullptr;     // [0..1] status, where; [2] the layout's arrivals;
+                                  // from kArrivals on the attention's, 2 a block
+    size_t ctrl_n = 0;
+    float *parts = nullptr;       // split attention rows
 };
 
 namespace {
 
-constexpr size_t kCtrlWords = 8;
+constexpr size_t kArrivals = 8;
 
 void free_plan(markov_paged_plan *p) {
     if (!p) return;
     if (p->ctrl) cudaFree(p->ctrl);
+    if (p->parts) cudaFree(p->parts);
     delete p;
 }
 
@@ -34,6 +39,26 @@ bool valid_view(const markov_cache_view *v, const markov_paged_desc &d) {
     if (v->num_pages < 1 || v->num_pages > INT32_MAX) return false;
     if (v->s_page < 0 || v->s_slot < d.head_dim || v->s_head < d.head_dim) return false;
     return v->s_page % 8 == 0 && v->s_slot % 8 == 0 && v->s_head % 8 == 0;
+}
+
+constexpr int64_t kMaxRoom = 1 << 30;     // keys of a table row
+
+// A cache as [pages, heads, slots, head_dim] tiles of 64 elements by a page's
+// slots (at most 128), 128-byte swizzle; pages out of range read as zero.
+bool encode_cache_map(CUtensorMap *m, const markov_cache_view &v, const markov_paged_plan &p) {
+    const EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn) return false;
+    const int page = p.d.page_size;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.d.head_dim, (cuuint64_t)page, (cuuint64_t)p.d.kv_heads,
+                                (cuuint64_t)v.num_pages};
+    // a lone page's stride is never used, but has to be one
+    const int64_t s_page = v.num_pages > 1 ? v.s_page : v.s_slot * page;
+    const cuuint64_t strides[3] = {(cuuint64_t)v.s_slot * 2, (cuuint64_t)v.s_head * 2, (cuuint64_t)s_page * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(page < 128 ? page : 128), 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, p.d.dtype == MARKOV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+              v.data, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Token rows [T, heads, head_dim].
@@ -75,8 +100,12 @@ markov_status markov_paged_plan_create(const markov_paged_desc *desc, markov_pag
     if (p->d.timeout_ms == 0) p->d.timeout_ms = 1000;
     p->sm_count = prop.multiProcessorCount;
     while ((1 << p->page_shift) < d.page_size) ++p->page_shift;
-    if (cudaMalloc(&p->ctrl, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
-        cudaMemset(p->ctrl, 0, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
+    p->blocks = p->sm_count;
+    p->ctrl_n = kArrivals + 2 * p->blocks;
+    if (paged_attention_prepare() != cudaSuccess ||
+        cudaMalloc(&p->ctrl, p->ctrl_n * sizeof(uint32_t)) != cudaSuccess ||
+        cudaMalloc(&p->parts, paged_attention_parts(d.head_dim, p->blocks) * sizeof(float)) != cudaSuccess ||
+        cudaMemset(p->ctrl, 0, p->ctrl_n * sizeof(uint32_t)) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         cudaGetLastError();
         free_plan(p);
@@ -105,7 +134,7 @@ markov_status markov_paged_plan_status(markov_paged_plan *p) {
     }
     if (ctrl[0] == 0u) return MARKOV_OK;
     // a kernel gave up: clear the status and every counter it may have left
-    if (cudaMemset(p->ctrl, 0, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
+    if (cudaMemset(p->ctrl, 0, p->ctrl_n * sizeof(uint32_t)) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         cudaGetLastError();
         return MARKOV_ECUDA;
@@ -226,28 +255,26 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     if (!valid_view(k_cache, p->d) || !valid_view(v_cache, p->d) ||
         k_cache->num_pages != v_cache->num_pages)
         return MARKOV_EINVAL;
+    const int64_t room = (int64_t)table_width << p->page_shift;
+    if (room > kMaxRoom || (int64_t)num_tokens * (p->d.q_heads / p->d.kv_heads) > INT32_MAX / 2)
+        return MARKOV_EINVAL;
     if (num_tokens == 0) return MARKOV_OK;
     if (!valid_rows(q, q_s0, q_s1, p->d) || !valid_rows(out, out_s0, out_s1, p->d) || q == out)
         return MARKOV_EINVAL;
     DeviceGuard guard(p->d.device);
     if (!guard.ok) return MARKOV_EDEVICE;
+    CUtensorMap kmap, vmap;
+    if (!encode_cache_map(&kmap, *k_cache, *p) || !encode_cache_map(&vmap, *v_cache, *p))
+        return MARKOV_EINVAL;
     AttnArgs a{};
     a.q = static_cast<const uint16_t *>(q);
     a.q_s0 = q_s0;
     a.q_s1 = q_s1;
-    a.k = static_cast<const uint16_t *>(k_cache->data);
-    a.v = static_cast<const uint16_t *>(v_cache->data);
-    a.k_page = k_cache->s_page;
-    a.k_slot = k_cache->s_slot;
-    a.k_head = k_cache->s_head;
-    a.v_page = v_cache->s_page;
-    a.v_slot = v_cache->s_slot;
-    a.v_head = v_cache->s_head;
-    a.num_pages = k_cache->num_pages;
+    a.q_sign = scale < 0.0f ? 0x80008000u : 0u;
     a.table = page_table;
     a.table_s0 = table_s0;
     a.num_states = num_states;
-    a.width = table_width;
+    a.room = (int)room;
     a.page_shift = p->page_shift;
     a.idx = row_state_idx;
     a.query_start = query_start;
@@ -257,16 +284,20 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     a.q_heads = p->d.q_heads;
     a.kv_heads = p->d.kv_heads;
     a.group = p->d.q_heads / p->d.kv_heads;
-    a.scale = scale;
-    a.window = window;
-    a.sinks = sinks;
+    a.scale2 = std::fmax(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
+    // a row has fewer keys than kMaxRoom
+    a.window = window >= kMaxRoom ? 0 : window;
+    a.sinks = sinks < kMaxRoom ? sinks : (int)kMaxRoom;
     a.out = static_cast<uint16_t *>(out);
     a.out_s0 = out_s0;
     a.out_s1 = out_s1;
     a.lse = lse;
+    a.parts = p->parts;
+    a.arrivals = p->ctrl + kArrivals;
     a.status = p->ctrl;
-    if (launch_paged_attention(a, p->d.head_dim, p->d.dtype == MARKOV_F16, (cudaStream_t)stream) !=
-        cudaSuccess) {
+    a.timeout_ns = (uint64_t)p->d.timeout_ms * 1000000ull;
+    if (launch_paged_attention(a, kmap, vmap, p->d.head_dim, p->d.dtype == MARKOV_F16, p->blocks,
+                               (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();
         return MARKOV_ECUDA;
     }

@@ -519,15 +519,15 @@ markov_status markov_paged_write(markov_paged_plan *plan, const void *key, int64
  *   q, out        [num_tokens, q_heads, head_dim], strides s0 (token) and s1
  *                 (head) multiples of 8, 16-byte aligned; out != q.
  *   lse           fp32 [num_tokens, q_heads] contiguous, or NULL.
- *   seq_lens      int32 [rows]; at most table_width * page_size (longer ones
- *                 see the table's keys only).
+ *   seq_lens      int32 [rows]; keys past the table's are not there to see.
  * Padding rows, and tokens outside every row, are not written.  Keys and
  * values that no token of the row sees (slots past its length, before its
  * window, foreign pages) may hold anything, NaN included, and table entries
  * for them are not read; page ids outside [0, num_pages) read as zeros.
  * Keys that one token of the row sees and another does not may be anything
  * too, values there must be finite.  One launch.  EINVAL for a bad shape,
- * stride or alignment. */
+ * stride or alignment, a table row of more than 2^30 keys, or 2^30 and more
+ * tokens times q_heads / kv_heads. */
 markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int64_t q_s0,
                                      int64_t q_s1, const markov_cache_view *k_cache,
                                      const markov_cache_view *v_cache, const int32_t *page_table,
