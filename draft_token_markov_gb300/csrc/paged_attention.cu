@@ -57,26 +57,26 @@ struct PaShape {
 
 struct PaItem {
     int r, h, m;               // request, key head, pair of row tiles
-    int n, qs, state;          // its new tokens, their first, its table row
-    int pos0;                  // position of its token 0
     int rows, row0;            // rows of the item, the first within the request
     int end, first, kept;      // some row sees keys [first, end) and [0, kept)
     int sink_tiles, w0, tiles; // key tiles: [0, sink_tiles), then from w0 on
 };
 
 struct PaReq {
-    int n, np, qs, pos0, state;   // np: tokens that there are queries for
+    int np, qs;                // tokens that there are queries for, the first
+    int pos0;                  // position of its token 0
+    int state;                 // its table row, -1 for none
 };
 
 __device__ __forceinline__ PaReq pa_request(const AttnArgs &a, int r) {
     PaReq q;
     const int64_t s = __ldg(a.idx + r);
     q.qs = __ldg(a.query_start + r);
-    q.n = __ldg(a.query_start + r + 1) - q.qs;
+    const int n = __ldg(a.query_start + r + 1) - q.qs;
     int len = __ldg(a.seq_lens + r);
     if (len < 0) len = 0;
-    q.np = s < 0 || q.qs < 0 || q.qs >= a.T || q.n < 0 ? 0 : min(q.n, a.T - q.qs);
-    q.pos0 = len - q.n;
+    q.np = s < 0 || q.qs < 0 || q.qs >= a.T || n < 0 ? 0 : min(n, a.T - q.qs);
+    q.pos0 = len - n;
     q.state = s < a.num_states ? (int)s : -1;
     return q;
 }
@@ -129,10 +129,6 @@ struct PaWalk {
     }
     __device__ __forceinline__ void set(const AttnArgs &a, int j) {
         units = pa_tiles(a, q, it.m, it);
-        it.n = q.n;
-        it.qs = q.qs;
-        it.state = q.state;
-        it.pos0 = q.pos0;
         j0 = j;
         j1 = (int)min((int64_t)units, u_end - u);
     }
@@ -316,6 +312,26 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return bf16x2_rn(lo, hi);
 }
 
+// Two fp32 values in one register pair, and the packed arithmetic on them.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void split2(uint64_t x, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float pa_ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -368,6 +384,8 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     const bool work = !abort_s && (int)blockIdx.x < start_s.blocks;
     const PaWait wait{a.timeout_ns, a.status, &abort_s};
     uint32_t filled = 0, fill_phase = 0;             // loader: stages it filled, and their phases
+    // registers: 8 x 32 x 200 + 4 x 32 x 104 are the launch's 384 x 168
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (work && warp == 9) {
         // ------------------------------------------------ key / value loads
         PaWalk w;
@@ -379,7 +397,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         bool ok = true;
         do {
             const PaItem &it = w.it;
-            const int32_t *table = a.table + (int64_t)max(it.state, 0) * a.table_s0;
+            const int32_t *table = a.table + (int64_t)max(w.q.state, 0) * a.table_s0;
             const int j1 = min(w.j1, it.tiles);
             for (int j = w.j0; ok && j < j1; ++j) {
                 const int key0 = (j < it.sink_tiles ? j : it.w0 + j - it.sink_tiles) * kPaTile;
@@ -501,7 +519,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 for (int e = t; e < rows * V; e += 64) {
                     const int row = e / V, c = e % V, x = it.row0 + s * kPaTile + row;
                     const int tok = x / a.group, head = it.h * a.group + x - tok * a.group;
-                    uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.q + (it.qs + tok) * a.q_s0 +
+                    uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.q + (w.q.qs + tok) * a.q_s0 +
                                                                     head * a.q_s1 + c * 8));
                     v.x ^= a.q_sign;
                     v.y ^= a.q_sign;
@@ -517,6 +535,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         } while (ok && w.next(a));
     } else if (work) {
         // -------------------------------------------- softmax and output
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int slot = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;             // TMEM lane of the warp
         const uint32_t t_s = tmem + slot * kPaTile + lanes, t_o = tmem + 2 * kPaTile + slot * D + lanes;
@@ -550,12 +569,12 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             }
             const int x = it.row0 + slot * kPaTile + row, tok = x / a.group;
             const int head = it.h * a.group + x - tok * a.group;
-            const int pos = it.pos0 + tok;
+            const int pos = w.q.pos0 + tok;
             // the warp's rows: positions of the first and the last that there is
             const int wrow = slot * kPaTile + (warp & 3) * 32;
             const bool busy = wrow < it.rows;
-            const int lo_pos = it.pos0 + (it.row0 + wrow) / a.group;
-            const int hi_pos = it.pos0 + (it.row0 + min(wrow + 31, it.rows - 1)) / a.group;
+            const int lo_pos = w.q.pos0 + (it.row0 + wrow) / a.group;
+            const int hi_pos = w.q.pos0 + (it.row0 + min(wrow + 31, it.rows - 1)) / a.group;
             const int limit = min(pos + 1, a.room);
             float m = -INFINITY, l = 0.0f;
             for (int j = w.j0; j < j1; ++j) {
@@ -570,25 +589,21 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                                        (a.window <= 0 || key0 > hi_pos - a.window || key0 + kPaTile <= a.sinks);
                     const int hi = limit - key0, sk = min(a.sinks - key0, hi);
                     const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
-                    auto hide = [&](float *s, int i0) {
+                    auto hide = [&](float (&s)[kPaTile]) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            s[i] = (i0 + i < hi && i0 + i >= lo) || i0 + i < sk ? s[i] : -INFINITY;
+                        for (int i = 0; i < kPaTile; ++i)
+                            s[i] = (i < hi && i >= lo) || i < sk ? s[i] : -INFINITY;
                     };
-                    // the scores are read from TMEM twice, 32 columns at a
-                    // time: once for the maximum, once for the weights
-                    float s[2][32], top = -INFINITY;
-                    ld_32x32b_x32(t_s, s[0]);
+                    float s[kPaTile], top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        tc::wait_ld();
-                        if (k < 3) ld_32x32b_x32(t_s + 32 * (k + 1), s[(k + 1) & 1]);
-                        float *x = s[k & 1];
-                        if (!whole) hide(x, 32 * k);
+                    for (int k = 0; k < 4; ++k) ld_32x32b_x32(t_s + 32 * k, s + 32 * k);
+                    tc::wait_ld();
+                    if (!whole) hide(s);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) top = fmaxf(top, x[i]);
-                    }
-                    ld_32x32b_x32(t_s, s[0]);
+                    for (int i = 0; i < kPaTile; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top4[k] = fmaxf(fmaxf(top4[k], s[i + 2 * k]), s[i + 2 * k + 1]);
+                    const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
                     // (top - m) c > kLazy; m = -inf until the row has seen a key
                     const bool grow = top > m && (m == -INFINITY || (top - m) * c > kLazy);
                     if (__any_sync(0xffffffffu, grow)) {
@@ -610,26 +625,24 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                         }
                     }
                     const float mc = m == -INFINITY ? 0.0f : kShift - m * c;
-                    float sum0 = 0.0f, sum1 = 0.0f;
+                    const uint64_t c2 = f32x2(c, c), mc2 = f32x2(mc, mc);
+                    uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        tc::wait_ld();
-                        if (k < 3) ld_32x32b_x32(t_s + 32 * (k + 1), s[(k + 1) & 1]);
-                        float *x = s[k & 1];
-                        if (!whole) hide(x, 32 * k);
                         uint32_t p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float p0 = pa_ex2(fmaf(x[2 * i], c, mc));
-                            const float p1 = pa_ex2(fmaf(x[2 * i + 1], c, mc));
-                            sum0 += p0;
-                            sum1 += p1;
+                            float x0, x1;
+                            split2(fma2(f32x2(s[32 * k + 2 * i], s[32 * k + 2 * i + 1]), c2, mc2), x0, x1);
+                            const float p0 = pa_ex2(x0), p1 = pa_ex2(x1);
+                            sum[i & 3] = add2(sum[i & 3], f32x2(p0, p1));
                             p[i] = pack2<F16>(p0, p1);
                         }
-                        // P's columns lie over scores that are read already
                         tc::st_32x32b_x16(t_s + 16 * k, p);
                     }
-                    l += sum0 + sum1;
+                    float s0, s1;
+                    split2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                    l += s0 + s1;
                 }
                 // value rows that nobody sees: zeros
                 const int key = key0 + row;
@@ -662,7 +675,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 tc::fence_after_sync();
             }
             const bool live = row < rows;
-            const int64_t token = it.qs + tok;
+            const int64_t token = w.q.qs + tok;
             if (w.j0 == 0 && w.j1 == w.units) {
                 // the whole item: the output
                 const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
@@ -758,9 +771,9 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             u[i] = L == 0.0f ? 0u : pack2<F16>(o[2 * i] * inv, o[2 * i + 1] * inv);
-                        *reinterpret_cast<uint4 *>(a.out + (it.qs + tt) * a.out_s0 + hh * a.out_s1 + cc * 8) = v;
+                        *reinterpret_cast<uint4 *>(a.out + (w.q.qs + tt) * a.out_s0 + hh * a.out_s1 + cc * 8) = v;
                         if (cc == 0 && a.lse)
-                            a.lse[(int64_t)(it.qs + tt) * a.q_heads + hh] =
+                            a.lse[(int64_t)(w.q.qs + tt) * a.q_heads + hh] =
                                 L == 0.0f ? -INFINITY : (M * c - kShift + __log2f(L)) * 0.69314718055994531f;
                     }
                 }
