@@ -50,7 +50,7 @@ struct WriteArgs {
 struct AttnArgs {
     const uint16_t *q;
     int64_t q_s0, q_s1;
-    uint32_t q_sign;           // flips the queries' signs when the scale is negative
+    int negate;                // the scale is negative
     const int32_t *table;
     int64_t table_s0;
     int num_states, room, page_shift;      // room: keys that a table row has pages for

@@ -270,7 +270,7 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     a.q = static_cast<const uint16_t *>(q);
     a.q_s0 = q_s0;
     a.q_s1 = q_s1;
-    a.q_sign = scale < 0.0f ? 0x80008000u : 0u;
+    a.negate = scale < 0.0f;
     a.table = page_table;
     a.table_s0 = table_s0;
     a.num_states = num_states;

@@ -8,13 +8,18 @@
 // for all of them.  An item is (request, key head, up to two such tiles); its
 // keys go by in tiles of 128:
 //   S = Q K^T           128 x 128, fp32 in TMEM (both operands in shared memory)
-//   m, p = 2^(S c - m c), l += sum p     a thread a row, in registers
+//   m, p = 2^(S c - m c), l += sum p
 //   O += P V            P rounded to the type into S's columns of TMEM, the
 //                       A operand; V as it lies in the cache (MN-major B)
-// with c = scale log2 e.  Two tiles take turns on the tensor core, one in its
-// MMAs while the other is in its softmax.  The maximum that p is taken
-// against moves only when a row's has grown by more than 2^8 (kLazy): then O
-// is rescaled in TMEM, else the sums go on, exact all the same.
+// with c = scale log2 e.  The maximum that p is taken against moves only when
+// a row's has grown by more than 2^8 (kLazy): then O is rescaled in TMEM,
+// else the sums go on, exact all the same.
+//
+// Two slots, each with its S, its O and a warpgroup, take turns on the tensor
+// core: while one is in its MMAs the other is in its softmax.  An item of two
+// row tiles has one in each; an item of one has its even key tiles in slot 0
+// and its odd ones in slot 1, and the two are joined at its end (O of both
+// slots lies in the same TMEM lanes).
 //
 // Work.  A unit is one key tile of an item.  The units of the call, in order
 // of request, key head, tile of rows and keys, are cut into one contiguous
@@ -24,11 +29,14 @@
 // fp32, in the plan's scratch, and the block that finishes last joins them in
 // the order of the keys.
 //
-// Roles.  Warps 0-3 and 4-7: softmax and output of the two tiles; warp 8
-// issues MMAs; warp 9 loads key and value tiles by TMA, a page a box (a box
-// of a page that nobody sees is read out of range, as zeros); warps 10-11
-// load queries.  Value rows that no row of the item sees can hold anything:
-// they are zeroed in shared memory before the MMA (0 * NaN).
+// Roles.  Warps 0-3 and 4-7: softmax and output of the two slots, a thread a
+// row; warp 8 issues MMAs; warp 9 loads key and value tiles by TMA, a page a
+// box (a box of a page that nobody sees is read out of range, as zeros); warp
+// 10 loads queries; warp 11 walks the block's items and leaves each for the
+// others in a ring in shared memory.  (Nothing of an item stays in a register
+// for long: shared memory takes nearly all of the L1 cache, so that a spilled
+// register costs a trip to L2.)  Value rows that no row of the item sees can
+// hold anything: they are zeroed in shared memory before the MMA (0 * NaN).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -39,6 +47,7 @@
 namespace dtm {
 
 constexpr int kPaThreads = 384;
+constexpr int kRing = 4;                     // items that are known ahead
 constexpr int kPaTile = 128;                 // keys of a tile, and rows
 constexpr float kLazy = 8.0f;
 
@@ -49,17 +58,23 @@ struct PaShape {
     static constexpr int kStages = D == 128 ? 5 : 12;
     static constexpr int kHalf = kPaTile * 128;              // 64 elements of every row
     static constexpr int kHalves = D / 64;
-    static constexpr int kData = 2 * kQBytes + kStages * kKvBytes;
-    static constexpr int kSmem = 1024 + kData + 512;
+    // tiles, slot 1's m and l, barriers, the schedule
+    static constexpr int kExchange = 2 * kQBytes + kStages * kKvBytes;
+    static constexpr int kBars = kExchange + 2 * kPaTile * 4;
+    static constexpr int kMisc = kBars + 8 * (2 * kStages + 16 + 2 * kRing);
+    static constexpr int kSmem = kMisc + 512;
 };
 
 // ------------------------------------------------------------------- items
 
 struct PaItem {
-    int r, h, m;               // request, key head, pair of row tiles
-    int rows, row0;            // rows of the item, the first within the request
+    int rows, row0;            // rows of the item (0: no more items), the first within the request
+    int qs, pos0, state;       // the request's first token, its position; its table row, -1 for none
+    int h;                     // key head
     int end, first, kept;      // some row sees keys [first, end) and [0, kept)
-    int sink_tiles, w0, tiles; // key tiles: [0, sink_tiles), then from w0 on
+    int sink_tiles, w0;        // key tiles: [0, sink_tiles), then from w0 on
+    int j0, steps;             // the block's share: key tiles from the j0-th on
+    int c0, c1;                // blocks that share the item
 };
 
 struct PaReq {
@@ -82,7 +97,7 @@ __device__ __forceinline__ PaReq pa_request(const AttnArgs &a, int r) {
 }
 
 // The key tiles of pair m of a request; at least one unit.
-__device__ __forceinline__ int pa_tiles(const AttnArgs &a, const PaReq &q, int m, PaItem &it) {
+__device__ __forceinline__ int pa_units(const AttnArgs &a, const PaReq &q, int m, PaItem &it) {
     it.row0 = m * 2 * kPaTile;
     it.rows = min(q.np * a.group - it.row0, 2 * kPaTile);
     const int p0 = q.pos0 + it.row0 / a.group, p1 = q.pos0 + (it.row0 + it.rows - 1) / a.group;
@@ -93,62 +108,21 @@ __device__ __forceinline__ int pa_tiles(const AttnArgs &a, const PaReq &q, int m
     const int nw = it.first < it.end ? (it.end + kPaTile - 1) / kPaTile - it.w0 : 0;
     it.sink_tiles = (it.kept + kPaTile - 1) / kPaTile;
     if (nw > 0 && it.sink_tiles > it.w0) it.sink_tiles = it.w0;
-    it.tiles = it.sink_tiles + nw;
-    return it.tiles > 0 ? it.tiles : 1;
+    it.steps = it.sink_tiles + nw;
+    return max(it.steps, 1);
 }
 
 __device__ __forceinline__ int pa_pairs(const AttnArgs &a, const PaReq &q) {
     return (q.np * a.group + 2 * kPaTile - 1) / (2 * kPaTile);
 }
 
-// Where a block's range starts, in shared memory.
-struct PaStart {
-    int r, h, m, j;            // first unit: request, key head, pair, key tile
+// Where a block's range starts, and what its warps share, in shared memory.
+struct PaShared {
+    int r, h, m, j;            // first unit: request, key head, pair of row tiles, key tile
     int blocks;                // blocks that have work
+    uint32_t abort, tmem, last[2];
     int64_t u0, u1, total;     // its units, all units
-};
-
-// A block's items one after the other; every role walks them by itself.
-struct PaWalk {
-    PaItem it;
-    PaReq q;
-    int64_t u;                 // the current item's first unit
-    int j0, j1;                // the range of it that is this block's
-    int units, pairs;
-    int64_t u_end;
-
-    __device__ __forceinline__ void start(const AttnArgs &a, const PaStart &s) {
-        it.r = s.r;
-        it.h = s.h;
-        it.m = s.m;
-        q = pa_request(a, s.r);
-        pairs = pa_pairs(a, q);
-        u_end = s.u1;
-        u = s.u0 - s.j;
-        set(a, s.j);
-    }
-    __device__ __forceinline__ void set(const AttnArgs &a, int j) {
-        units = pa_tiles(a, q, it.m, it);
-        j0 = j;
-        j1 = (int)min((int64_t)units, u_end - u);
-    }
-    __device__ __forceinline__ bool next(const AttnArgs &a) {
-        u += units;
-        if (u >= u_end) return false;
-        if (++it.m == pairs) {
-            it.m = 0;
-            if (++it.h == a.kv_heads) {
-                it.h = 0;
-                do {
-                    ++it.r;
-                    q = pa_request(a, it.r);
-                } while (q.np <= 0);
-                pairs = pa_pairs(a, q);
-            }
-        }
-        set(a, 0);
-        return true;
-    }
+    PaItem ring[kRing];
 };
 
 __device__ __forceinline__ int64_t pa_first_unit(int64_t total, int blocks, int c) {
@@ -161,8 +135,8 @@ __device__ __forceinline__ int pa_block_of(int64_t total, int blocks, int64_t u)
     return c;
 }
 
-// Every thread: this block's range.  scratch: 16 int64.
-__device__ void pa_schedule(const AttnArgs &a, PaStart *out, int64_t *scratch) {
+// Every thread: this block's range.  scratch: an int64 a warp.
+__device__ __forceinline__ void pa_schedule(const AttnArgs &a, PaShared *out, int64_t *scratch) {
     constexpr int kPer = (kPagedMaxRows + kPaThreads - 1) / kPaThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int64_t mine[kPer], sum = 0;
@@ -175,7 +149,7 @@ __device__ void pa_schedule(const AttnArgs &a, PaStart *out, int64_t *scratch) {
             const PaReq q = pa_request(a, r);
             const int pairs = pa_pairs(a, q);
             int64_t units = 0;
-            for (int m = 0; m < pairs; ++m) units += pa_tiles(a, q, m, it);
+            for (int m = 0; m < pairs; ++m) units += pa_units(a, q, m, it);
             mine[k] = units * a.kv_heads;
         }
         sum += mine[k];
@@ -214,7 +188,7 @@ __device__ void pa_schedule(const AttnArgs &a, PaStart *out, int64_t *scratch) {
             rem -= h * head;
             int m = 0;
             for (;; ++m) {
-                const int units = pa_tiles(a, q, m, it);
+                const int units = pa_units(a, q, m, it);
                 if (rem < units) break;
                 rem -= units;
             }
@@ -345,71 +319,141 @@ __global__ void __launch_bounds__(kPaThreads, 1)
 paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap) {
     using S = PaShape<D>;
-    extern __shared__ uint8_t raw[];
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t base[];
     uint8_t *q_smem = base, *kv_smem = base + 2 * S::kQBytes;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(base + S::kData);
-    __shared__ PaStart start_s;
-    __shared__ int64_t scratch_s[16];
-    __shared__ uint32_t tmem_s, abort_s, last_s[2];
+    float *exchange = reinterpret_cast<float *>(base + S::kExchange);
+    PaShared &sh = *reinterpret_cast<PaShared *>(base + S::kMisc);
+    static_assert(sizeof(PaShared) <= 512, "kSmem");
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t bar0 = tc::smem_u32(bars);
-    const uint32_t kv_full = bar0, kv_empty = bar0 + 8 * S::kStages;
-    const uint32_t q_full = bar0 + 16 * S::kStages, q_empty = q_full + 16, s_full = q_full + 32,
-                   p_full = q_full + 48, pv_done = q_full + 64, group = q_full + 80, leave = q_full + 96;
+    const uint32_t kv_full = tc::smem_u32(base + S::kBars), kv_empty = kv_full + 8 * S::kStages;
+    const uint32_t q_full = kv_empty + 8 * S::kStages, q_empty = q_full + 16, s_full = q_full + 32,
+                   p_full = q_full + 48, pv_done = q_full + 64, group = q_full + 80,
+                   merge_full = q_full + 96, merge_free = q_full + 104, leave = q_full + 112,
+                   item_full = q_full + 128, item_empty = item_full + 8 * kRing;
     if (tid == 0) {
-        abort_s = ld_acquire_u32(a.status);          // a pending status: nothing is done
+        sh.abort = ld_acquire_u32(a.status);         // a pending status: nothing is done
         for (int i = 0; i < S::kStages; ++i) {
             tc::mbar_init(kv_full + 8 * i, 1);
             tc::mbar_init(kv_empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(q_full + 8 * i, 2);       // the two loading warps
+            tc::mbar_init(q_full + 8 * i, 1);
             tc::mbar_init(q_empty + 8 * i, 1);
             tc::mbar_init(s_full + 8 * i, 1);
-            tc::mbar_init(p_full + 8 * i, 4);       // the tile's four warps
+            tc::mbar_init(p_full + 8 * i, 4);        // the slot's warps
             tc::mbar_init(pv_done + 8 * i, 1);
-            tc::mbar_init(group + 8 * i, 128);
+            tc::mbar_init(group + 8 * i, 4);
         }
+        tc::mbar_init(merge_full, 4);                // slot 1's warps
+        tc::mbar_init(merge_free, 4);                // slot 0's
         tc::mbar_init(leave, 1);
+        for (int i = 0; i < kRing; ++i) {
+            tc::mbar_init(item_full + 8 * i, 1);
+            tc::mbar_init(item_empty + 8 * i, 11);   // the warps that read it
+        }
         tc::mbar_init_fence();
     }
-    if (warp == 8) tc::tmem_alloc(tc::smem_u32(&tmem_s), 512);
-    pa_schedule(a, &start_s, scratch_s);
+    if (warp == 8) tc::tmem_alloc(tc::smem_u32(&sh.tmem), 512);
+    pa_schedule(a, &sh, reinterpret_cast<int64_t *>(exchange));
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tmem = tmem_s;
-    const bool work = !abort_s && (int)blockIdx.x < start_s.blocks;
-    const PaWait wait{a.timeout_ns, a.status, &abort_s};
-    uint32_t filled = 0, fill_phase = 0;             // loader: stages it filled, and their phases
-    // registers: 8 x 32 x 200 + 4 x 32 x 104 are the launch's 384 x 168
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (work && warp == 9) {
+    const uint32_t tmem = sh.tmem;
+    const bool work = !sh.abort && (int)blockIdx.x < sh.blocks;
+    const PaWait wait{a.timeout_ns, a.status, &sh.abort};
+    // a wait that some lane gives up is given up by the warp
+    auto all_wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
+        return (bool)__all_sync(0xffffffffu, wait(bar, parity, where));
+    };
+    auto arrive = [&](uint32_t bar) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
+    };
+    // key and value tiles in the order they are loaded: K V K V ...
+    auto stage_of = [](uint32_t at) { return at % S::kStages; };
+    auto phase_of = [](uint32_t at) { return (at / S::kStages) & 1; };
+    // the n-th item; its fields are read from shared memory where they are used
+    auto item = [&](uint32_t n) -> const volatile PaItem & { return sh.ring[n % kRing]; };
+    auto item_wait = [&](uint32_t n) { return all_wait(item_full + 8 * (n % kRing), (n / kRing) & 1, 0x500); };
+    auto item_done = [&](uint32_t n) { arrive(item_empty + 8 * (n % kRing)); };
+
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (work && warp == 11) {
+        // ------------------------------------------------------- the walk
+        PaItem it;
+        PaReq q = pa_request(a, sh.r);
+        int r = sh.r, h = sh.h, m = sh.m, j = sh.j, pairs = pa_pairs(a, q);
+        int64_t u = sh.u0 - j;                       // the current item's first unit
+        bool ok = true;
+        for (uint32_t n = 0; ok; ++n) {
+            ok = all_wait(item_empty + 8 * (n % kRing), (n / kRing & 1) ^ 1, 0x510);
+            if (!ok) break;
+            const bool more = u < sh.u1;
+            if (more) {
+                const int units = pa_units(a, q, m, it);
+                it.qs = q.qs;
+                it.pos0 = q.pos0;
+                it.state = q.state;
+                it.h = h;
+                it.j0 = j;
+                const int j1 = (int)min((int64_t)units, sh.u1 - u);
+                it.c0 = it.c1 = blockIdx.x;
+                if (j > 0 || j1 < units) {
+                    it.c0 = pa_block_of(sh.total, sh.blocks, u);
+                    it.c1 = pa_block_of(sh.total, sh.blocks, u + units - 1);
+                }
+                it.steps = min(j1, it.steps) - j;    // 0 where nothing is seen
+                u += units;
+                j = 0;
+                if (++m == pairs) {
+                    m = 0;
+                    if (++h == a.kv_heads) {
+                        h = 0;
+                        if (u < sh.u1) {
+                            do {
+                                q = pa_request(a, ++r);
+                            } while (q.np <= 0);
+                            pairs = pa_pairs(a, q);
+                        }
+                    }
+                }
+            } else {
+                it.rows = 0;
+            }
+            if (lane == 0) sh.ring[n % kRing] = it;
+            arrive(item_full + 8 * (n % kRing));
+            if (!more) break;
+        }
+    } else if (work && warp == 9) {
         // ------------------------------------------------ key / value loads
-        PaWalk w;
-        w.start(a, start_s);
+        uint32_t filled = 0, fill_phase = 0;         // stages it filled, and their phases
         const int page = 1 << a.page_shift;
         const int box = min(page, kPaTile), boxes = kPaTile / box;     // boxes of a tile
-        int stage = 0;
-        uint32_t phase = 0;
+        uint32_t at = 0;
         bool ok = true;
-        do {
-            const PaItem &it = w.it;
-            const int32_t *table = a.table + (int64_t)max(w.q.state, 0) * a.table_s0;
-            const int j1 = min(w.j1, it.tiles);
-            for (int j = w.j0; ok && j < j1; ++j) {
-                const int key0 = (j < it.sink_tiles ? j : it.w0 + j - it.sink_tiles) * kPaTile;
-                int pid = -1;
-                const int key = key0 + lane * box;
-                if (lane < boxes && key < it.end && (key + box > it.first || key < it.kept))
-                    pid = __ldg(table + (key >> a.page_shift));
-                for (int kv = 0; ok && kv < 2; ++kv) {
-                    if (lane == 0) ok = wait(kv_empty + 8 * stage, phase ^ 1, 0x100 + stage);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (uint32_t n = 0; ok; ++n) {
+            ok = item_wait(n);
+            const volatile PaItem &it = item(n);
+            if (!ok || it.rows == 0) break;
+            const int32_t *table = a.table + (int64_t)max(it.state, 0) * a.table_s0;
+            const int j0 = it.j0, j1 = j0 + it.steps, sinks = it.sink_tiles, w0 = it.w0;
+            const int end = it.end, first = it.first, kept = it.kept, h = it.h;
+            item_done(n);
+            auto page_of = [&](int j) {
+                const int key = (j < sinks ? j : w0 + j - sinks) * kPaTile + lane * box;
+                return lane < boxes && key < end && (key + box > first || key < kept)
+                           ? __ldg(table + (key >> a.page_shift)) : -1;
+            };
+            int next = j0 < j1 ? page_of(j0) : -1;
+            for (int j = j0; ok && j < j1; ++j) {
+                const int pid = next;
+                if (j + 1 < j1) next = page_of(j + 1);
+                const int key = (j < sinks ? j : w0 + j - sinks) * kPaTile + lane * box;
+                for (int kv = 0; ok && kv < 2; ++kv, ++at) {
+                    const uint32_t stage = stage_of(at), phase = phase_of(at), full = kv_full + 8 * stage;
+                    ok = all_wait(kv_empty + 8 * stage, phase ^ 1, 0x100 + stage);
                     if (!ok) break;
-                    const uint32_t full = kv_full + 8 * stage;
                     if (lane == 0) tc::mbar_expect_tx(full, S::kKvBytes);
                     __syncwarp();
                     if (lane < boxes) {
@@ -417,192 +461,201 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
 #pragma unroll
                         for (int half = 0; half < S::kHalves; ++half)
                             tma_load_4d(dst + half * S::kHalf, kv ? &vmap : &kmap, half * 64,
-                                        key & (page - 1), it.h, pid, full);
+                                        key & (page - 1), h, pid, full);
                     }
                     filled |= 1u << stage;
                     fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
-                    if (++stage == S::kStages) { stage = 0; phase ^= 1; }
                 }
             }
-        } while (ok && w.next(a));
+        }
+        if (lane == 0 && sh.abort) {
+            // gave up: no load may be in flight when the block leaves
+            const uint64_t until = tc::now_ns() + a.timeout_ns;
+            for (int i = 0; i < S::kStages; ++i)
+                if (filled >> i & 1)
+                    while (!tc::mbar_test(kv_full + 8 * i, fill_phase >> i & 1) && tc::now_ns() < until) {}
+        }
     } else if (work && warp == 8) {
         // ---------------------------------------------------- MMA issue
-        if (lane == 0) {
-            PaWalk w;
-            w.start(a, start_s);
-            int stage = 0;
-            uint32_t phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-            bool ok = true;
-            const uint32_t q_addr = tc::smem_u32(q_smem), kv_addr = tc::smem_u32(kv_smem);
-            constexpr uint32_t kIdescS = pa_idesc<F16>(kPaTile, false), kIdescO = pa_idesc<F16>(D, true);
-            auto scores = [&](int slot, int st) {
+        // the whole warp, so that control flow and descriptors stay uniform;
+        // an elected lane issues
+        uint32_t at = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        bool ok = true;
+        const uint32_t q_addr = tc::smem_u32(q_smem), kv_addr = tc::smem_u32(kv_smem);
+        constexpr uint32_t kIdescS = pa_idesc<F16>(kPaTile, false), kIdescO = pa_idesc<F16>(D, true);
+        auto loaded = [&](uint32_t k) { return all_wait(kv_full + 8 * stage_of(k), phase_of(k), 0x200); };
+        auto scores = [&](int slot, int q_tile, uint32_t k) {
+            const uint32_t q0 = q_addr + q_tile * S::kQBytes, k0 = kv_addr + stage_of(k) * S::kKvBytes;
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k / 4) * S::kHalf + (k % 4) * 32;
-                    tc::mma_smemA(tmem + slot * kPaTile, tc::sw128_desc(q_addr + slot * S::kQBytes + off),
-                                  tc::sw128_desc(kv_addr + st * S::kKvBytes + off), kIdescS, k > 0);
-                }
-                tc::commit(s_full + 8 * slot);
-            };
-            auto values = [&](int slot, int st, bool accumulate) {
+            for (int i = 0; i < D / 16; ++i) {
+                const uint32_t off = (i / 4) * S::kHalf + (i % 4) * 32;
+                tc::mma_smemA_elect(tmem + slot * kPaTile, tc::sw128_desc(q0 + off),
+                                    tc::sw128_desc(k0 + off), kIdescS, i > 0);
+            }
+            tc::commit_elect(s_full + 8 * slot);
+        };
+        auto values = [&](int slot, uint32_t v, bool accumulate) {
+            const uint32_t v0 = kv_addr + stage_of(v) * S::kKvBytes;
 #pragma unroll
-                for (int k = 0; k < kPaTile / 16; ++k)
-                    tc::mma_tmemA(tmem + 2 * kPaTile + slot * D, tmem + slot * kPaTile + k * 8,
-                                  sw128_mn_desc(kv_addr + st * S::kKvBytes + k * 2048, S::kHalf), kIdescO,
-                                  accumulate || k > 0);
-                tc::commit(pv_done + 8 * slot);
-            };
-            do {
-                const int slots = w.it.rows > kPaTile ? 2 : 1;
-                const int j1 = min(w.j1, w.it.tiles);
-                if (w.j0 >= j1) continue;            // nothing seen: the output is written without MMAs
-                ok = wait(kv_full + 8 * stage, phase, 0x200);
-                for (int s = 0; ok && s < slots; ++s) {
-                    ok = wait(q_full + 8 * s, q_phase[s], 0x210 + s);
-                    if (!ok) break;
+            for (int i = 0; i < kPaTile / 16; ++i)
+                tc::mma_tmemA_elect(tmem + 2 * kPaTile + slot * D, tmem + slot * kPaTile + i * 8,
+                                    sw128_mn_desc(v0 + i * 2048, S::kHalf), kIdescO, accumulate || i > 0);
+            tc::commit_elect(pv_done + 8 * slot);
+        };
+        auto release = [&](uint32_t k) { tc::commit_elect(kv_empty + 8 * stage_of(k)); };
+        for (uint32_t n = 0; ok; ++n) {
+            ok = item_wait(n);
+            const int rows = item(n).rows, steps = item(n).steps;
+            if (!ok || rows == 0) break;
+            item_done(n);
+            if (steps <= 0) continue;                // nothing seen: the output is written without MMAs
+            const bool two = rows > kPaTile;         // row tiles
+            // the first scores
+            for (int s = 0; ok && s < 2; ++s) {
+                if (!two && s == steps) break;
+                const uint32_t k = at + (two ? 0 : 2 * s);
+                ok = loaded(k);
+                if (ok && (two || s == 0)) {
+                    ok = all_wait(q_full + 8 * s, q_phase[s], 0x210 + s);
                     q_phase[s] ^= 1;
-                    tc::fence_after_sync();
-                    scores(s, stage);
-                    if (w.j0 + 1 == j1) tc::commit(q_empty + 8 * s);
                 }
                 if (!ok) break;
-                tc::commit(kv_empty + 8 * stage);
-                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
-                for (int j = w.j0; ok && j < j1; ++j) {
-                    const int v_stage = stage;
-                    const uint32_t v_phase = phase;
-                    if (++stage == S::kStages) { stage = 0; phase ^= 1; }
-                    const bool more = j + 1 < j1;
-                    for (int s = 0; ok && s < slots; ++s) {
-                        ok = wait(p_full + 8 * s, p_phase[s], 0x220 + s) &&
-                             wait(kv_full + 8 * v_stage, v_phase, 0x230);
+                tc::fence_after_sync();
+                scores(s, two ? s : 0, k);
+                if (!two || s == 1) release(k);
+                if (two ? steps == 1 : s + 1 == min(steps, 2) && steps <= 2) tc::commit_elect(q_empty + (two ? 8 * s : 0));
+            }
+            for (int j = 0; ok && j < steps; ++j) {
+                const uint32_t v = at + 2 * j + 1;
+                const int ahead = two ? 1 : 2;       // key tiles to the slot's next scores
+                for (int s = two ? 0 : j & 1, e = two ? 2 : s + 1; ok && s < e; ++s) {
+                    ok = all_wait(p_full + 8 * s, p_phase[s], 0x220 + s) && loaded(v);
+                    if (!ok) break;
+                    p_phase[s] ^= 1;
+                    tc::fence_after_sync();
+                    values(s, v, j >= ahead);
+                    if (s == e - 1) release(v);
+                    if (j + ahead < steps) {
+                        const uint32_t k = at + 2 * (j + ahead);
+                        ok = loaded(k);
                         if (!ok) break;
-                        p_phase[s] ^= 1;
                         tc::fence_after_sync();
-                        values(s, v_stage, j > w.j0);
-                        if (s == slots - 1) tc::commit(kv_empty + 8 * v_stage);
-                        if (more) {
-                            ok = wait(kv_full + 8 * stage, phase, 0x240);
-                            if (!ok) break;
-                            tc::fence_after_sync();
-                            scores(s, stage);
-                            if (j + 2 == j1) tc::commit(q_empty + 8 * s);
-                        }
-                    }
-                    if (ok && more) {
-                        tc::commit(kv_empty + 8 * stage);
-                        if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+                        scores(s, two ? s : 0, k);
+                        if (s == e - 1) release(k);
+                        if (j + ahead + 1 == steps) tc::commit_elect(q_empty + (two ? 8 * s : 0));
                     }
                 }
-            } while (ok && w.next(a));
+            }
+            at += 2 * steps;
         }
-        __syncwarp();
-    } else if (work && warp >= 10) {
+        if (sh.abort) {
+            // gave up: no MMA may be in flight when the block leaves
+            tc::commit_elect(leave);
+            tc::mbar_wait_for(leave, 0, a.timeout_ns);
+        }
+    } else if (work && warp == 10) {
         // ------------------------------------------------- query loads
-        PaWalk w;
-        w.start(a, start_s);
         uint32_t phase[2] = {0, 0};
-        const int t = tid - 320;
-        constexpr int V = D / 8;                     // 16-byte pieces of a row
+        constexpr int V = D / 8, kRows = 32 / V;     // 16-byte pieces of a row, rows a round
+        const int c = lane % V;
         bool ok = true;
-        do {
-            const PaItem &it = w.it;
-            if (w.j0 >= min(w.j1, it.tiles)) continue;
-            for (int s = 0; ok && s * kPaTile < it.rows; ++s) {
-                const int rows = min(it.rows - s * kPaTile, kPaTile);
-                if (lane == 0) ok = wait(q_empty + 8 * s, phase[s] ^ 1, 0x300 + s);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
+        for (uint32_t n = 0; ok; ++n) {
+            ok = item_wait(n);
+            const volatile PaItem &it = item(n);
+            if (!ok || it.rows == 0) break;
+            const int all = it.rows, row0 = it.row0, steps = it.steps, group_size = a.group;
+            const uint16_t *q = a.q + (int64_t)it.qs * a.q_s0 + (int64_t)it.h * group_size * a.q_s1 + c * 8;
+            item_done(n);
+            if (steps <= 0) continue;
+            for (int s = 0; ok && s * kPaTile < all; ++s) {
+                const int rows = min(all - s * kPaTile, kPaTile);
+                ok = all_wait(q_empty + 8 * s, phase[s] ^ 1, 0x300 + s);
                 if (!ok) break;
                 phase[s] ^= 1;
-                uint8_t *dst = q_smem + s * S::kQBytes;
-#pragma unroll 4
-                for (int e = t; e < rows * V; e += 64) {
-                    const int row = e / V, c = e % V, x = it.row0 + s * kPaTile + row;
-                    const int tok = x / a.group, head = it.h * a.group + x - tok * a.group;
-                    uint4 v = __ldg(reinterpret_cast<const uint4 *>(a.q + (w.q.qs + tok) * a.q_s0 +
-                                                                    head * a.q_s1 + c * 8));
-                    v.x ^= a.q_sign;
-                    v.y ^= a.q_sign;
-                    v.z ^= a.q_sign;
-                    v.w ^= a.q_sign;
-                    *reinterpret_cast<uint4 *>(dst + (c >> 3) * S::kHalf + row * 128 +
-                                               (((c & 7) ^ (row & 7)) << 4)) = v;
+                const uint32_t dst = tc::smem_u32(q_smem) + s * S::kQBytes + (c >> 3) * S::kHalf;
+                int row = lane / V;
+                const int x = row0 + s * kPaTile + row, tok = x / group_size;
+                int head = x - tok * group_size;
+                const uint16_t *src = q + tok * a.q_s0 + head * a.q_s1;
+                for (; row < rows; row += kRows) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                     dst + row * 128 + (((c & 7) ^ (row & 7)) << 4)),
+                                 "l"(src)
+                                 : "memory");
+                    head += kRows;
+                    src += kRows * a.q_s1;
+                    while (head >= group_size) { head -= group_size; src += a.q_s0 - group_size * a.q_s1; }
                 }
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(q_full + 8 * s);
+                arrive(q_full + 8 * s);
             }
-        } while (ok && w.next(a));
+        }
     } else if (work) {
         // -------------------------------------------- softmax and output
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int slot = warp >> 2, row = tid & 127;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;             // TMEM lane of the warp
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // TMEM lane of the warp
         const uint32_t t_s = tmem + slot * kPaTile + lanes, t_o = tmem + 2 * kPaTile + slot * D + lanes;
         const float c = a.scale2;
         constexpr float kShift = F16 ? 7.0f : 0.0f;   // fp16 weights: up to 2^15, small ones stay normal
-        PaWalk w;
-        w.start(a, start_s);
-        uint32_t s_phase = 0, pv_phase = 0, v_stage = 0, v_phase = 0;  // v_*: this block's next value tile
-        const uint32_t kv_addr = tc::smem_u32(kv_smem);
-        bool ok = true;
-        // a wait that some lane gives up is given up by the warp
-        auto all_wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
-            return (bool)__all_sync(0xffffffffu, wait(bar, parity, where));
-        };
-        uint32_t group_phase = 0;
+        uint32_t s_phase = 0, pv_phase = 0, group_phase = 0, merge_phase = 0, at = 0;
+        bool ok = true, owed = false;                 // owed: slot 0 may not have read what slot 1 left
         auto group_sync = [&]() {
-            tc::mbar_arrive(group + 8 * slot);
-            const bool r = all_wait(group + 8 * slot, group_phase, 0x440 + slot);
+            arrive(group + 8 * slot);
+            const bool r = all_wait(group + 8 * slot, group_phase, 0x450);
             group_phase ^= 1;
             return r;
         };
-        do {
-            const PaItem &it = w.it;
-            const int j1 = min(w.j1, it.tiles), rows = it.rows - slot * kPaTile;
-            const int steps = max(0, j1 - w.j0);
-            if (rows <= 0) {                          // one tile: this group has none
-                const uint32_t x = v_stage + 2 * steps;
-                v_phase ^= (x / S::kStages) & 1;
-                v_stage = x % S::kStages;
-                continue;
+        for (uint32_t n = 0; ok; ++n) {
+            ok = item_wait(n);
+            const volatile PaItem &it = item(n);
+            if (!ok || it.rows == 0) break;
+            const bool two = it.rows > kPaTile;
+            const int tile0 = two ? slot * kPaTile : 0, rows = min(it.rows - tile0, kPaTile);
+            const int steps = it.steps, ahead = two ? 1 : 2;
+            const int pos = it.pos0 + (it.row0 + tile0 + row) / a.group;
+            const bool busy = (warp & 3) * 32 < rows;
+            // a tile is seen whole by the warp's rows when its last key is
+            // not past the first one's and its first within the last one's window
+            int whole_end, whole_first;
+            {
+                const int wrow = it.row0 + tile0 + (warp & 3) * 32, last = it.row0 + tile0 + rows - 1;
+                whole_end = min(it.pos0 + wrow / a.group + 1, a.room);
+                whole_first = a.window > 0 ? it.pos0 + min(wrow + 31, last) / a.group - a.window + 1 : 0;
             }
-            const int x = it.row0 + slot * kPaTile + row, tok = x / a.group;
-            const int head = it.h * a.group + x - tok * a.group;
-            const int pos = w.q.pos0 + tok;
-            // the warp's rows: positions of the first and the last that there is
-            const int wrow = slot * kPaTile + (warp & 3) * 32;
-            const bool busy = wrow < it.rows;
-            const int lo_pos = w.q.pos0 + (it.row0 + wrow) / a.group;
-            const int hi_pos = w.q.pos0 + (it.row0 + min(wrow + 31, it.rows - 1)) / a.group;
-            const int limit = min(pos + 1, a.room);
             float m = -INFINITY, l = 0.0f;
-            for (int j = w.j0; j < j1; ++j) {
-                const int key0 = (j < it.sink_tiles ? j : it.w0 + j - it.sink_tiles) * kPaTile;
-                if (++v_stage == S::kStages) { v_stage = 0; v_phase ^= 1; }    // past the key tile
+            bool any = false;                         // a key tile of this slot's went by
+            for (int i = two ? 0 : slot; i < steps; i += ahead) {
+                int key0 = it.j0 + i;
+                {
+                    const int sink_tiles = it.sink_tiles;
+                    key0 = (key0 < sink_tiles ? key0 : it.w0 + key0 - sink_tiles) * kPaTile;
+                }
                 ok = all_wait(s_full + 8 * slot, s_phase, 0x400 + slot);
                 if (!ok) break;
                 s_phase ^= 1;
                 tc::fence_after_sync();
                 if (busy) {
-                    const bool whole = key0 + kPaTile <= min(lo_pos + 1, a.room) &&
-                                       (a.window <= 0 || key0 > hi_pos - a.window || key0 + kPaTile <= a.sinks);
-                    const int hi = limit - key0, sk = min(a.sinks - key0, hi);
-                    const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
-                    auto hide = [&](float (&s)[kPaTile]) {
-#pragma unroll
-                        for (int i = 0; i < kPaTile; ++i)
-                            s[i] = (i < hi && i >= lo) || i < sk ? s[i] : -INFINITY;
-                    };
                     float s[kPaTile], top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) ld_32x32b_x32(t_s + 32 * k, s + 32 * k);
                     tc::wait_ld();
-                    if (!whole) hide(s);
+                    if (a.negate) {
 #pragma unroll
-                    for (int i = 0; i < kPaTile; i += 8)
+                        for (int k = 0; k < kPaTile; ++k) s[k] = -s[k];
+                    }
+                    if (key0 + kPaTile > whole_end || (key0 < whole_first && key0 + kPaTile > a.sinks)) {
+                        const int hi = min(pos + 1, a.room) - key0, sk = min(a.sinks - key0, hi);
+                        const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) top4[k] = fmaxf(fmaxf(top4[k], s[i + 2 * k]), s[i + 2 * k + 1]);
+                        for (int k = 0; k < kPaTile; ++k)
+                            s[k] = (k < hi && k >= lo) || k < sk ? s[k] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int k = 0; k < kPaTile; k += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top4[e] = fmaxf(fmaxf(top4[e], s[k + 2 * e]), s[k + 2 * e + 1]);
                     const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
                     // (top - m) c > kLazy; m = -inf until the row has seen a key
                     const bool grow = top > m && (m == -INFINITY || (top - m) * c > kLazy);
@@ -610,191 +663,237 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                         const float mn = fmaxf(m, top);
                         const float f = m == -INFINITY ? 0.0f : pa_ex2((m - mn) * c);
                         m = mn;
-                        if (j > w.j0) {
+                        if (any) {
                             // the last PV is done: S's commit came after it
                             l *= f;
 #pragma unroll
-                            for (int k = 0; k < D / 32; ++k) {
-                                float o[32];
-                                ld_32x32b_x32(t_o + 32 * k, o);
+                            for (int k = 0; k < D / 16; ++k) {
+                                uint32_t o[16];
+                                tc::ld_32x32b_x16(t_o + 16 * k, o);
                                 tc::wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= f;
-                                st_32x32b_x32(t_o + 32 * k, reinterpret_cast<const uint32_t *>(o));
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tc::st_32x32b_x16(t_o + 16 * k, o);
                             }
                         }
                     }
                     const float mc = m == -INFINITY ? 0.0f : kShift - m * c;
                     const uint64_t c2 = f32x2(c, c), mc2 = f32x2(mc, mc);
-                    uint64_t sum[4] = {0, 0, 0, 0};
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < kPaTile / 32; ++k) {
                         uint32_t p[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
+                        for (int e = 0; e < 16; ++e) {
                             float x0, x1;
-                            split2(fma2(f32x2(s[32 * k + 2 * i], s[32 * k + 2 * i + 1]), c2, mc2), x0, x1);
+                            split2(fma2(f32x2(s[32 * k + 2 * e], s[32 * k + 2 * e + 1]), c2, mc2), x0, x1);
                             const float p0 = pa_ex2(x0), p1 = pa_ex2(x1);
-                            sum[i & 3] = add2(sum[i & 3], f32x2(p0, p1));
-                            p[i] = pack2<F16>(p0, p1);
+                            sum[e & 1] = add2(sum[e & 1], f32x2(p0, p1));
+                            p[e] = pack2<F16>(p0, p1);
                         }
                         tc::st_32x32b_x16(t_s + 16 * k, p);
                     }
                     float s0, s1;
-                    split2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
+                    split2(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;
                 }
+                any = true;
                 // value rows that nobody sees: zeros
-                const int key = key0 + row;
-                if (key0 + kPaTile > it.end || (key0 < it.first && key0 + kPaTile > it.kept)) {
-                    ok = all_wait(kv_full + 8 * v_stage, v_phase, 0x420 + slot);
-                    if (!ok) break;
-                    if (key >= it.end || (key < it.first && key >= it.kept)) {
-                        const uint32_t at = kv_addr + v_stage * S::kKvBytes + row * 128;
+                {
+                    const int end = it.end, first = it.first, kept = it.kept;
+                    if (key0 + kPaTile > end || (key0 < first && key0 + kPaTile > kept)) {
+                        const uint32_t v = at + 2 * i + 1;
+                        ok = all_wait(kv_full + 8 * stage_of(v), phase_of(v), 0x420 + slot);
+                        if (!ok) break;
+                        const int key = key0 + row;
+                        if (key >= end || (key < first && key >= kept)) {
+                            const uint32_t dst = tc::smem_u32(kv_smem) + stage_of(v) * S::kKvBytes + row * 128;
 #pragma unroll
-                        for (int half = 0; half < S::kHalves; ++half)
+                            for (int half = 0; half < S::kHalves; ++half)
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + half * S::kHalf + 16 * i),
-                                             "r"(0)
-                                             : "memory");
+                                for (int k = 0; k < 8; ++k)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + half * S::kHalf + 16 * k),
+                                                 "r"(0)
+                                                 : "memory");
+                        }
+                        tc::fence_proxy_async_smem();
                     }
-                    tc::fence_proxy_async_smem();
                 }
-                if (++v_stage == S::kStages) { v_stage = 0; v_phase ^= 1; }
                 if (busy) tc::wait_st();
+                if (owed) {                           // before this slot's O is written again
+                    ok = all_wait(merge_free, merge_phase, 0x460);
+                    if (!ok) break;
+                    merge_phase ^= 1;
+                    owed = false;
+                }
                 tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(p_full + 8 * slot);
-                pv_phase ^= 1;                        // P is on its way: one more PV to come
+                arrive(p_full + 8 * slot);
+                pv_phase ^= 1;                        // one more PV to come
             }
             if (!ok) break;
-            if (steps > 0) {
+            at += 2 * steps;
+            if (any) {
                 ok = all_wait(pv_done + 8 * slot, pv_phase ^ 1, 0x430 + slot);
                 if (!ok) break;
                 tc::fence_after_sync();
             }
+            if (!two && slot == 1) {
+                // an odd slot leaves m and l; its O lies beside slot 0's
+                if (any) {
+                    exchange[row] = m;
+                    exchange[kPaTile + row] = l;
+                    tc::fence_before_sync();
+                    arrive(merge_full);
+                    owed = true;
+                }
+                item_done(n);
+                continue;
+            }
+            // O = f0 O_0 + f1 O_1
+            float f0 = any ? 1.0f : 0.0f, f1 = 0.0f;
+            const bool merge = !two && steps > 1;
+            if (merge) {
+                ok = all_wait(merge_full, merge_phase, 0x470);
+                if (!ok) break;
+                merge_phase ^= 1;
+                tc::fence_after_sync();
+                const float m1 = exchange[row], l1 = exchange[kPaTile + row];
+                const float mn = fmaxf(m, m1);
+                f0 = m == -INFINITY ? 0.0f : pa_ex2((m - mn) * c);
+                f1 = m1 == -INFINITY ? 0.0f : pa_ex2((m1 - mn) * c);
+                m = mn;
+                l = l * f0 + l1 * f1;
+            }
+            const int c0 = it.c0, c1 = it.c1, h = it.h, qs = it.qs, row0 = it.row0 + tile0;
+            item_done(n);
             const bool live = row < rows;
-            const int64_t token = w.q.qs + tok;
-            if (w.j0 == 0 && w.j1 == w.units) {
+            // columns [16 k, 16 k + 16) of the row's O
+            auto columns = [&](int k, float (&o)[16]) {
+                uint32_t u[16];
+                if (any) {
+                    tc::ld_32x32b_x16(t_o + 16 * k, u);
+                    tc::wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = any ? __uint_as_float(u[e]) * f0 : 0.0f;
+                if (merge) {
+                    tc::ld_32x32b_x16(t_o + D + 16 * k, u);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] += __uint_as_float(u[e]) * f1;
+                }
+            };
+            auto log_sum = [&](float m, float l) {
+                return l == 0.0f ? -INFINITY : (m * c - kShift + __log2f(l)) * 0.69314718055994531f;
+            };
+            if (c0 == c1) {
                 // the whole item: the output
                 const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-                if (live && a.lse)
-                    a.lse[token * a.q_heads + head] = l == 0.0f ? -INFINITY : (m * c - kShift + __log2f(l)) * 0.69314718055994531f;
+                const int x = row0 + row, tok = x / a.group, head = h * a.group + x - tok * a.group;
+                const int64_t token = qs + tok;
                 uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1;
-                if (steps > 0 && busy) {
+                if (busy) {
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        float o[32];
-                        ld_32x32b_x32(t_o + 32 * k, o);
-                        tc::wait_ld();
+                    for (int k = 0; k < D / 16; ++k) {
+                        float o[16];
+                        columns(k, o);
                         if (live) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint4 v;
-                                uint32_t *u = &v.x;
+                            for (int i = 0; i < 2; ++i) {
+                                uint32_t v[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    u[e] = l == 0.0f ? 0u : pack2<F16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
-                                *reinterpret_cast<uint4 *>(out + 32 * k + 8 * i) = v;
+                                    v[e] = l == 0.0f ? 0u : pack2<F16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
+                                *reinterpret_cast<uint4 *>(out + 16 * k + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
                             }
                         }
                     }
-                } else if (live) {
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4 *>(out + 8 * i) = make_uint4(0, 0, 0, 0);
                 }
-            } else {
-                // a part of it: unnormalised, for the block that comes last
-                const int64_t total = start_s.total;
-                const int blocks = start_s.blocks;
-                const int c0 = pa_block_of(total, blocks, w.u), c1 = pa_block_of(total, blocks, w.u + w.units - 1);
-                auto part = [&](int block) {          // the item's first block has it as its last
-                    return a.parts + ((int64_t)(block * 2 + (block == c0 ? 1 : 0)) * 2 + slot) * kPaTile * (D + 2);
-                };
-                float *mine = part(blockIdx.x);
-                if (busy) {
+                if (live && a.lse) a.lse[token * a.q_heads + head] = log_sum(m, l);
+                // O is read: the next item's values may come (its P arrives after this)
+                tc::fence_before_sync();
+                if (merge) arrive(merge_free);
+                continue;
+            }
+            // a part, unnormalised, for the block that comes last: [D / 4][128 rows]
+            // vectors of four columns, then m and l, so that a warp writes and
+            // reads rows side by side
+            auto part = [&](int block) {              // the item's first block has it as its last
+                return a.parts + ((int64_t)(block * 2 + (block == c0 ? 1 : 0)) * 2 + slot) * kPaTile * (D + 2);
+            };
+            if (busy) {
+                float *dst = part(blockIdx.x);
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        float o[32];
-                        ld_32x32b_x32(t_o + 32 * k, o);
-                        tc::wait_ld();
-                        if (live) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<float4 *>(mine + row * D + 32 * k + 4 * i) =
-                                    make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                        }
-                    }
+                for (int k = 0; k < D / 16; ++k) {
+                    float o[16];
+                    columns(k, o);
                     if (live) {
-                        mine[kPaTile * D + row] = m;
-                        mine[kPaTile * D + kPaTile + row] = l;
-                    }
-                }
-                __threadfence();
-                if (!(ok = group_sync())) break;
-                if (row == 0) {
-                    const uint32_t before = atomicAdd(a.arrivals + c0 * 2 + slot, 1u);
-                    last_s[slot] = before == (uint32_t)(c1 - c0);
-                    if (before == (uint32_t)(c1 - c0)) a.arrivals[c0 * 2 + slot] = 0u;
-                }
-                if (!(ok = group_sync())) break;
-                if (last_s[slot]) {
-                    __threadfence();
-                    constexpr int V = D / 8;
-                    const int n = min(rows, kPaTile) * V;
-                    for (int e = row; e < n; e += 128) {
-                        const int rr = e / V, cc = e % V;
-                        float M = -INFINITY, L = 0.0f, o[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = 0.0f;
-#pragma unroll 4
-                        for (int b = c0; b <= c1; ++b) {
-                            const float *p = part(b);
-                            const float pm = __ldcg(p + kPaTile * D + rr), pl = __ldcg(p + kPaTile * D + kPaTile + rr);
-                            const float4 u = __ldcg(reinterpret_cast<const float4 *>(p + rr * D + cc * 8));
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + rr * D + cc * 8) + 1);
-                            const float mn = fmaxf(M, pm);
-                            const float f = M == -INFINITY ? 0.0f : pa_ex2((M - mn) * c);
-                            const float g = pm == -INFINITY ? 0.0f : pa_ex2((pm - mn) * c);
-                            M = mn;
-                            L = L * f + pl * g;
-                            const float y[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = o[i] * f + y[i] * g;
-                        }
-                        const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
-                        const int xx = it.row0 + slot * kPaTile + rr, tt = xx / a.group;
-                        const int hh = it.h * a.group + xx - tt * a.group;
-                        uint4 v;
-                        uint32_t *u = &v.x;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            u[i] = L == 0.0f ? 0u : pack2<F16>(o[2 * i] * inv, o[2 * i + 1] * inv);
-                        *reinterpret_cast<uint4 *>(a.out + (w.q.qs + tt) * a.out_s0 + hh * a.out_s1 + cc * 8) = v;
-                        if (cc == 0 && a.lse)
-                            a.lse[(int64_t)(w.q.qs + tt) * a.q_heads + hh] =
-                                L == 0.0f ? -INFINITY : (M * c - kShift + __log2f(L)) * 0.69314718055994531f;
+                            *reinterpret_cast<float4 *>(dst + ((4 * k + i) * kPaTile + row) * 4) =
+                                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
+                if (live) {
+                    dst[kPaTile * D + row] = m;
+                    dst[kPaTile * D + kPaTile + row] = l;
+                }
             }
-            // O is read: the next item's values may come (its P arrives after this)
             tc::fence_before_sync();
-        } while (ok && w.next(a));
+            if (merge) arrive(merge_free);
+            __threadfence();
+            if (!(ok = group_sync())) break;
+            if (row == 0) {
+                const bool last = atomicAdd(a.arrivals + c0 * 2 + slot, 1u) == (uint32_t)(c1 - c0);
+                sh.last[slot] = last;
+                if (last) a.arrivals[c0 * 2 + slot] = 0u;
+            }
+            if (!(ok = group_sync())) break;
+            if (!sh.last[slot]) continue;
+            __threadfence();
+            // a thread joins some rows' some columns: its row's parts' maximum,
+            // then their weighted sums
+            const int groups = (rows + 31) / 32;      // of 32 rows
+            for (int e = warp & 3; e < groups * (D / 16); e += 4) {
+                const int r = e % groups * 32 + lane, k0 = e / groups * 4;
+                if (r >= rows) continue;
+                float M = -INFINITY, L = 0.0f, o[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = 0.0f;
+#pragma unroll 4
+                for (int b = c0; b <= c1; ++b) M = fmaxf(M, __ldcg(part(b) + kPaTile * D + r));
+                if (M == -INFINITY) M = 0.0f;
+#pragma unroll 2
+                for (int b = c0; b <= c1; ++b) {
+                    const float *p = part(b);
+                    const float g = pa_ex2((__ldcg(p + kPaTile * D + r) - M) * c);
+                    L += __ldcg(p + kPaTile * D + kPaTile + r) * g;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + ((k0 + k) * kPaTile + r) * 4));
+                        o[4 * k] += y.x * g;
+                        o[4 * k + 1] += y.y * g;
+                        o[4 * k + 2] += y.z * g;
+                        o[4 * k + 3] += y.w * g;
+                    }
+                }
+                const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
+                const int x = row0 + r, tok = x / a.group, head = h * a.group + x - tok * a.group;
+                const int64_t token = qs + tok;
+                uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1 + 4 * k0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t v[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        v[k] = L == 0.0f ? 0u : pack2<F16>(o[8 * i + 2 * k] * inv, o[8 * i + 2 * k + 1] * inv);
+                    *reinterpret_cast<uint4 *>(out + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                if (k0 == 0 && a.lse) a.lse[token * a.q_heads + head] = log_sum(M, L);
+            }
+        }
     }
     __syncwarp();
-    if (work && warp == 9 && lane == 0 && abort_s) {
-        // gave up: no load may be in flight when the block leaves
-        const uint64_t until = tc::now_ns() + a.timeout_ns;
-        for (int i = 0; i < S::kStages; ++i)
-            if (filled >> i & 1)
-                while (!tc::mbar_test(kv_full + 8 * i, fill_phase >> i & 1) && tc::now_ns() < until) {}
-    }
-    if (work && warp == 8 && lane == 0 && abort_s) {
-        // nor an MMA
-        tc::commit(leave);
-        tc::mbar_wait_for(leave, 0, a.timeout_ns);
-    }
     tc::fence_before_sync();
     __syncthreads();
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
