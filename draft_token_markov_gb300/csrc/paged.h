@@ -48,8 +48,6 @@ struct WriteArgs {
 };
 
 struct AttnArgs {
-    const uint16_t *q;
-    int64_t q_s0, q_s1;
     int negate;                // the scale is negative
     const int32_t *table;
     int64_t table_s0;
@@ -57,6 +55,7 @@ struct AttnArgs {
     const int64_t *idx;
     const int32_t *query_start, *seq_lens;
     int rows, T, q_heads, kv_heads, group;
+    int tile_tokens;           // tokens of a row tile: 128 / group
     float scale2;              // |scale| log2(e), not zero
     int window, sinks;
     uint16_t *out;
@@ -99,7 +98,8 @@ cudaError_t launch_paged_layout(const LayoutArgs &a, cudaStream_t s);
 cudaError_t launch_paged_write(const WriteArgs &a, cudaStream_t s);
 cudaError_t paged_attention_prepare();
 size_t paged_attention_parts(int head_dim, int blocks);
-cudaError_t launch_paged_attention(const AttnArgs &a, const CUtensorMap &k, const CUtensorMap &v,
+cudaError_t launch_paged_attention(const AttnArgs &a, const CUtensorMap &q, const CUtensorMap &k,
+                                   const CUtensorMap &v,
                                    int head_dim, bool f16, int blocks, cudaStream_t s);
 cudaError_t launch_verify(VerifyArgs a, bool target_f32, bool cache_f32, int sms, cudaStream_t s);
 

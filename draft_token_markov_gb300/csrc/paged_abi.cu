@@ -61,6 +61,24 @@ bool encode_cache_map(CUtensorMap *m, const markov_cache_view &v, const markov_p
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries [tokens, heads, head_dim] as tiles of 64 elements by a group of
+// heads by the tokens that 128 rows hold.
+bool encode_query_map(CUtensorMap *m, const void *q, int64_t s0, int64_t s1, int tokens,
+                      const markov_paged_plan &p) {
+    const EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn) return false;
+    const int group = p.d.q_heads / p.d.kv_heads;
+    const cuuint64_t dims[3] = {(cuuint64_t)p.d.head_dim, (cuuint64_t)p.d.q_heads, (cuuint64_t)tokens};
+    // a lone token's stride is never used, but has to be one
+    const cuuint64_t strides[2] = {(cuuint64_t)s1 * 2, (cuuint64_t)(tokens > 1 ? s0 : s1 * p.d.q_heads) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)(128 / group)};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, p.d.dtype == MARKOV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void *>(q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Token rows [T, heads, head_dim].
 bool valid_rows(const void *p, int64_t s0, int64_t s1, const markov_paged_desc &d) {
     return p && aligned16(p) && s0 >= 0 && s1 >= d.head_dim && s0 % 8 == 0 && s1 % 8 == 0;
@@ -75,7 +93,8 @@ markov_status markov_paged_plan_create(const markov_paged_desc *desc, markov_pag
     *out = nullptr;
     if (!desc) return MARKOV_EINVAL;
     const markov_paged_desc d = *desc;
-    if (d.kv_heads < 1 || d.q_heads < d.kv_heads || d.q_heads > 256 || d.q_heads % d.kv_heads != 0)
+    if (d.kv_heads < 1 || d.q_heads < d.kv_heads || d.q_heads > 256 || d.q_heads % d.kv_heads != 0 ||
+        d.q_heads / d.kv_heads > 128)
         return MARKOV_EINVAL;
     if (d.head_dim != 64 && d.head_dim != 128) return MARKOV_EINVAL;
     if (d.page_size < 8 || d.page_size > 256 || (d.page_size & (d.page_size - 1)) != 0)
@@ -263,13 +282,11 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
         return MARKOV_EINVAL;
     DeviceGuard guard(p->d.device);
     if (!guard.ok) return MARKOV_EDEVICE;
-    CUtensorMap kmap, vmap;
-    if (!encode_cache_map(&kmap, *k_cache, *p) || !encode_cache_map(&vmap, *v_cache, *p))
+    CUtensorMap qmap, kmap, vmap;
+    if (!encode_query_map(&qmap, q, q_s0, q_s1, num_tokens, *p) ||
+        !encode_cache_map(&kmap, *k_cache, *p) || !encode_cache_map(&vmap, *v_cache, *p))
         return MARKOV_EINVAL;
     AttnArgs a{};
-    a.q = static_cast<const uint16_t *>(q);
-    a.q_s0 = q_s0;
-    a.q_s1 = q_s1;
     a.negate = scale < 0.0f;
     a.table = page_table;
     a.table_s0 = table_s0;
@@ -284,6 +301,7 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     a.q_heads = p->d.q_heads;
     a.kv_heads = p->d.kv_heads;
     a.group = p->d.q_heads / p->d.kv_heads;
+    a.tile_tokens = 128 / a.group;
     a.scale2 = std::fmax(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
     // a row has fewer keys than kMaxRoom
     a.window = window >= kMaxRoom ? 0 : window;
@@ -296,7 +314,7 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     a.arrivals = p->ctrl + kArrivals;
     a.status = p->ctrl;
     a.timeout_ns = (uint64_t)p->d.timeout_ms * 1000000ull;
-    if (launch_paged_attention(a, kmap, vmap, p->d.head_dim, p->d.dtype == MARKOV_F16, p->blocks,
+    if (launch_paged_attention(a, qmap, kmap, vmap, p->d.head_dim, p->d.dtype == MARKOV_F16, p->blocks,
                                (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();
         return MARKOV_ECUDA;

@@ -4,8 +4,8 @@
 //
 // Rows.  The queries of a row's tokens that share a key head are stacked,
 // row = token * group + head in group, so an MMA tile of 128 rows holds
-// 128 / group tokens whatever the group, and keys and values are read once
-// for all of them.  An item is (request, key head, up to two such tiles); its
+// 128 / group whole tokens (one box of a TMA load), and keys and values are
+// read once for all of them.  An item is (request, key head, up to two such tiles); its
 // keys go by in tiles of 128:
 //   S = Q K^T           128 x 128, fp32 in TMEM (both operands in shared memory)
 //   m, p = 2^(S c - m c), l += sum p
@@ -24,19 +24,21 @@
 // Work.  A unit is one key tile of an item.  The units of the call, in order
 // of request, key head, tile of rows and keys, are cut into one contiguous
 // range a block, whatever the lengths, so every block streams the same number
-// of tiles; every block finds its range from the lengths by itself (a scan
-// over the rows).  An item cut between blocks leaves its parts, O, m and l in
+// of tiles; a warp of every block finds its range from the lengths by itself
+// (a scan over the rows).  An item cut between blocks leaves its parts, O, m and l in
 // fp32, in the plan's scratch, and the block that finishes last joins them in
 // the order of the keys.
 //
 // Roles.  Warps 0-3 and 4-7: softmax and output of the two slots, a thread a
-// row; warp 8 issues MMAs; warp 9 loads key and value tiles by TMA, a page a
-// box (a box of a page that nobody sees is read out of range, as zeros); warp
-// 10 loads queries; warp 11 walks the block's items and leaves each for the
-// others in a ring in shared memory.  (Nothing of an item stays in a register
-// for long: shared memory takes nearly all of the L1 cache, so that a spilled
-// register costs a trip to L2.)  Value rows that no row of the item sees can
-// hold anything: they are zeroed in shared memory before the MMA (0 * NaN).
+// row; warp 8 issues MMAs; warps 9 and 10 load key and value tiles by TMA, a
+// page a box (a box of a page that nobody sees is read out of range, as
+// zeros; at 16 keys a page one warp for both would take as long as the
+// loads); warp 11 walks the block's items, leaves each for the others in a
+// ring in shared memory and loads its queries.  (Nothing of an item stays in
+// a register for long: shared memory takes nearly all of the L1 cache, so that
+// a spilled register costs a trip to L2.)  Value rows that no row of the item
+// sees can hold anything: they are zeroed in shared memory before the MMA
+// (0 * NaN).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -68,7 +70,7 @@ struct PaShape {
 // ------------------------------------------------------------------- items
 
 struct PaItem {
-    int rows, row0;            // rows of the item (0: no more items), the first within the request
+    int tokens, t0;            // tokens of the item (0: no more items), the first within the request
     int qs, pos0, state;       // the request's first token, its position; its table row, -1 for none
     int h;                     // key head
     int end, first, kept;      // some row sees keys [first, end) and [0, kept)
@@ -96,11 +98,12 @@ __device__ __forceinline__ PaReq pa_request(const AttnArgs &a, int r) {
     return q;
 }
 
-// The key tiles of pair m of a request; at least one unit.
+// The units of the m-th pair of row tiles of a request: its key tiles, at
+// least one.
 __device__ __forceinline__ int pa_units(const AttnArgs &a, const PaReq &q, int m, PaItem &it) {
-    it.row0 = m * 2 * kPaTile;
-    it.rows = min(q.np * a.group - it.row0, 2 * kPaTile);
-    const int p0 = q.pos0 + it.row0 / a.group, p1 = q.pos0 + (it.row0 + it.rows - 1) / a.group;
+    it.t0 = m * 2 * a.tile_tokens;
+    it.tokens = min(q.np - it.t0, 2 * a.tile_tokens);
+    const int p0 = q.pos0 + it.t0, p1 = p0 + it.tokens - 1;
     it.end = q.state < 0 ? 0 : max(0, min(p1 + 1, a.room));
     it.first = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
     it.kept = min(min(a.sinks, it.first), it.end);
@@ -113,95 +116,30 @@ __device__ __forceinline__ int pa_units(const AttnArgs &a, const PaReq &q, int m
 }
 
 __device__ __forceinline__ int pa_pairs(const AttnArgs &a, const PaReq &q) {
-    return (q.np * a.group + 2 * kPaTile - 1) / (2 * kPaTile);
+    return (q.np + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
 }
 
-// Where a block's range starts, and what its warps share, in shared memory.
+// What the block's warps share, in shared memory.
 struct PaShared {
-    int r, h, m, j;            // first unit: request, key head, pair of row tiles, key tile
-    int blocks;                // blocks that have work
     uint32_t abort, tmem, last[2];
-    int64_t u0, u1, total;     // its units, all units
     PaItem ring[kRing];
 };
 
-__device__ __forceinline__ int64_t pa_first_unit(int64_t total, int blocks, int c) {
-    return total * c / blocks;
-}
+// The call's units cut into ranges of equal length, the first `rem` one longer.
+struct PaSplit {
+    uint32_t blocks, base, rem;
 
-__device__ __forceinline__ int pa_block_of(int64_t total, int blocks, int64_t u) {
-    int c = (int)(u * blocks / total);
-    while (pa_first_unit(total, blocks, c + 1) <= u) ++c;
-    return c;
-}
-
-// Every thread: this block's range.  scratch: an int64 a warp.
-__device__ __forceinline__ void pa_schedule(const AttnArgs &a, PaShared *out, int64_t *scratch) {
-    constexpr int kPer = (kPagedMaxRows + kPaThreads - 1) / kPaThreads;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t mine[kPer], sum = 0;
-    PaItem it;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int r = tid * kPer + k;
-        mine[k] = 0;
-        if (r < a.rows) {
-            const PaReq q = pa_request(a, r);
-            const int pairs = pa_pairs(a, q);
-            int64_t units = 0;
-            for (int m = 0; m < pairs; ++m) units += pa_units(a, q, m, it);
-            mine[k] = units * a.kv_heads;
-        }
-        sum += mine[k];
+    __device__ __forceinline__ void cut(uint32_t total, uint32_t grid) {
+        blocks = min(grid, total);
+        base = blocks ? total / blocks : 0;
+        rem = total - base * blocks;
     }
-    int64_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+    __device__ __forceinline__ uint32_t first(uint32_t c) const { return c * base + min(c, rem); }
+    __device__ __forceinline__ uint32_t block_of(uint32_t u) const {
+        const uint32_t longer = rem * (base + 1);
+        return u < longer ? u / (base + 1) : rem + (u - longer) / base;
     }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kPaThreads / 32; ++w) {
-        if (w < warp) incl += scratch[w];
-        total += scratch[w];
-    }
-    const int blocks = (int)min((int64_t)gridDim.x, total);
-    if (tid == 0) {
-        out->total = total;
-        out->blocks = blocks;
-    }
-    if ((int)blockIdx.x >= blocks) return;
-    const int64_t u0 = pa_first_unit(total, blocks, blockIdx.x);
-    int64_t before = incl - sum;
-    if (u0 < before || u0 >= incl) return;
-    // the thread whose rows hold the first unit
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        if (u0 >= before && u0 < before + mine[k]) {
-            const int r = tid * kPer + k;
-            const PaReq q = pa_request(a, r);
-            const int64_t head = mine[k] / a.kv_heads;
-            int64_t rem = u0 - before;
-            const int h = (int)(rem / head);
-            rem -= h * head;
-            int m = 0;
-            for (;; ++m) {
-                const int units = pa_units(a, q, m, it);
-                if (rem < units) break;
-                rem -= units;
-            }
-            out->r = r;
-            out->h = h;
-            out->m = m;
-            out->j = (int)rem;
-            out->u0 = u0;
-            out->u1 = pa_first_unit(total, blocks, blockIdx.x + 1);
-        }
-        before += mine[k];
-    }
-}
+};
 
 // ----------------------------------------------------------------- helpers
 
@@ -252,6 +190,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int 
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, int x, int y, int z,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 __device__ __forceinline__ void ld_32x32b_x32(uint32_t taddr, float *r) {
     uint32_t *u = reinterpret_cast<uint32_t *>(r);
     asm volatile(
@@ -286,6 +233,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return bf16x2_rn(lo, hi);
 }
 
+// The lowest n bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t ones(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
 // Two fp32 values in one register pair, and the packed arithmetic on them.
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
     uint64_t r;
@@ -316,8 +268,8 @@ __device__ __forceinline__ float pa_ex2(float x) {
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kPaThreads, 1)
-paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap kmap,
-                       const __grid_constant__ CUtensorMap vmap) {
+paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap qmap,
+                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using S = PaShape<D>;
     extern __shared__ __align__(1024) uint8_t base[];
     uint8_t *q_smem = base, *kv_smem = base + 2 * S::kQBytes;
@@ -332,7 +284,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                    merge_full = q_full + 96, merge_free = q_full + 104, leave = q_full + 112,
                    item_full = q_full + 128, item_empty = item_full + 8 * kRing;
     if (tid == 0) {
-        sh.abort = ld_acquire_u32(a.status);         // a pending status: nothing is done
+        sh.abort = 0;
         for (int i = 0; i < S::kStages; ++i) {
             tc::mbar_init(kv_full + 8 * i, 1);
             tc::mbar_init(kv_empty + 8 * i, 1);
@@ -354,13 +306,18 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         }
         tc::mbar_init_fence();
     }
+    // the scan's first loads are on their way while the block sets up
+    PaReq q{0, 0, 0, 0};
+    uint32_t pending = 0;
+    if (warp == 11) {
+        pending = ld_acquire_u32(a.status);          // a pending status: nothing is done
+        if (lane < a.rows) q = pa_request(a, lane);
+    }
     if (warp == 8) tc::tmem_alloc(tc::smem_u32(&sh.tmem), 512);
-    pa_schedule(a, &sh, reinterpret_cast<int64_t *>(exchange));
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
-    const bool work = !sh.abort && (int)blockIdx.x < sh.blocks;
     const PaWait wait{a.timeout_ns, a.status, &sh.abort};
     // a wait that some lane gives up is given up by the warp
     auto all_wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
@@ -370,7 +327,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
     };
-    // key and value tiles in the order they are loaded: K V K V ...
+    // key and value tiles in the order they are used: K V K V ...
     auto stage_of = [](uint32_t at) { return at % S::kStages; };
     auto phase_of = [](uint32_t at) { return (at / S::kStages) & 1; };
     // the n-th item; its fields are read from shared memory where they are used
@@ -379,17 +336,76 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     auto item_done = [&](uint32_t n) { arrive(item_empty + 8 * (n % kRing)); };
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (work && warp == 11) {
-        // ------------------------------------------------------- the walk
+    if (warp == 11) {
+        // ------------------------------------------- the walk, query loads
         PaItem it;
-        PaReq q = pa_request(a, sh.r);
-        int r = sh.r, h = sh.h, m = sh.m, j = sh.j, pairs = pa_pairs(a, q);
-        int64_t u = sh.u0 - j;                       // the current item's first unit
+        int64_t total = 0;
+        // the rows' units before and with each, where key tiles will be
+        uint32_t *units_to = reinterpret_cast<uint32_t *>(kv_smem);
+        for (int r0 = 0; r0 < a.rows; r0 += 32) {
+            if (r0 > 0) {
+                q.np = 0;
+                if (r0 + lane < a.rows) q = pa_request(a, r0 + lane);
+            }
+            const int pairs = pa_pairs(a, q);
+            int64_t x = 0;
+            for (int m = 0; m < pairs; ++m) x += pa_units(a, q, m, it);
+            x *= a.kv_heads;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            units_to[r0 + lane] = (uint32_t)(total + x);
+            total += __shfl_sync(0xffffffffu, x, 31);
+        }
+        __syncwarp();
+        if (total > INT32_MAX) {                     // units are counted in 32 bits
+            if (lane == 0 && !pending) set_status(a.status, 2u /* MARKOV_EUNSUPPORTED */, 0x600);
+            total = 0;
+        }
+        PaSplit split;
+        split.cut(pending ? 0u : (uint32_t)total, gridDim.x);
+        uint32_t u = 0, u_end = 0;                   // the current item's first unit, the range's end
+        int r = 0, h = 0, m = 0, j = 0, pairs = 0;
+        if (blockIdx.x < split.blocks) {
+            const uint32_t u0 = split.first(blockIdx.x);
+            u_end = split.first(blockIdx.x + 1);
+            for (int r0 = 0;; r0 += 32) {
+                const int x = r0 + lane;
+                const bool here = x < a.rows && u0 < units_to[x] && (x == 0 || u0 >= units_to[x - 1]);
+                const uint32_t found = __ballot_sync(0xffffffffu, here);
+                if (found) { r = r0 + __ffs(found) - 1; break; }
+            }
+            const uint32_t before = r ? units_to[r - 1] : 0u, head = (units_to[r] - before) / a.kv_heads;
+            if (a.rows <= 32) {                      // a lane has it
+                q.np = __shfl_sync(0xffffffffu, q.np, r);
+                q.qs = __shfl_sync(0xffffffffu, q.qs, r);
+                q.pos0 = __shfl_sync(0xffffffffu, q.pos0, r);
+                q.state = __shfl_sync(0xffffffffu, q.state, r);
+            } else {
+                q = pa_request(a, r);
+            }
+            pairs = pa_pairs(a, q);
+            h = (u0 - before) / head;
+            u = before + h * head;
+            for (;; ++m) {
+                const uint32_t units = pa_units(a, q, m, it);
+                if (u0 - u < units) break;
+                u += units;
+            }
+            j = u0 - u;
+        }
+        tc::fence_proxy_async_smem();                // units_to is read; TMA writes come
+        uint32_t q_phase[2] = {0, 0};
+        int q_token = 0, q_head = 0, q_tiles = 0;    // the queries of the item published last
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
+            const bool more = u < u_end;
+            const int last_token = q_token, last_head = q_head, last_tiles = q_tiles;
             ok = all_wait(item_empty + 8 * (n % kRing), (n / kRing & 1) ^ 1, 0x510);
             if (!ok) break;
-            const bool more = u < sh.u1;
+            q_tiles = 0;
             if (more) {
                 const int units = pa_units(a, q, m, it);
                 it.qs = q.qs;
@@ -397,20 +413,25 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 it.state = q.state;
                 it.h = h;
                 it.j0 = j;
-                const int j1 = (int)min((int64_t)units, sh.u1 - u);
+                const int j1 = (int)min((uint32_t)units, u_end - u);
                 it.c0 = it.c1 = blockIdx.x;
                 if (j > 0 || j1 < units) {
-                    it.c0 = pa_block_of(sh.total, sh.blocks, u);
-                    it.c1 = pa_block_of(sh.total, sh.blocks, u + units - 1);
+                    it.c0 = split.block_of(u);
+                    it.c1 = split.block_of(u + units - 1);
                 }
                 it.steps = min(j1, it.steps) - j;    // 0 where nothing is seen
+                if (it.steps > 0) {
+                    q_token = q.qs + it.t0;
+                    q_head = h * a.group;
+                    q_tiles = it.tokens > a.tile_tokens ? 2 : 1;
+                }
                 u += units;
                 j = 0;
                 if (++m == pairs) {
                     m = 0;
                     if (++h == a.kv_heads) {
                         h = 0;
-                        if (u < sh.u1) {
+                        if (u < u_end) {
                             do {
                                 q = pa_request(a, ++r);
                             } while (q.np <= 0);
@@ -419,23 +440,50 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     }
                 }
             } else {
-                it.rows = 0;
+                it.tokens = 0;
             }
             if (lane == 0) sh.ring[n % kRing] = it;
             arrive(item_full + 8 * (n % kRing));
+            // the queries of the item before (of the first at once), so that
+            // the loads of keys know of an item ahead
+            auto load = [&](int token, int head, int tiles) {
+                for (int s = 0; ok && s < tiles; ++s) {
+                    ok = all_wait(q_empty + 8 * s, q_phase[s] ^ 1, 0x300 + s);
+                    if (!ok) break;
+                    q_phase[s] ^= 1;
+                    if (lane == 0) {
+                        tc::mbar_expect_tx(q_full + 8 * s, a.tile_tokens * a.group * D * 2);
+                        for (int half = 0; half < S::kHalves; ++half)
+                            tma_load_3d(tc::smem_u32(q_smem) + s * S::kQBytes + half * S::kHalf, &qmap, half * 64,
+                                        head, token + s * a.tile_tokens, q_full + 8 * s);
+                    }
+                    __syncwarp();
+                }
+            };
+            if (n > 1) load(last_token, last_head, last_tiles);
+            if (n == 0) load(q_token, q_head, q_tiles);
+            if (n == 0) q_tiles = 0;
             if (!more) break;
         }
-    } else if (work && warp == 9) {
+        if (lane == 0 && sh.abort) {
+            // gave up: no load may be in flight when the block leaves
+            const uint64_t until = tc::now_ns() + a.timeout_ns;
+            for (int s = 0; s < 2; ++s)
+                while (!tc::mbar_test(q_full + 8 * s, q_phase[s] ^ 1) && tc::now_ns() < until) {}
+        }
+    } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------ key / value loads
+        const bool values = warp == 10;
+        const CUtensorMap *map = values ? &vmap : &kmap;
         uint32_t filled = 0, fill_phase = 0;         // stages it filled, and their phases
         const int page = 1 << a.page_shift;
         const int box = min(page, kPaTile), boxes = kPaTile / box;     // boxes of a tile
-        uint32_t at = 0;
+        uint32_t at = values ? 1 : 0;
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
             ok = item_wait(n);
             const volatile PaItem &it = item(n);
-            if (!ok || it.rows == 0) break;
+            if (!ok || it.tokens == 0) break;
             const int32_t *table = a.table + (int64_t)max(it.state, 0) * a.table_s0;
             const int j0 = it.j0, j1 = j0 + it.steps, sinks = it.sink_tiles, w0 = it.w0;
             const int end = it.end, first = it.first, kept = it.kept, h = it.h;
@@ -446,26 +494,23 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                            ? __ldg(table + (key >> a.page_shift)) : -1;
             };
             int next = j0 < j1 ? page_of(j0) : -1;
-            for (int j = j0; ok && j < j1; ++j) {
+            for (int j = j0; j < j1; ++j, at += 2) {
                 const int pid = next;
                 if (j + 1 < j1) next = page_of(j + 1);
                 const int key = (j < sinks ? j : w0 + j - sinks) * kPaTile + lane * box;
-                for (int kv = 0; ok && kv < 2; ++kv, ++at) {
-                    const uint32_t stage = stage_of(at), phase = phase_of(at), full = kv_full + 8 * stage;
-                    ok = all_wait(kv_empty + 8 * stage, phase ^ 1, 0x100 + stage);
-                    if (!ok) break;
-                    if (lane == 0) tc::mbar_expect_tx(full, S::kKvBytes);
-                    __syncwarp();
-                    if (lane < boxes) {
-                        const uint32_t dst = tc::smem_u32(kv_smem + stage * S::kKvBytes) + lane * box * 128;
+                const uint32_t stage = stage_of(at), phase = phase_of(at), full = kv_full + 8 * stage;
+                ok = all_wait(kv_empty + 8 * stage, phase ^ 1, 0x100 + stage);
+                if (!ok) break;
+                if (lane == 0) tc::mbar_expect_tx(full, S::kKvBytes);
+                __syncwarp();
+                if (lane < boxes) {
+                    const uint32_t dst = tc::smem_u32(kv_smem + stage * S::kKvBytes) + lane * box * 128;
 #pragma unroll
-                        for (int half = 0; half < S::kHalves; ++half)
-                            tma_load_4d(dst + half * S::kHalf, kv ? &vmap : &kmap, half * 64,
-                                        key & (page - 1), h, pid, full);
-                    }
-                    filled |= 1u << stage;
-                    fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
+                    for (int half = 0; half < S::kHalves; ++half)
+                        tma_load_4d(dst + half * S::kHalf, map, half * 64, key & (page - 1), h, pid, full);
                 }
+                filled |= 1u << stage;
+                fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
             }
         }
         if (lane == 0 && sh.abort) {
@@ -475,7 +520,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 if (filled >> i & 1)
                     while (!tc::mbar_test(kv_full + 8 * i, fill_phase >> i & 1) && tc::now_ns() < until) {}
         }
-    } else if (work && warp == 8) {
+    } else if (warp == 8) {
         // ---------------------------------------------------- MMA issue
         // the whole warp, so that control flow and descriptors stay uniform;
         // an elected lane issues
@@ -505,11 +550,11 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         auto release = [&](uint32_t k) { tc::commit_elect(kv_empty + 8 * stage_of(k)); };
         for (uint32_t n = 0; ok; ++n) {
             ok = item_wait(n);
-            const int rows = item(n).rows, steps = item(n).steps;
-            if (!ok || rows == 0) break;
+            const int tokens = item(n).tokens, steps = item(n).steps;
+            if (!ok || tokens == 0) break;
             item_done(n);
             if (steps <= 0) continue;                // nothing seen: the output is written without MMAs
-            const bool two = rows > kPaTile;         // row tiles
+            const bool two = tokens > a.tile_tokens; // row tiles
             // the first scores
             for (int s = 0; ok && s < 2; ++s) {
                 if (!two && s == steps) break;
@@ -553,45 +598,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             tc::commit_elect(leave);
             tc::mbar_wait_for(leave, 0, a.timeout_ns);
         }
-    } else if (work && warp == 10) {
-        // ------------------------------------------------- query loads
-        uint32_t phase[2] = {0, 0};
-        constexpr int V = D / 8, kRows = 32 / V;     // 16-byte pieces of a row, rows a round
-        const int c = lane % V;
-        bool ok = true;
-        for (uint32_t n = 0; ok; ++n) {
-            ok = item_wait(n);
-            const volatile PaItem &it = item(n);
-            if (!ok || it.rows == 0) break;
-            const int all = it.rows, row0 = it.row0, steps = it.steps, group_size = a.group;
-            const uint16_t *q = a.q + (int64_t)it.qs * a.q_s0 + (int64_t)it.h * group_size * a.q_s1 + c * 8;
-            item_done(n);
-            if (steps <= 0) continue;
-            for (int s = 0; ok && s * kPaTile < all; ++s) {
-                const int rows = min(all - s * kPaTile, kPaTile);
-                ok = all_wait(q_empty + 8 * s, phase[s] ^ 1, 0x300 + s);
-                if (!ok) break;
-                phase[s] ^= 1;
-                const uint32_t dst = tc::smem_u32(q_smem) + s * S::kQBytes + (c >> 3) * S::kHalf;
-                int row = lane / V;
-                const int x = row0 + s * kPaTile + row, tok = x / group_size;
-                int head = x - tok * group_size;
-                const uint16_t *src = q + tok * a.q_s0 + head * a.q_s1;
-                for (; row < rows; row += kRows) {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     dst + row * 128 + (((c & 7) ^ (row & 7)) << 4)),
-                                 "l"(src)
-                                 : "memory");
-                    head += kRows;
-                    src += kRows * a.q_s1;
-                    while (head >= group_size) { head -= group_size; src += a.q_s0 - group_size * a.q_s1; }
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                tc::fence_proxy_async_smem();
-                arrive(q_full + 8 * s);
-            }
-        }
-    } else if (work) {
+    } else {
         // -------------------------------------------- softmax and output
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int slot = warp >> 2, row = tid & 127;
@@ -610,20 +617,18 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         for (uint32_t n = 0; ok; ++n) {
             ok = item_wait(n);
             const volatile PaItem &it = item(n);
-            if (!ok || it.rows == 0) break;
-            const bool two = it.rows > kPaTile;
-            const int tile0 = two ? slot * kPaTile : 0, rows = min(it.rows - tile0, kPaTile);
+            if (!ok || it.tokens == 0) break;
+            const bool two = it.tokens > a.tile_tokens;
+            const int t0 = it.t0 + (two ? slot * a.tile_tokens : 0);
+            const int rows = min(it.tokens + it.t0 - t0, a.tile_tokens) * a.group;
             const int steps = it.steps, ahead = two ? 1 : 2;
-            const int pos = it.pos0 + (it.row0 + tile0 + row) / a.group;
+            const int pos = it.pos0 + t0 + row / a.group;
             const bool busy = (warp & 3) * 32 < rows;
             // a tile is seen whole by the warp's rows when its last key is
             // not past the first one's and its first within the last one's window
-            int whole_end, whole_first;
-            {
-                const int wrow = it.row0 + tile0 + (warp & 3) * 32, last = it.row0 + tile0 + rows - 1;
-                whole_end = min(it.pos0 + wrow / a.group + 1, a.room);
-                whole_first = a.window > 0 ? it.pos0 + min(wrow + 31, last) / a.group - a.window + 1 : 0;
-            }
+            const int whole_end = min(__shfl_sync(0xffffffffu, pos, 0) + 1, a.room);
+            const int whole_first = a.window > 0 ? __shfl_sync(0xffffffffu, pos, 31) - a.window + 1 : 0;
+            const int end = it.end, first = it.first, kept = it.kept;
             float m = -INFINITY, l = 0.0f;
             bool any = false;                         // a key tile of this slot's went by
             for (int i = two ? 0 : slot; i < steps; i += ahead) {
@@ -649,8 +654,12 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                         const int hi = min(pos + 1, a.room) - key0, sk = min(a.sinks - key0, hi);
                         const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
 #pragma unroll
-                        for (int k = 0; k < kPaTile; ++k)
-                            s[k] = (k < hi && k >= lo) || k < sk ? s[k] : -INFINITY;
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t seen = (ones(hi - 32 * k) & ~ones(lo - 32 * k)) | ones(sk - 32 * k);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[32 * k + e] = seen & (1u << e) ? s[32 * k + e] : -INFINITY;
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < kPaTile; k += 8)
@@ -700,7 +709,6 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 any = true;
                 // value rows that nobody sees: zeros
                 {
-                    const int end = it.end, first = it.first, kept = it.kept;
                     if (key0 + kPaTile > end || (key0 < first && key0 + kPaTile > kept)) {
                         const uint32_t v = at + 2 * i + 1;
                         ok = all_wait(kv_full + 8 * stage_of(v), phase_of(v), 0x420 + slot);
@@ -764,7 +772,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 m = mn;
                 l = l * f0 + l1 * f1;
             }
-            const int c0 = it.c0, c1 = it.c1, h = it.h, qs = it.qs, row0 = it.row0 + tile0;
+            const int c0 = it.c0, c1 = it.c1, h = it.h, token0 = it.qs + t0;
             item_done(n);
             const bool live = row < rows;
             // columns [16 k, 16 k + 16) of the row's O
@@ -789,8 +797,8 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             if (c0 == c1) {
                 // the whole item: the output
                 const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-                const int x = row0 + row, tok = x / a.group, head = h * a.group + x - tok * a.group;
-                const int64_t token = qs + tok;
+                const int tok = row / a.group, head = h * a.group + row - tok * a.group;
+                const int64_t token = token0 + tok;
                 uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1;
                 if (busy) {
 #pragma unroll
@@ -851,38 +859,55 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             if (!(ok = group_sync())) break;
             if (!sh.last[slot]) continue;
             __threadfence();
-            // a thread joins some rows' some columns: its row's parts' maximum,
-            // then their weighted sums
-            const int groups = (rows + 31) / 32;      // of 32 rows
-            for (int e = warp & 3; e < groups * (D / 16); e += 4) {
-                const int r = e % groups * 32 + lane, k0 = e / groups * 4;
-                if (r >= rows) continue;
-                float M = -INFINITY, L = 0.0f, o[16];
+            // a warp joins a quarter of the columns, a lane a row, four parts
+            // at a time, all their loads in flight
+            constexpr int kVec = D / 16;
+            const int k0 = (warp & 3) * kVec;
+            for (int r0 = 0; r0 < rows; r0 += 32) {
+                const int r = min(r0 + lane, rows - 1);
+                float M = -INFINITY, L = 0.0f, o[4 * kVec];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = 0.0f;
-#pragma unroll 4
-                for (int b = c0; b <= c1; ++b) M = fmaxf(M, __ldcg(part(b) + kPaTile * D + r));
-                if (M == -INFINITY) M = 0.0f;
-#pragma unroll 2
-                for (int b = c0; b <= c1; ++b) {
-                    const float *p = part(b);
-                    const float g = pa_ex2((__ldcg(p + kPaTile * D + r) - M) * c);
-                    L += __ldcg(p + kPaTile * D + kPaTile + r) * g;
+                for (int k = 0; k < 4 * kVec; ++k) o[k] = 0.0f;
+                for (int b0 = c0; b0 <= c1; b0 += 4) {
+                    float pm[4], pl[4];
+                    float4 y[4][kVec];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(p + ((k0 + k) * kPaTile + r) * 4));
-                        o[4 * k] += y.x * g;
-                        o[4 * k + 1] += y.y * g;
-                        o[4 * k + 2] += y.z * g;
-                        o[4 * k + 3] += y.w * g;
+                    for (int e = 0; e < 4; ++e) {
+                        const float *p = part(min(b0 + e, c1));
+                        pm[e] = __ldcg(p + kPaTile * D + r);
+                        pl[e] = __ldcg(p + kPaTile * D + kPaTile + r);
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k)
+                            y[e][k] = __ldcg(reinterpret_cast<const float4 *>(p + ((k0 + k) * kPaTile + r) * 4));
+                    }
+                    float mn = M;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mn = fmaxf(mn, pm[e]);
+                    const float f = M == -INFINITY ? 0.0f : pa_ex2((M - mn) * c);
+                    M = mn;
+                    L *= f;
+#pragma unroll
+                    for (int k = 0; k < 4 * kVec; ++k) o[k] *= f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float g = b0 + e > c1 || pm[e] == -INFINITY ? 0.0f : pa_ex2((pm[e] - M) * c);
+                        L += pl[e] * g;
+#pragma unroll
+                        for (int k = 0; k < kVec; ++k) {
+                            o[4 * k] += y[e][k].x * g;
+                            o[4 * k + 1] += y[e][k].y * g;
+                            o[4 * k + 2] += y[e][k].z * g;
+                            o[4 * k + 3] += y[e][k].w * g;
+                        }
                     }
                 }
+                if (r0 + lane >= rows) continue;
                 const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
-                const int x = row0 + r, tok = x / a.group, head = h * a.group + x - tok * a.group;
-                const int64_t token = qs + tok;
+                const int tok = r / a.group, head = h * a.group + r - tok * a.group;
+                const int64_t token = token0 + tok;
                 uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1 + 4 * k0;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
+                for (int i = 0; i < kVec / 2; ++i) {
                     uint32_t v[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -900,17 +925,17 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
 }
 
 template <int D, bool F16>
-static cudaError_t launch_typed(const AttnArgs &a, const CUtensorMap &k, const CUtensorMap &v, int blocks,
+static cudaError_t launch_typed(const AttnArgs &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, int blocks,
                                 cudaStream_t s) {
-    paged_attention_kernel<D, F16><<<blocks, kPaThreads, PaShape<D>::kSmem, s>>>(a, k, v);
+    paged_attention_kernel<D, F16><<<blocks, kPaThreads, PaShape<D>::kSmem, s>>>(a, q, k, v);
     return cudaGetLastError();
 }
 
-cudaError_t launch_paged_attention(const AttnArgs &a, const CUtensorMap &k, const CUtensorMap &v,
+cudaError_t launch_paged_attention(const AttnArgs &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                    int head_dim, bool f16, int blocks, cudaStream_t s) {
     if (head_dim == 64)
-        return f16 ? launch_typed<64, true>(a, k, v, blocks, s) : launch_typed<64, false>(a, k, v, blocks, s);
-    return f16 ? launch_typed<128, true>(a, k, v, blocks, s) : launch_typed<128, false>(a, k, v, blocks, s);
+        return f16 ? launch_typed<64, true>(a, q, k, v, blocks, s) : launch_typed<64, false>(a, q, k, v, blocks, s);
+    return f16 ? launch_typed<128, true>(a, q, k, v, blocks, s) : launch_typed<128, false>(a, q, k, v, blocks, s);
 }
 
 cudaError_t paged_attention_prepare() {

@@ -415,7 +415,7 @@ markov_status markov_chain_sample_sharded(markov_shard_plan *plan, const uint16_
  * results of split rows, counters, the status word).  Calls on one plan must
  * not overlap on the GPU; calls that may overlap need plans of their own. */
 typedef struct markov_paged_desc {
-    int32_t q_heads;      /* a multiple of kv_heads; kv_heads <= q_heads <= 256 */
+    int32_t q_heads;      /* at most 256, a multiple of kv_heads, at most 128 for each */
     int32_t kv_heads;     /* >= 1 */
     int32_t head_dim;     /* 64 or 128 */
     int32_t page_size;    /* a power of two, 8 .. 256 */

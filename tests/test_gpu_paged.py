@@ -534,7 +534,7 @@ def test_refusals(gpu_lib):
     plan.close()
 
 
-@pytest.mark.parametrize("bad", [dict(q_heads=5), dict(q_heads=1), dict(q_heads=258), dict(kv_heads=0),
+@pytest.mark.parametrize("bad", [dict(q_heads=5), dict(q_heads=1), dict(q_heads=258), dict(q_heads=256, kv_heads=1), dict(kv_heads=0),
                                  dict(head_dim=96), dict(page_size=24), dict(page_size=4), dict(page_size=512),
                                  dict(max_rows=0), dict(max_rows=1025), dict(timeout_ms=-1)])
 def test_plan_refusals(gpu_lib, bad):

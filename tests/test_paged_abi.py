@@ -29,7 +29,7 @@ def test_null_plans_are_refused(L):
     L.markov_paged_plan_destroy(None)
 
 
-@pytest.mark.parametrize("bad", [dict(q_heads=5), dict(q_heads=1), dict(q_heads=258), dict(kv_heads=0),
+@pytest.mark.parametrize("bad", [dict(q_heads=5), dict(q_heads=1), dict(q_heads=258), dict(q_heads=256, kv_heads=1), dict(kv_heads=0),
                                  dict(head_dim=96), dict(page_size=24), dict(page_size=4), dict(page_size=512),
                                  dict(max_rows=0), dict(max_rows=1025), dict(dtype=1), dict(dtype=3),
                                  dict(timeout_ms=-1)])
