@@ -56,6 +56,7 @@ struct AttnArgs {
     const int32_t *query_start, *seq_lens;
     int rows, T, q_heads, kv_heads, group;
     int tile_tokens;           // tokens of a row tile: 128 / group
+    int group_inv;             // ceil(2^16 / group): row * group_inv >> 16 is row / group below 128
     float scale2;              // |scale| log2(e), not zero
     int window, sinks;
     uint16_t *out;

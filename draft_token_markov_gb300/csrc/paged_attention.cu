@@ -63,7 +63,7 @@ struct PaShape {
     // tiles, slot 1's m and l, barriers, the schedule
     static constexpr int kExchange = 2 * kQBytes + kStages * kKvBytes;
     static constexpr int kBars = kExchange + 2 * kPaTile * 4;
-    static constexpr int kMisc = kBars + 8 * (2 * kStages + 16 + 2 * kRing);
+    static constexpr int kMisc = kBars + 8 * (2 * kStages + 17 + 2 * kRing);
     static constexpr int kSmem = kMisc + 512;
 };
 
@@ -85,7 +85,7 @@ struct PaReq {
     int state;                 // its table row, -1 for none
 };
 
-__device__ __forceinline__ PaReq pa_request(const AttnArgs &a, int r) {
+__device__ __noinline__ PaReq pa_request(const AttnArgs &a, int r) {
     PaReq q;
     const int64_t s = __ldg(a.idx + r);
     q.qs = __ldg(a.query_start + r);
@@ -98,9 +98,9 @@ __device__ __forceinline__ PaReq pa_request(const AttnArgs &a, int r) {
     return q;
 }
 
-// The units of the m-th pair of row tiles of a request: its key tiles, at
-// least one.
-__device__ __forceinline__ int pa_units(const AttnArgs &a, const PaReq &q, int m, PaItem &it) {
+// The m-th pair of row tiles of a request: its keys and its key tiles (none
+// where nothing is seen; it counts as one unit then).
+__device__ __forceinline__ void pa_span(const AttnArgs &a, const PaReq &q, int m, PaItem &it) {
     it.t0 = m * 2 * a.tile_tokens;
     it.tokens = min(q.np - it.t0, 2 * a.tile_tokens);
     const int p0 = q.pos0 + it.t0, p1 = p0 + it.tokens - 1;
@@ -112,6 +112,11 @@ __device__ __forceinline__ int pa_units(const AttnArgs &a, const PaReq &q, int m
     it.sink_tiles = (it.kept + kPaTile - 1) / kPaTile;
     if (nw > 0 && it.sink_tiles > it.w0) it.sink_tiles = it.w0;
     it.steps = it.sink_tiles + nw;
+}
+
+__device__ __noinline__ int pa_units(const AttnArgs &a, PaReq q, int m) {
+    PaItem it;
+    pa_span(a, q, m, it);
     return max(it.steps, 1);
 }
 
@@ -143,30 +148,21 @@ struct PaSplit {
 
 // ----------------------------------------------------------------- helpers
 
-// Bounded waits: a wait that gives up records the status and raises the
-// block's abort flag, and every role leaves at its next wait.
-struct PaWait {
-    uint64_t timeout_ns;
-    uint32_t *status;
-    volatile uint32_t *abort;
-
-    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, uint32_t where) const {
-        if (tc::mbar_test(bar, parity)) return true;
-        return slow(bar, parity, where);
-    }
-    __device__ __forceinline__ bool slow(uint32_t bar, uint32_t parity, uint32_t where) const {
-        const uint64_t deadline = tc::now_ns() + timeout_ns;
-        while (!tc::mbar_test_sleep(bar, parity)) {
-            if (*abort) return false;
-            if (tc::now_ns() > deadline) {
-                set_status(status, 4u /* MARKOV_ETIMEOUT */, where);
-                *abort = 1u;
-                return false;
-            }
+// The rest of a bounded wait.  One that gives up raises the block's abort
+// flag, at which every role leaves at its next wait; the block records the
+// status as it ends.
+__device__ __forceinline__ bool pa_wait_on(uint32_t bar, uint32_t parity, uint32_t where, uint64_t timeout_ns,
+                                           volatile uint32_t *abort) {
+    const uint64_t deadline = tc::now_ns() + timeout_ns;
+    do {
+        if (*abort) return false;
+        if (tc::now_ns() > deadline) {
+            *abort = where;
+            return false;
         }
-        return true;
-    }
-};
+    } while (!tc::mbar_test_sleep(bar, parity));
+    return true;
+}
 
 // B operand, MN-major, 128-byte swizzle: 64 elements of N contiguous, the
 // next 64 `lbo` bytes on; 8 rows of K 128 bytes apart, the next 8 1024 on.
@@ -181,11 +177,13 @@ __host__ __device__ constexpr uint32_t pa_idesc(uint32_t N, bool mn_major_b) {
            ((N >> 3) << 17) | ((128u >> 4) << 24);
 }
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z,
+// Called by the whole warp; an elected lane issues.
+__device__ __forceinline__ void tma_load_4d_elect(uint32_t dst, const void *tmap, int x, int y, int z,
                                             int w, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-        "%3, %4, %5}], [%6];" ::"r"(dst),
+        "{ .reg .pred p; elect.sync _|p, 0xffffffff;\n"
+        "@p cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3, %4, %5}], [%6]; }" ::"r"(dst),
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
 }
@@ -231,6 +229,38 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         return r;
     }
     return bf16x2_rn(lo, hi);
+}
+
+// Four MMAs, their operands `da` and `db` (in the descriptors' 16-byte units;
+// TMEM columns for an A there) apart.  Called by the whole warp, an elected
+// lane issues.
+__device__ __forceinline__ void mma4_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p, q; .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+        "setp.ne.u32 q, %4, 0; elect.sync _|p, 0xffffffff;\n"
+        "add.s64 a1, %1, 2; add.s64 a2, %1, 4; add.s64 a3, %1, 6;\n"
+        "add.s64 b1, %2, 2; add.s64 b2, %2, 4; add.s64 b3, %2, 6;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n"
+        "setp.eq.u32 q, 0, 0;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma4_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p, q; .reg .b32 a1, a2, a3; .reg .b64 b1, b2, b3;\n"
+        "setp.ne.u32 q, %4, 0; elect.sync _|p, 0xffffffff;\n"
+        "add.s32 a1, %1, 8; add.s32 a2, %1, 16; add.s32 a3, %1, 24;\n"
+        "add.s64 b1, %2, 128; add.s64 b2, %2, 256; add.s64 b3, %2, 384;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n"
+        "setp.eq.u32 q, 0, 0;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // The lowest n bits (none for n <= 0, all from 32 on).
@@ -280,9 +310,9 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t kv_full = tc::smem_u32(base + S::kBars), kv_empty = kv_full + 8 * S::kStages;
     const uint32_t q_full = kv_empty + 8 * S::kStages, q_empty = q_full + 16, s_full = q_full + 32,
-                   p_full = q_full + 48, pv_done = q_full + 64, group = q_full + 80,
-                   merge_full = q_full + 96, merge_free = q_full + 104, leave = q_full + 112,
-                   item_full = q_full + 128, item_empty = item_full + 8 * kRing;
+                   p_full = q_full + 48, pv_done = q_full + 80, group = q_full + 96,
+                   merge_full = q_full + 112, merge_free = q_full + 120, leave = q_full + 128,
+                   item_full = q_full + 136, item_empty = item_full + 8 * kRing;
     if (tid == 0) {
         sh.abort = 0;
         for (int i = 0; i < S::kStages; ++i) {
@@ -293,7 +323,8 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             tc::mbar_init(q_full + 8 * i, 1);
             tc::mbar_init(q_empty + 8 * i, 1);
             tc::mbar_init(s_full + 8 * i, 1);
-            tc::mbar_init(p_full + 8 * i, 4);        // the slot's warps
+            tc::mbar_init(p_full + 16 * i, 4);       // the slot's warps, the halves of P
+            tc::mbar_init(p_full + 16 * i + 8, 4);
             tc::mbar_init(pv_done + 8 * i, 1);
             tc::mbar_init(group + 8 * i, 4);
         }
@@ -318,10 +349,10 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
-    const PaWait wait{a.timeout_ns, a.status, &sh.abort};
     // a wait that some lane gives up is given up by the warp
     auto all_wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
-        return (bool)__all_sync(0xffffffffu, wait(bar, parity, where));
+        if (__all_sync(0xffffffffu, tc::mbar_test(bar, parity))) return true;
+        return (bool)__all_sync(0xffffffffu, pa_wait_on(bar, parity, where, a.timeout_ns, &sh.abort));
     };
     auto arrive = [&](uint32_t bar) {
         __syncwarp();
@@ -342,6 +373,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         int64_t total = 0;
         // the rows' units before and with each, where key tiles will be
         uint32_t *units_to = reinterpret_cast<uint32_t *>(kv_smem);
+#pragma unroll 1
         for (int r0 = 0; r0 < a.rows; r0 += 32) {
             if (r0 > 0) {
                 q.np = 0;
@@ -349,7 +381,8 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             }
             const int pairs = pa_pairs(a, q);
             int64_t x = 0;
-            for (int m = 0; m < pairs; ++m) x += pa_units(a, q, m, it);
+#pragma unroll 1
+            for (int m = 0; m < pairs; ++m) x += pa_units(a, q, m);
             x *= a.kv_heads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -390,24 +423,25 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             h = (u0 - before) / head;
             u = before + h * head;
             for (;; ++m) {
-                const uint32_t units = pa_units(a, q, m, it);
+                const uint32_t units = pa_units(a, q, m);
                 if (u0 - u < units) break;
                 u += units;
             }
             j = u0 - u;
         }
         tc::fence_proxy_async_smem();                // units_to is read; TMA writes come
-        uint32_t q_phase[2] = {0, 0};
+        uint32_t q_phase = 0;                        // a bit a slot
         int q_token = 0, q_head = 0, q_tiles = 0;    // the queries of the item published last
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
             const bool more = u < u_end;
-            const int last_token = q_token, last_head = q_head, last_tiles = q_tiles;
+            int token = q_token, head = q_head, tiles = q_tiles;
             ok = all_wait(item_empty + 8 * (n % kRing), (n / kRing & 1) ^ 1, 0x510);
             if (!ok) break;
             q_tiles = 0;
             if (more) {
-                const int units = pa_units(a, q, m, it);
+                pa_span(a, q, m, it);
+                const int units = max(it.steps, 1);
                 it.qs = q.qs;
                 it.pos0 = q.pos0;
                 it.state = q.state;
@@ -446,30 +480,33 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             arrive(item_full + 8 * (n % kRing));
             // the queries of the item before (of the first at once), so that
             // the loads of keys know of an item ahead
-            auto load = [&](int token, int head, int tiles) {
-                for (int s = 0; ok && s < tiles; ++s) {
-                    ok = all_wait(q_empty + 8 * s, q_phase[s] ^ 1, 0x300 + s);
-                    if (!ok) break;
-                    q_phase[s] ^= 1;
-                    if (lane == 0) {
-                        tc::mbar_expect_tx(q_full + 8 * s, a.tile_tokens * a.group * D * 2);
-                        for (int half = 0; half < S::kHalves; ++half)
-                            tma_load_3d(tc::smem_u32(q_smem) + s * S::kQBytes + half * S::kHalf, &qmap, half * 64,
-                                        head, token + s * a.tile_tokens, q_full + 8 * s);
-                    }
-                    __syncwarp();
+            if (n == 0) {
+                token = q_token;
+                head = q_head;
+                tiles = q_tiles;
+                q_tiles = 0;
+            }
+#pragma unroll 1
+            for (int s = 0; s < tiles; ++s, token += a.tile_tokens) {
+                ok = all_wait(q_empty + 8 * s, (q_phase >> s & 1) ^ 1, 0x300 + s);
+                if (!ok) break;
+                q_phase ^= 1u << s;
+                if (lane == 0) {
+                    tc::mbar_expect_tx(q_full + 8 * s, a.tile_tokens * a.group * D * 2);
+#pragma unroll 1
+                    for (int half = 0; half < S::kHalves; ++half)
+                        tma_load_3d(tc::smem_u32(q_smem) + s * S::kQBytes + half * S::kHalf, &qmap, half * 64, head,
+                                    token, q_full + 8 * s);
                 }
-            };
-            if (n > 1) load(last_token, last_head, last_tiles);
-            if (n == 0) load(q_token, q_head, q_tiles);
-            if (n == 0) q_tiles = 0;
+                __syncwarp();
+            }
             if (!more) break;
         }
         if (lane == 0 && sh.abort) {
             // gave up: no load may be in flight when the block leaves
             const uint64_t until = tc::now_ns() + a.timeout_ns;
             for (int s = 0; s < 2; ++s)
-                while (!tc::mbar_test(q_full + 8 * s, q_phase[s] ^ 1) && tc::now_ns() < until) {}
+                while (!tc::mbar_test(q_full + 8 * s, (q_phase >> s & 1) ^ 1) && tc::now_ns() < until) {}
         }
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------ key / value loads
@@ -497,17 +534,20 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             for (int j = j0; j < j1; ++j, at += 2) {
                 const int pid = next;
                 if (j + 1 < j1) next = page_of(j + 1);
-                const int key = (j < sinks ? j : w0 + j - sinks) * kPaTile + lane * box;
+                const int slot0 = (j < sinks ? j : w0 + j - sinks) * kPaTile & (page - 1);
                 const uint32_t stage = stage_of(at), phase = phase_of(at), full = kv_full + 8 * stage;
                 ok = all_wait(kv_empty + 8 * stage, phase ^ 1, 0x100 + stage);
                 if (!ok) break;
                 if (lane == 0) tc::mbar_expect_tx(full, S::kKvBytes);
                 __syncwarp();
-                if (lane < boxes) {
-                    const uint32_t dst = tc::smem_u32(kv_smem + stage * S::kKvBytes) + lane * box * 128;
+                // the whole warp goes through the boxes, an elected lane issues
+                uint32_t dst = tc::smem_u32(kv_smem + stage * S::kKvBytes);
+#pragma unroll 2
+                for (int b = 0; b < boxes; ++b, dst += box * 128) {
+                    const int id = __shfl_sync(0xffffffffu, pid, b);
 #pragma unroll
                     for (int half = 0; half < S::kHalves; ++half)
-                        tma_load_4d(dst + half * S::kHalf, map, half * 64, key & (page - 1), h, pid, full);
+                        tma_load_4d_elect(dst + half * S::kHalf, map, half * 64, slot0, h, id, full);
                 }
                 filled |= 1u << stage;
                 fill_phase = (fill_phase & ~(1u << stage)) | (phase << stage);
@@ -524,7 +564,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         // ---------------------------------------------------- MMA issue
         // the whole warp, so that control flow and descriptors stay uniform;
         // an elected lane issues
-        uint32_t at = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        uint32_t at = 0, q_phase = 0, p_phase = 0;   // a bit a slot
         bool ok = true;
         const uint32_t q_addr = tc::smem_u32(q_smem), kv_addr = tc::smem_u32(kv_smem);
         constexpr uint32_t kIdescS = pa_idesc<F16>(kPaTile, false), kIdescO = pa_idesc<F16>(D, true);
@@ -532,20 +572,15 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         auto scores = [&](int slot, int q_tile, uint32_t k) {
             const uint32_t q0 = q_addr + q_tile * S::kQBytes, k0 = kv_addr + stage_of(k) * S::kKvBytes;
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                const uint32_t off = (i / 4) * S::kHalf + (i % 4) * 32;
-                tc::mma_smemA_elect(tmem + slot * kPaTile, tc::sw128_desc(q0 + off),
-                                    tc::sw128_desc(k0 + off), kIdescS, i > 0);
-            }
+            for (int i = 0; i < S::kHalves; ++i)
+                mma4_smem(tmem + slot * kPaTile, tc::sw128_desc(q0 + i * S::kHalf),
+                          tc::sw128_desc(k0 + i * S::kHalf), kIdescS, i > 0);
             tc::commit_elect(s_full + 8 * slot);
         };
-        auto values = [&](int slot, uint32_t v, bool accumulate) {
-            const uint32_t v0 = kv_addr + stage_of(v) * S::kKvBytes;
-#pragma unroll
-            for (int i = 0; i < kPaTile / 16; ++i)
-                tc::mma_tmemA_elect(tmem + 2 * kPaTile + slot * D, tmem + slot * kPaTile + i * 8,
-                                    sw128_mn_desc(v0 + i * 2048, S::kHalf), kIdescO, accumulate || i > 0);
-            tc::commit_elect(pv_done + 8 * slot);
+        auto values = [&](int slot, uint32_t v, int half, bool accumulate) {
+            mma4_tmem(tmem + 2 * kPaTile + slot * D, tmem + slot * kPaTile + half * 32,
+                      sw128_mn_desc(kv_addr + stage_of(v) * S::kKvBytes + half * 4 * 2048, S::kHalf), kIdescO,
+                      accumulate);
         };
         auto release = [&](uint32_t k) { tc::commit_elect(kv_empty + 8 * stage_of(k)); };
         for (uint32_t n = 0; ok; ++n) {
@@ -556,13 +591,14 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             if (steps <= 0) continue;                // nothing seen: the output is written without MMAs
             const bool two = tokens > a.tile_tokens; // row tiles
             // the first scores
+#pragma unroll 1
             for (int s = 0; ok && s < 2; ++s) {
                 if (!two && s == steps) break;
                 const uint32_t k = at + (two ? 0 : 2 * s);
                 ok = loaded(k);
                 if (ok && (two || s == 0)) {
-                    ok = all_wait(q_full + 8 * s, q_phase[s], 0x210 + s);
-                    q_phase[s] ^= 1;
+                    ok = all_wait(q_full + 8 * s, q_phase >> s & 1, 0x210 + s);
+                    q_phase ^= 1u << s;
                 }
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -570,15 +606,23 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 if (!two || s == 1) release(k);
                 if (two ? steps == 1 : s + 1 == min(steps, 2) && steps <= 2) tc::commit_elect(q_empty + (two ? 8 * s : 0));
             }
+#pragma unroll 1
             for (int j = 0; ok && j < steps; ++j) {
                 const uint32_t v = at + 2 * j + 1;
                 const int ahead = two ? 1 : 2;       // key tiles to the slot's next scores
+#pragma unroll 1
                 for (int s = two ? 0 : j & 1, e = two ? 2 : s + 1; ok && s < e; ++s) {
-                    ok = all_wait(p_full + 8 * s, p_phase[s], 0x220 + s) && loaded(v);
+                    ok = loaded(v);
+#pragma unroll 1
+                    for (int half = 0; ok && half < 2; ++half) {
+                        ok = all_wait(p_full + 16 * s + 8 * half, p_phase >> s & 1, 0x220 + s);
+                        if (!ok) break;
+                        tc::fence_after_sync();
+                        values(s, v, half, j >= ahead || half > 0);
+                    }
                     if (!ok) break;
-                    p_phase[s] ^= 1;
-                    tc::fence_after_sync();
-                    values(s, v, j >= ahead);
+                    p_phase ^= 1u << s;
+                    tc::commit_elect(pv_done + 8 * s);
                     if (s == e - 1) release(v);
                     if (j + ahead < steps) {
                         const uint32_t k = at + 2 * (j + ahead);
@@ -622,7 +666,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             const int t0 = it.t0 + (two ? slot * a.tile_tokens : 0);
             const int rows = min(it.tokens + it.t0 - t0, a.tile_tokens) * a.group;
             const int steps = it.steps, ahead = two ? 1 : 2;
-            const int pos = it.pos0 + t0 + row / a.group;
+            const int tok = row * a.group_inv >> 16, pos = it.pos0 + t0 + tok;
             const bool busy = (warp & 3) * 32 < rows;
             // a tile is seen whole by the warp's rows when its last key is
             // not past the first one's and its first within the last one's window
@@ -641,25 +685,57 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 if (!ok) break;
                 s_phase ^= 1;
                 tc::fence_after_sync();
+                // value rows that nobody sees: zeros
+                if (key0 + kPaTile > end || (key0 < first && key0 + kPaTile > kept)) {
+                    const uint32_t v = at + 2 * i + 1;
+                    ok = all_wait(kv_full + 8 * stage_of(v), phase_of(v), 0x420 + slot);
+                    if (!ok) break;
+                    const int key = key0 + row;
+                    if (key >= end || (key < first && key >= kept)) {
+                        const uint32_t dst = tc::smem_u32(kv_smem) + stage_of(v) * S::kKvBytes + row * 128;
+#pragma unroll 2
+                        for (int k = 0; k < 8 * S::kHalves; ++k)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             dst + (k >> 3) * S::kHalf + 16 * (k & 7)),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                    tc::fence_proxy_async_smem();
+                }
+                if (owed) {                           // before this slot's O is written again
+                    ok = all_wait(merge_free, merge_phase, 0x460);
+                    if (!ok) break;
+                    merge_phase ^= 1;
+                    owed = false;
+                }
                 if (busy) {
-                    float s[kPaTile], top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    float s[kPaTile];
+                    if (key0 + kPaTile > whole_end || (key0 < whole_first && key0 + kPaTile > a.sinks)) {
+                        // hidden scores to -inf where they lie (a loop of few
+                        // instructions; in registers it would be 128 selects)
+                        const int hi = min(pos + 1, a.room) - key0, sk = min(a.sinks - key0, hi);
+                        const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
+#pragma unroll 1
+                        for (int k = 0; k < kPaTile; k += 16) {
+                            const uint32_t seen = (ones(hi - k) & ~ones(lo - k)) | ones(sk - k);
+                            if (__all_sync(0xffffffffu, (seen & 0xffffu) == 0xffffu)) continue;
+                            uint32_t x[16];
+                            tc::ld_32x32b_x16(t_s + k, x);
+                            tc::wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (!(seen & (1u << e))) x[e] = a.negate ? 0x7f800000u : 0xff800000u;
+                            tc::st_32x32b_x16(t_s + k, x);
+                        }
+                        tc::wait_st();
+                    }
+                    float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) ld_32x32b_x32(t_s + 32 * k, s + 32 * k);
                     tc::wait_ld();
                     if (a.negate) {
 #pragma unroll
                         for (int k = 0; k < kPaTile; ++k) s[k] = -s[k];
-                    }
-                    if (key0 + kPaTile > whole_end || (key0 < whole_first && key0 + kPaTile > a.sinks)) {
-                        const int hi = min(pos + 1, a.room) - key0, sk = min(a.sinks - key0, hi);
-                        const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t seen = (ones(hi - 32 * k) & ~ones(lo - 32 * k)) | ones(sk - 32 * k);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                s[32 * k + e] = seen & (1u << e) ? s[32 * k + e] : -INFINITY;
-                        }
                     }
 #pragma unroll
                     for (int k = 0; k < kPaTile; k += 8)
@@ -675,7 +751,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                         if (any) {
                             // the last PV is done: S's commit came after it
                             l *= f;
-#pragma unroll
+#pragma unroll 1
                             for (int k = 0; k < D / 16; ++k) {
                                 uint32_t o[16];
                                 tc::ld_32x32b_x16(t_o + 16 * k, o);
@@ -701,41 +777,22 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                             p[e] = pack2<F16>(p0, p1);
                         }
                         tc::st_32x32b_x16(t_s + 16 * k, p);
+                        if (k == 1) {                 // half of P: its MMAs may start
+                            tc::wait_st();
+                            tc::fence_before_sync();
+                            arrive(p_full + 16 * slot);
+                        }
                     }
                     float s0, s1;
                     split2(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;
+                    tc::wait_st();
+                } else {
+                    arrive(p_full + 16 * slot);
                 }
                 any = true;
-                // value rows that nobody sees: zeros
-                {
-                    if (key0 + kPaTile > end || (key0 < first && key0 + kPaTile > kept)) {
-                        const uint32_t v = at + 2 * i + 1;
-                        ok = all_wait(kv_full + 8 * stage_of(v), phase_of(v), 0x420 + slot);
-                        if (!ok) break;
-                        const int key = key0 + row;
-                        if (key >= end || (key < first && key >= kept)) {
-                            const uint32_t dst = tc::smem_u32(kv_smem) + stage_of(v) * S::kKvBytes + row * 128;
-#pragma unroll
-                            for (int half = 0; half < S::kHalves; ++half)
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + half * S::kHalf + 16 * k),
-                                                 "r"(0)
-                                                 : "memory");
-                        }
-                        tc::fence_proxy_async_smem();
-                    }
-                }
-                if (busy) tc::wait_st();
-                if (owed) {                           // before this slot's O is written again
-                    ok = all_wait(merge_free, merge_phase, 0x460);
-                    if (!ok) break;
-                    merge_phase ^= 1;
-                    owed = false;
-                }
                 tc::fence_before_sync();
-                arrive(p_full + 8 * slot);
+                arrive(p_full + 16 * slot + 8);
                 pv_phase ^= 1;                        // one more PV to come
             }
             if (!ok) break;
@@ -775,80 +832,94 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             const int c0 = it.c0, c1 = it.c1, h = it.h, token0 = it.qs + t0;
             item_done(n);
             const bool live = row < rows;
-            // columns [16 k, 16 k + 16) of the row's O
-            auto columns = [&](int k, float (&o)[16]) {
-                uint32_t u[16];
-                if (any) {
-                    tc::ld_32x32b_x16(t_o + 16 * k, u);
-                    tc::wait_ld();
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = any ? __uint_as_float(u[e]) * f0 : 0.0f;
-                if (merge) {
-                    tc::ld_32x32b_x16(t_o + D + 16 * k, u);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) o[e] += __uint_as_float(u[e]) * f1;
-                }
-            };
             auto log_sum = [&](float m, float l) {
                 return l == 0.0f ? -INFINITY : (m * c - kShift + __log2f(l)) * 0.69314718055994531f;
             };
-            if (c0 == c1) {
-                // the whole item: the output
-                const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-                const int tok = row / a.group, head = h * a.group + row - tok * a.group;
-                const int64_t token = token0 + tok;
-                uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1;
-                if (busy) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        float o[16];
-                        columns(k, o);
-                        if (live) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                uint32_t v[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    v[e] = l == 0.0f ? 0u : pack2<F16>(o[8 * i + 2 * e] * inv, o[8 * i + 2 * e + 1] * inv);
-                                *reinterpret_cast<uint4 *>(out + 16 * k + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
-                            }
-                        }
-                    }
-                }
-                if (live && a.lse) a.lse[token * a.q_heads + head] = log_sum(m, l);
-                // O is read: the next item's values may come (its P arrives after this)
-                tc::fence_before_sync();
-                if (merge) arrive(merge_free);
-                continue;
-            }
-            // a part, unnormalised, for the block that comes last: [D / 4][128 rows]
-            // vectors of four columns, then m and l, so that a warp writes and
-            // reads rows side by side
+            // a part lies as [D / 4][128 rows] vectors of four columns, then m
+            // and l, so that a warp writes and reads rows side by side
             auto part = [&](int block) {              // the item's first block has it as its last
                 return a.parts + ((int64_t)(block * 2 + (block == c0 ? 1 : 0)) * 2 + slot) * kPaTile * (D + 2);
             };
+            const bool split = c0 != c1;
+            if (!split) {                             // the whole item: the output
+                const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                f0 *= inv;
+                f1 *= inv;
+            }
+            const int64_t token = token0 + tok;
+            const int head = h * a.group + row - tok * a.group;
+            uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1;
             if (busy) {
-                float *dst = part(blockIdx.x);
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    float o[32];
+                    if (any) {
+                        ld_32x32b_x32(t_o + k, o);
+                        tc::wait_ld();
+                    }
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    float o[16];
-                    columns(k, o);
-                    if (live) {
+                    for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * f0 : 0.0f;
+                    if (merge) {
+                        float x[32];
+                        ld_32x32b_x32(t_o + D + k, x);
+                        tc::wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<float4 *>(dst + ((4 * k + i) * kPaTile + row) * 4) =
-                                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        for (int e = 0; e < 32; ++e) o[e] += x[e] * f1;
+                    }
+                    if (split) {
+                        float *dst = part(blockIdx.x) + (k / 4 * kPaTile + row) * 4;
+                        if (live) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<float4 *>(dst + e * kPaTile * 4) =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                        continue;
+                    }
+                    // 4 x 4 transposition of 16-byte pieces over four lanes: a
+                    // lane then has the same piece of four rows, and a store
+                    // writes 64 bytes of each of eight rows (a row a lane, 16
+                    // bytes each, measured 11 us an item)
+                    uint32_t w[4][4];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e / 4][e % 4] = l == 0.0f ? 0u : pack2<F16>(o[2 * e], o[2 * e + 1]);
+#pragma unroll
+                    for (int b = 1; b < 4; b <<= 1) {
+                        const bool upper = lane & b;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (e & b) continue;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t send = upper ? w[e][i] : w[e | b][i];
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, send, b);
+                                if (upper) w[e][i] = got; else w[e | b][i] = got;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint64_t to = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), (lane & 28) + e);
+                        if ((row & 124) + e < rows)
+                            *reinterpret_cast<uint4 *>(to + (k + (lane & 3) * 8) * 2) =
+                                make_uint4(w[e][0], w[e][1], w[e][2], w[e][3]);
                     }
                 }
-                if (live) {
-                    dst[kPaTile * D + row] = m;
-                    dst[kPaTile * D + kPaTile + row] = l;
-                }
             }
+            // O is read: the next item's values may come (its P arrives after this)
             tc::fence_before_sync();
             if (merge) arrive(merge_free);
+            if (!split) {
+                if (live && a.lse) a.lse[token * a.q_heads + head] = log_sum(m, l);
+                continue;
+            }
+            // unnormalised, for the block that comes last
+            if (live) {
+                float *dst = part(blockIdx.x) + kPaTile * D + row;
+                dst[0] = m;
+                dst[kPaTile] = l;
+            }
             __threadfence();
             if (!(ok = group_sync())) break;
             if (row == 0) {
@@ -863,11 +934,13 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             // at a time, all their loads in flight
             constexpr int kVec = D / 16;
             const int k0 = (warp & 3) * kVec;
+#pragma unroll 1
             for (int r0 = 0; r0 < rows; r0 += 32) {
                 const int r = min(r0 + lane, rows - 1);
                 float M = -INFINITY, L = 0.0f, o[4 * kVec];
 #pragma unroll
                 for (int k = 0; k < 4 * kVec; ++k) o[k] = 0.0f;
+#pragma unroll 1
                 for (int b0 = c0; b0 <= c1; b0 += 4) {
                     float pm[4], pl[4];
                     float4 y[4][kVec];
@@ -903,7 +976,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 }
                 if (r0 + lane >= rows) continue;
                 const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
-                const int tok = r / a.group, head = h * a.group + r - tok * a.group;
+                const int tok = r * a.group_inv >> 16, head = h * a.group + r - tok * a.group;
                 const int64_t token = token0 + tok;
                 uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1 + 4 * k0;
 #pragma unroll
@@ -921,6 +994,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
+    if (tid == 0 && sh.abort) set_status(a.status, 4u /* MARKOV_ETIMEOUT */, sh.abort);
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
