@@ -153,14 +153,20 @@ struct PaSplit {
 // status as it ends.
 __device__ __forceinline__ bool pa_wait_on(uint32_t bar, uint32_t parity, uint32_t where, uint64_t timeout_ns,
                                            volatile uint32_t *abort) {
-    const uint64_t deadline = tc::now_ns() + timeout_ns;
-    do {
+    // a test sleeps for some microseconds at most; the timer, whose reading
+    // costs hundreds of cycles, is looked at every 16th time
+    uint64_t deadline = 0;
+    for (uint32_t i = 1; !tc::mbar_test_sleep(bar, parity); ++i) {
         if (*abort) return false;
-        if (tc::now_ns() > deadline) {
-            *abort = where;
-            return false;
+        if (i % 16 == 0) {
+            const uint64_t now = tc::now_ns();
+            if (deadline == 0) deadline = now + timeout_ns;
+            if (now > deadline) {
+                *abort = where;
+                return false;
+            }
         }
-    } while (!tc::mbar_test_sleep(bar, parity));
+    }
     return true;
 }
 
