@@ -63,7 +63,7 @@ struct AttnArgs {
     int64_t out_s0, out_s1;
     float *lse;
     float *parts;              // split items' parts: [blocks][2][2 tiles][128 (D + 2)]
-    uint32_t *arrivals;        // [blocks][2 tiles]: parts that are there; zero between calls
+    void *joins;               // [blocks]: the item that begins in a block and goes on
     uint32_t *status;
     uint64_t timeout_ns;
 };
@@ -99,6 +99,7 @@ cudaError_t launch_paged_layout(const LayoutArgs &a, cudaStream_t s);
 cudaError_t launch_paged_write(const WriteArgs &a, cudaStream_t s);
 cudaError_t paged_attention_prepare();
 size_t paged_attention_parts(int head_dim, int blocks);
+size_t paged_attention_joins(int blocks);
 cudaError_t launch_paged_attention(const AttnArgs &a, const CUtensorMap &q, const CUtensorMap &k,
                                    const CUtensorMap &v,
                                    int head_dim, bool f16, int blocks, cudaStream_t s);

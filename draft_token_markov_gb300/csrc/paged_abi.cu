@@ -16,20 +16,20 @@ struct markov_paged_plan {
     int sm_count = 0;
     int page_shift = 0;
     int blocks = 0;               // of an attention launch: one a multiprocessor
-    uint32_t *ctrl = nullptr;     // [0..1] status, where; [2] the layout's arrivals;
-                                  // from kArrivals on the attention's, 2 a block
-    size_t ctrl_n = 0;
+    uint32_t *ctrl = nullptr;     // [0..1] status, where; [2] the layout's arrivals
     float *parts = nullptr;       // split attention rows
+    void *joins = nullptr;        // which they are
 };
 
 namespace {
 
-constexpr size_t kArrivals = 8;
+constexpr size_t kCtrlWords = 8;
 
 void free_plan(markov_paged_plan *p) {
     if (!p) return;
     if (p->ctrl) cudaFree(p->ctrl);
     if (p->parts) cudaFree(p->parts);
+    if (p->joins) cudaFree(p->joins);
     delete p;
 }
 
@@ -120,11 +120,11 @@ markov_status markov_paged_plan_create(const markov_paged_desc *desc, markov_pag
     p->sm_count = prop.multiProcessorCount;
     while ((1 << p->page_shift) < d.page_size) ++p->page_shift;
     p->blocks = p->sm_count;
-    p->ctrl_n = kArrivals + 2 * p->blocks;
     if (paged_attention_prepare() != cudaSuccess ||
-        cudaMalloc(&p->ctrl, p->ctrl_n * sizeof(uint32_t)) != cudaSuccess ||
+        cudaMalloc(&p->ctrl, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
         cudaMalloc(&p->parts, paged_attention_parts(d.head_dim, p->blocks) * sizeof(float)) != cudaSuccess ||
-        cudaMemset(p->ctrl, 0, p->ctrl_n * sizeof(uint32_t)) != cudaSuccess ||
+        cudaMalloc(&p->joins, paged_attention_joins(p->blocks)) != cudaSuccess ||
+        cudaMemset(p->ctrl, 0, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         cudaGetLastError();
         free_plan(p);
@@ -153,7 +153,7 @@ markov_status markov_paged_plan_status(markov_paged_plan *p) {
     }
     if (ctrl[0] == 0u) return MARKOV_OK;
     // a kernel gave up: clear the status and every counter it may have left
-    if (cudaMemset(p->ctrl, 0, p->ctrl_n * sizeof(uint32_t)) != cudaSuccess ||
+    if (cudaMemset(p->ctrl, 0, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         cudaGetLastError();
         return MARKOV_ECUDA;
@@ -312,7 +312,7 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     a.out_s1 = out_s1;
     a.lse = lse;
     a.parts = p->parts;
-    a.arrivals = p->ctrl + kArrivals;
+    a.joins = p->joins;
     a.status = p->ctrl;
     a.timeout_ns = (uint64_t)p->d.timeout_ms * 1000000ull;
     if (launch_paged_attention(a, qmap, kmap, vmap, p->d.head_dim, p->d.dtype == MARKOV_F16, p->blocks,

@@ -21,13 +21,17 @@
 // and its odd ones in slot 1, and the two are joined at its end (O of both
 // slots lies in the same TMEM lanes).
 //
-// Work.  A unit is one key tile of an item.  The units of the call, in order
-// of request, key head, tile of rows and keys, are cut into one contiguous
-// range a block, whatever the lengths, so every block streams the same number
-// of tiles; a warp of every block finds its range from the lengths by itself
-// (a scan over the rows).  An item cut between blocks leaves its parts, O, m and l in
-// fp32, in the plan's scratch, and the block that finishes last joins them in
-// the order of the keys.
+// Work.  An item weighs kWeight and one for each of its key tiles, two where
+// it has two row tiles (a slot's turn then does one of them, not half of both).
+// The items of the call, in order of request, key head and rows, lie end to
+// end, and the whole is cut into one range of equal weight a block, whatever
+// the lengths; a key tile belongs to the block that its last unit falls to.  A
+// warp of every block finds its range from the lengths by itself (a scan over
+// the rows).  An item cut between blocks leaves its parts, O, m and l in fp32,
+// in the plan's scratch; a second launch, a programmatic dependent of the
+// first, joins them in the order of the keys.  (Joined by the block that
+// finished last instead, with its 128 threads' loads, a part of 72 rows took
+// 3 to 5 us at the call's end.)
 //
 // Roles.  Warps 0-3 and 4-7: softmax and output of the two slots, a thread a
 // row; warp 8 issues MMAs; warps 9 and 10 load key and value tiles by TMA, a
@@ -52,6 +56,7 @@ constexpr int kPaThreads = 384;
 constexpr int kRing = 4;                     // items that are known ahead
 constexpr int kPaTile = 128;                 // keys of a tile, and rows
 constexpr float kLazy = 8.0f;
+constexpr int kWeight = 4;                   // an item's start and end, in single key tiles
 
 template <int D>
 struct PaShape {
@@ -63,7 +68,7 @@ struct PaShape {
     // tiles, slot 1's m and l, barriers, the schedule
     static constexpr int kExchange = 2 * kQBytes + kStages * kKvBytes;
     static constexpr int kBars = kExchange + 2 * kPaTile * 4;
-    static constexpr int kMisc = kBars + 8 * (2 * kStages + 17 + 2 * kRing);
+    static constexpr int kMisc = kBars + 8 * (2 * kStages + 15 + 2 * kRing);
     static constexpr int kSmem = kMisc + 512;
 };
 
@@ -114,10 +119,21 @@ __device__ __forceinline__ void pa_span(const AttnArgs &a, const PaReq &q, int m
     it.steps = it.sink_tiles + nw;
 }
 
-__device__ __noinline__ int pa_units(const AttnArgs &a, PaReq q, int m) {
+// An item's weight, and how many of its key tiles begin before an offset.
+__device__ __forceinline__ int pa_tile_weight(const AttnArgs &a, const PaItem &it) {
+    return it.tokens > a.tile_tokens ? 2 : 1;
+}
+__device__ __forceinline__ uint32_t pa_weight(const AttnArgs &a, const PaItem &it) {
+    return kWeight + max(it.steps, 1) * pa_tile_weight(a, it);
+}
+__device__ __forceinline__ int pa_tile_at(const AttnArgs &a, const PaItem &it, uint32_t off) {
+    if (off <= kWeight) return 0;
+    return min((int)(off - kWeight) / pa_tile_weight(a, it), max(it.steps, 1));
+}
+__device__ __noinline__ uint32_t pa_units(const AttnArgs &a, PaReq q, int m) {
     PaItem it;
     pa_span(a, q, m, it);
-    return max(it.steps, 1);
+    return pa_weight(a, it);
 }
 
 __device__ __forceinline__ int pa_pairs(const AttnArgs &a, const PaReq &q) {
@@ -126,7 +142,7 @@ __device__ __forceinline__ int pa_pairs(const AttnArgs &a, const PaReq &q) {
 
 // What the block's warps share, in shared memory.
 struct PaShared {
-    uint32_t abort, tmem, last[2];
+    uint32_t abort, tmem;
     PaItem ring[kRing];
 };
 
@@ -135,7 +151,7 @@ struct PaSplit {
     uint32_t blocks, base, rem;
 
     __device__ __forceinline__ void cut(uint32_t total, uint32_t grid) {
-        blocks = min(grid, total);
+        blocks = min(grid, total / 2);               // a range holds a tile of either weight
         base = blocks ? total / blocks : 0;
         rem = total - base * blocks;
     }
@@ -300,6 +316,31 @@ __device__ __forceinline__ float pa_ex2(float x) {
     return y;
 }
 
+// An item's part from a block, for one slot: [D / 4][128 rows] vectors of
+// four columns, then m and l, so that a warp writes and reads rows side by
+// side.  A block has two at most: its last item's if that goes on in the next
+// block, and its first one's if that began in one before.
+template <int D>
+__device__ __forceinline__ float *pa_part(const AttnArgs &a, int block, bool begins, int slot) {
+    return a.parts + ((int64_t)(block * 2 + (begins ? 1 : 0)) * 2 + slot) * kPaTile * (D + 2);
+}
+
+// What the joining launch has to know of the item that begins in a block and
+// goes on in the next (c0 == c1: none).
+struct PaJoin {
+    int c0, c1;
+    int token, tokens, head;   // its first token, its tokens, its first query head
+};
+
+template <bool F16>
+__device__ __forceinline__ constexpr float pa_shift() { return F16 ? 7.0f : 0.0f; }
+
+// m c + log2 l, less the weights' shift, as a natural logarithm.
+template <bool F16>
+__device__ __forceinline__ float pa_lse(float m, float l, float c) {
+    return l == 0.0f ? -INFINITY : (m * c - pa_shift<F16>() + __log2f(l)) * 0.69314718055994531f;
+}
+
 // ------------------------------------------------------------------ kernel
 
 template <int D, bool F16>
@@ -308,6 +349,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                        const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
     using S = PaShape<D>;
     extern __shared__ __align__(1024) uint8_t base[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     uint8_t *q_smem = base, *kv_smem = base + 2 * S::kQBytes;
     float *exchange = reinterpret_cast<float *>(base + S::kExchange);
     PaShared &sh = *reinterpret_cast<PaShared *>(base + S::kMisc);
@@ -316,9 +358,9 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t kv_full = tc::smem_u32(base + S::kBars), kv_empty = kv_full + 8 * S::kStages;
     const uint32_t q_full = kv_empty + 8 * S::kStages, q_empty = q_full + 16, s_full = q_full + 32,
-                   p_full = q_full + 48, pv_done = q_full + 80, group = q_full + 96,
-                   merge_full = q_full + 112, merge_free = q_full + 120, leave = q_full + 128,
-                   item_full = q_full + 136, item_empty = item_full + 8 * kRing;
+                   p_full = q_full + 48, pv_done = q_full + 80,
+                   merge_full = q_full + 96, merge_free = q_full + 104, leave = q_full + 112,
+                   item_full = q_full + 120, item_empty = item_full + 8 * kRing;
     if (tid == 0) {
         sh.abort = 0;
         for (int i = 0; i < S::kStages; ++i) {
@@ -332,7 +374,6 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             tc::mbar_init(p_full + 16 * i, 4);       // the slot's warps, the halves of P
             tc::mbar_init(p_full + 16 * i + 8, 4);
             tc::mbar_init(pv_done + 8 * i, 1);
-            tc::mbar_init(group + 8 * i, 4);
         }
         tc::mbar_init(merge_full, 4);                // slot 1's warps
         tc::mbar_init(merge_free, 4);                // slot 0's
@@ -347,8 +388,12 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     PaReq q{0, 0, 0, 0};
     uint32_t pending = 0;
     if (warp == 11) {
-        pending = ld_acquire_u32(a.status);          // a pending status: nothing is done
+        pending = __ldcg(a.status);                  // a pending status: nothing is done
         if (lane < a.rows) q = pa_request(a, lane);
+    }
+    if (warp >= 9 && lane == 0) {
+        const CUtensorMap *map = warp == 9 ? &kmap : warp == 10 ? &vmap : &qmap;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     }
     if (warp == 8) tc::tmem_alloc(tc::smem_u32(&sh.tmem), 512);
     tc::fence_before_sync();
@@ -405,10 +450,10 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         }
         PaSplit split;
         split.cut(pending ? 0u : (uint32_t)total, gridDim.x);
-        uint32_t u = 0, u_end = 0;                   // the current item's first unit, the range's end
-        int r = 0, h = 0, m = 0, j = 0, pairs = 0;
+        uint32_t u = 0, u_begin = 0, u_end = 0;      // the current item's first unit, the range
+        int r = 0, h = 0, m = 0, pairs = 0;
         if (blockIdx.x < split.blocks) {
-            const uint32_t u0 = split.first(blockIdx.x);
+            const uint32_t u0 = u_begin = split.first(blockIdx.x);
             u_end = split.first(blockIdx.x + 1);
             for (int r0 = 0;; r0 += 32) {
                 const int x = r0 + lane;
@@ -433,40 +478,43 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 if (u0 - u < units) break;
                 u += units;
             }
-            j = u0 - u;
         }
         tc::fence_proxy_async_smem();                // units_to is read; TMA writes come
         uint32_t q_phase = 0;                        // a bit a slot
+        PaJoin join{0, 0, 0, 0, 0};
         int q_token = 0, q_head = 0, q_tiles = 0;    // the queries of the item published last
         bool ok = true;
         for (uint32_t n = 0; ok; ++n) {
-            const bool more = u < u_end;
             int token = q_token, head = q_head, tiles = q_tiles;
             ok = all_wait(item_empty + 8 * (n % kRing), (n / kRing & 1) ^ 1, 0x510);
             if (!ok) break;
             q_tiles = 0;
-            if (more) {
+            bool more = false;
+            while (!more && u < u_end) {
                 pa_span(a, q, m, it);
-                const int units = max(it.steps, 1);
-                it.qs = q.qs;
-                it.pos0 = q.pos0;
-                it.state = q.state;
-                it.h = h;
-                it.j0 = j;
-                const int j1 = (int)min((uint32_t)units, u_end - u);
-                it.c0 = it.c1 = blockIdx.x;
-                if (j > 0 || j1 < units) {
-                    it.c0 = split.block_of(u);
-                    it.c1 = split.block_of(u + units - 1);
-                }
-                it.steps = min(j1, it.steps) - j;    // 0 where nothing is seen
-                if (it.steps > 0) {
-                    q_token = q.qs + it.t0;
-                    q_head = h * a.group;
-                    q_tiles = it.tokens > a.tile_tokens ? 2 : 1;
+                const uint32_t units = pa_weight(a, it), weight = pa_tile_weight(a, it);
+                const int all = max(it.steps, 1);
+                it.j0 = u_begin > u ? pa_tile_at(a, it, u_begin - u) : 0;
+                const int j1 = u_end - u < units ? pa_tile_at(a, it, u_end - u) : all;
+                more = it.j0 < j1;                   // not a tile of it: another block's
+                if (more) {
+                    it.qs = q.qs;
+                    it.pos0 = q.pos0;
+                    it.state = q.state;
+                    it.h = h;
+                    it.c0 = it.c1 = blockIdx.x;
+                    if (it.j0 > 0 || j1 < all) {
+                        it.c0 = split.block_of(u + kWeight + weight - 1);
+                        it.c1 = split.block_of(u + units - 1);
+                    }
+                    it.steps = min(j1, it.steps) - it.j0;    // 0 where nothing is seen
+                    if (it.steps > 0) {
+                        q_token = q.qs + it.t0;
+                        q_head = h * a.group;
+                        q_tiles = weight;
+                    }
                 }
                 u += units;
-                j = 0;
                 if (++m == pairs) {
                     m = 0;
                     if (++h == a.kv_heads) {
@@ -479,9 +527,10 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                         }
                     }
                 }
-            } else {
-                it.tokens = 0;
             }
+            if (!more) it.tokens = 0;
+            if (more && it.c0 != it.c1 && it.c0 == (int)blockIdx.x)
+                join = PaJoin{it.c0, it.c1, it.qs + it.t0, it.tokens, it.h * a.group};
             if (lane == 0) sh.ring[n % kRing] = it;
             arrive(item_full + 8 * (n % kRing));
             // the queries of the item before (of the first at once), so that
@@ -508,6 +557,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             }
             if (!more) break;
         }
+        if (lane == 0) reinterpret_cast<PaJoin *>(a.joins)[blockIdx.x] = join;
         if (lane == 0 && sh.abort) {
             // gave up: no load may be in flight when the block leaves
             const uint64_t until = tc::now_ns() + a.timeout_ns;
@@ -655,15 +705,9 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // TMEM lane of the warp
         const uint32_t t_s = tmem + slot * kPaTile + lanes, t_o = tmem + 2 * kPaTile + slot * D + lanes;
         const float c = a.scale2;
-        constexpr float kShift = F16 ? 7.0f : 0.0f;   // fp16 weights: up to 2^15, small ones stay normal
-        uint32_t s_phase = 0, pv_phase = 0, group_phase = 0, merge_phase = 0, at = 0;
+        constexpr float kShift = pa_shift<F16>();     // fp16 weights: up to 2^15, small ones stay normal
+        uint32_t s_phase = 0, pv_phase = 0, merge_phase = 0, at = 0;
         bool ok = true, owed = false;                 // owed: slot 0 may not have read what slot 1 left
-        auto group_sync = [&]() {
-            arrive(group + 8 * slot);
-            const bool r = all_wait(group + 8 * slot, group_phase, 0x450);
-            group_phase ^= 1;
-            return r;
-        };
         for (uint32_t n = 0; ok; ++n) {
             ok = item_wait(n);
             const volatile PaItem &it = item(n);
@@ -716,25 +760,6 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 }
                 if (busy) {
                     float s[kPaTile];
-                    if (key0 + kPaTile > whole_end || (key0 < whole_first && key0 + kPaTile > a.sinks)) {
-                        // hidden scores to -inf where they lie (a loop of few
-                        // instructions; in registers it would be 128 selects)
-                        const int hi = min(pos + 1, a.room) - key0, sk = min(a.sinks - key0, hi);
-                        const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
-#pragma unroll 1
-                        for (int k = 0; k < kPaTile; k += 16) {
-                            const uint32_t seen = (ones(hi - k) & ~ones(lo - k)) | ones(sk - k);
-                            if (__all_sync(0xffffffffu, (seen & 0xffffu) == 0xffffu)) continue;
-                            uint32_t x[16];
-                            tc::ld_32x32b_x16(t_s + k, x);
-                            tc::wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (!(seen & (1u << e))) x[e] = a.negate ? 0x7f800000u : 0xff800000u;
-                            tc::st_32x32b_x16(t_s + k, x);
-                        }
-                        tc::wait_st();
-                    }
                     float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) ld_32x32b_x32(t_s + 32 * k, s + 32 * k);
@@ -742,6 +767,17 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     if (a.negate) {
 #pragma unroll
                         for (int k = 0; k < kPaTile; ++k) s[k] = -s[k];
+                    }
+                    if (key0 + kPaTile > whole_end || (key0 < whole_first && key0 + kPaTile > a.sinks)) {
+                        const int hi = min(pos + 1, a.room) - key0, sk = min(a.sinks - key0, hi);
+                        const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t seen = (ones(hi - 32 * k) & ~ones(lo - 32 * k)) | ones(sk - 32 * k);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                s[32 * k + e] = seen & (1u << e) ? s[32 * k + e] : -INFINITY;
+                        }
                     }
 #pragma unroll
                     for (int k = 0; k < kPaTile; k += 8)
@@ -838,15 +874,8 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             const int c0 = it.c0, c1 = it.c1, h = it.h, token0 = it.qs + t0;
             item_done(n);
             const bool live = row < rows;
-            auto log_sum = [&](float m, float l) {
-                return l == 0.0f ? -INFINITY : (m * c - kShift + __log2f(l)) * 0.69314718055994531f;
-            };
-            // a part lies as [D / 4][128 rows] vectors of four columns, then m
-            // and l, so that a warp writes and reads rows side by side
-            auto part = [&](int block) {              // the item's first block has it as its last
-                return a.parts + ((int64_t)(block * 2 + (block == c0 ? 1 : 0)) * 2 + slot) * kPaTile * (D + 2);
-            };
             const bool split = c0 != c1;
+            float *part = pa_part<D>(a, blockIdx.x, (int)blockIdx.x == c0, slot);
             if (!split) {                             // the whole item: the output
                 const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
                 f0 *= inv;
@@ -873,7 +902,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                         for (int e = 0; e < 32; ++e) o[e] += x[e] * f1;
                     }
                     if (split) {
-                        float *dst = part(blockIdx.x) + (k / 4 * kPaTile + row) * 4;
+                        float *dst = part + (k / 4 * kPaTile + row) * 4;
                         if (live) {
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
@@ -917,83 +946,14 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             tc::fence_before_sync();
             if (merge) arrive(merge_free);
             if (!split) {
-                if (live && a.lse) a.lse[token * a.q_heads + head] = log_sum(m, l);
+                if (live && a.lse) a.lse[token * a.q_heads + head] = pa_lse<F16>(m, l, c);
                 continue;
             }
-            // unnormalised, for the block that comes last
+            // unnormalised, for the second launch
             if (live) {
-                float *dst = part(blockIdx.x) + kPaTile * D + row;
+                float *dst = part + kPaTile * D + row;
                 dst[0] = m;
                 dst[kPaTile] = l;
-            }
-            __threadfence();
-            if (!(ok = group_sync())) break;
-            if (row == 0) {
-                const bool last = atomicAdd(a.arrivals + c0 * 2 + slot, 1u) == (uint32_t)(c1 - c0);
-                sh.last[slot] = last;
-                if (last) a.arrivals[c0 * 2 + slot] = 0u;
-            }
-            if (!(ok = group_sync())) break;
-            if (!sh.last[slot]) continue;
-            __threadfence();
-            // a warp joins a quarter of the columns, a lane a row, four parts
-            // at a time, all their loads in flight
-            constexpr int kVec = D / 16;
-            const int k0 = (warp & 3) * kVec;
-#pragma unroll 1
-            for (int r0 = 0; r0 < rows; r0 += 32) {
-                const int r = min(r0 + lane, rows - 1);
-                float M = -INFINITY, L = 0.0f, o[4 * kVec];
-#pragma unroll
-                for (int k = 0; k < 4 * kVec; ++k) o[k] = 0.0f;
-#pragma unroll 1
-                for (int b0 = c0; b0 <= c1; b0 += 4) {
-                    float pm[4], pl[4];
-                    float4 y[4][kVec];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float *p = part(min(b0 + e, c1));
-                        pm[e] = __ldcg(p + kPaTile * D + r);
-                        pl[e] = __ldcg(p + kPaTile * D + kPaTile + r);
-#pragma unroll
-                        for (int k = 0; k < kVec; ++k)
-                            y[e][k] = __ldcg(reinterpret_cast<const float4 *>(p + ((k0 + k) * kPaTile + r) * 4));
-                    }
-                    float mn = M;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) mn = fmaxf(mn, pm[e]);
-                    const float f = M == -INFINITY ? 0.0f : pa_ex2((M - mn) * c);
-                    M = mn;
-                    L *= f;
-#pragma unroll
-                    for (int k = 0; k < 4 * kVec; ++k) o[k] *= f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float g = b0 + e > c1 || pm[e] == -INFINITY ? 0.0f : pa_ex2((pm[e] - M) * c);
-                        L += pl[e] * g;
-#pragma unroll
-                        for (int k = 0; k < kVec; ++k) {
-                            o[4 * k] += y[e][k].x * g;
-                            o[4 * k + 1] += y[e][k].y * g;
-                            o[4 * k + 2] += y[e][k].z * g;
-                            o[4 * k + 3] += y[e][k].w * g;
-                        }
-                    }
-                }
-                if (r0 + lane >= rows) continue;
-                const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
-                const int tok = r * a.group_inv >> 16, head = h * a.group + r - tok * a.group;
-                const int64_t token = token0 + tok;
-                uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1 + 4 * k0;
-#pragma unroll
-                for (int i = 0; i < kVec / 2; ++i) {
-                    uint32_t v[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        v[k] = L == 0.0f ? 0u : pack2<F16>(o[8 * i + 2 * k] * inv, o[8 * i + 2 * k + 1] * inv);
-                    *reinterpret_cast<uint4 *>(out + 8 * i) = make_uint4(v[0], v[1], v[2], v[3]);
-                }
-                if (k0 == 0 && a.lse) a.lse[token * a.q_heads + head] = log_sum(M, L);
             }
         }
     }
@@ -1004,11 +964,91 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
 }
 
+// ----------------------------------------------------------------- joining
+
+constexpr int kJoinThreads = 256;
+
+// Block (b, g): 32 rows of the item that begins in block b and is cut, g =
+// slot * 4 + their quarter of the tile.  A thread has a row and some vectors of
+// four columns; four parts' loads are in flight together.
 template <int D, bool F16>
-static cudaError_t launch_typed(const AttnArgs &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, int blocks,
-                                cudaStream_t s) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PaJoin j = reinterpret_cast<const PaJoin *>(a.joins)[blockIdx.x];
+    const int slot = blockIdx.y >> 2, r = (blockIdx.y & 3) * 32 + (threadIdx.x & 31);
+    const int tokens = min(j.tokens - slot * a.tile_tokens, a.tile_tokens);
+    if (j.c0 == j.c1 || r >= tokens * a.group || __ldcg(a.status) != 0u) return;
+    constexpr int kVec = D / 4 / (kJoinThreads / 32);
+    const int k0 = (threadIdx.x >> 5) * kVec;
+    const float c = a.scale2;
+    float M = -INFINITY, L = 0.0f, o[4 * kVec];
+#pragma unroll
+    for (int k = 0; k < 4 * kVec; ++k) o[k] = 0.0f;
+    for (int b0 = j.c0; b0 <= j.c1; b0 += 4) {
+        float pm[4], pl[4], mn = M;
+        float4 y[4][kVec];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            pm[e] = -INFINITY;
+            pl[e] = 0.0f;
+            if (b0 + e > j.c1) continue;
+            const float *p = pa_part<D>(a, b0 + e, b0 + e == j.c0, slot);
+            pm[e] = __ldcg(p + kPaTile * D + r);
+            pl[e] = __ldcg(p + kPaTile * D + kPaTile + r);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                y[e][k] = __ldcg(reinterpret_cast<const float4 *>(p + ((k0 + k) * kPaTile + r) * 4));
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mn = fmaxf(mn, pm[e]);
+        const float f = M == -INFINITY ? 0.0f : pa_ex2((M - mn) * c);
+        M = mn;
+        L *= f;
+#pragma unroll
+        for (int k = 0; k < 4 * kVec; ++k) o[k] *= f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (b0 + e > j.c1) continue;
+            const float g = pm[e] == -INFINITY ? 0.0f : pa_ex2((pm[e] - M) * c);
+            L += pl[e] * g;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) {
+                o[4 * k] += y[e][k].x * g;
+                o[4 * k + 1] += y[e][k].y * g;
+                o[4 * k + 2] += y[e][k].z * g;
+                o[4 * k + 3] += y[e][k].w * g;
+            }
+        }
+    }
+    const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
+    const int tok = r * a.group_inv >> 16, head = j.head + r - tok * a.group;
+    const int64_t token = j.token + slot * a.tile_tokens + tok;
+    uint16_t *out = a.out + token * a.out_s0 + head * a.out_s1 + 4 * k0;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+        uint2 v = make_uint2(pack2<F16>(o[4 * k] * inv, o[4 * k + 1] * inv), pack2<F16>(o[4 * k + 2] * inv, o[4 * k + 3] * inv));
+        if (L == 0.0f) v = make_uint2(0u, 0u);
+        *reinterpret_cast<uint2 *>(out + 4 * k) = v;
+    }
+    if (k0 == 0 && a.lse) a.lse[token * a.q_heads + head] = pa_lse<F16>(M, L, c);
+}
+
+template <int D, bool F16>
+static cudaError_t launch_typed(const AttnArgs &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                                int blocks, cudaStream_t s) {
     paged_attention_kernel<D, F16><<<blocks, kPaThreads, PaShape<D>::kSmem, s>>>(a, q, k, v);
-    return cudaGetLastError();
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 8);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, F16>, a);
 }
 
 cudaError_t launch_paged_attention(const AttnArgs &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
@@ -1033,5 +1073,7 @@ cudaError_t paged_attention_prepare() {
 size_t paged_attention_parts(int head_dim, int blocks) {
     return (size_t)blocks * 4 * kPaTile * (head_dim + 2);
 }
+
+size_t paged_attention_joins(int blocks) { return blocks * sizeof(PaJoin); }
 
 }  // namespace dtm
