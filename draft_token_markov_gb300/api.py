@@ -125,8 +125,14 @@ def _check(code: int, what: str):
         raise MarkovError(code, what)
 
 
+# the current stream's handle without a Stream object (3 us to build)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -134,7 +140,7 @@ def _stream(stream) -> int | None:
 def _dev(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     return t.data_ptr()
 
@@ -424,6 +430,10 @@ class PagedPlan:
         self._h = h
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.page_size, self.dtype, self.max_rows, self.device = page_size, dtype, max_rows, device
+        self._cache_shape = torch.Size((page_size, kv_heads, head_dim))
+        # the two caches of a call, described in place
+        self._k_view, self._v_view = _CacheView(), _CacheView()
+        self._views = ctypes.byref(self._k_view), ctypes.byref(self._v_view)
 
     @property
     def handle(self):
@@ -464,46 +474,54 @@ def _new(stream, shape, dtype, device):
 
 def _flat(t: torch.Tensor, dtype: torch.dtype, n: int, name: str) -> int:
     """A contiguous CUDA tensor of n elements."""
-    p = _dev(t, dtype, name)
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
-    return p
+    try:
+        if t.dtype is dtype and t.is_cuda and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name)
+    raise ValueError(f"{name} must be contiguous with {n} elements, got {tuple(t.shape)}")
 
 
-def _page_table(page_table) -> int:
-    p = _dev(page_table, torch.int32, "page_table")
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [states, pages] with contiguous rows")
-    return p
+def _page_table(t):
+    """(pointer, row stride, states, pages) of [states, pages] int32."""
+    p = _dev(t, torch.int32, "page_table")
+    if t.dim() != 2:
+        raise ValueError("page_table must be [states, pages]")
+    states, pages = t.shape
+    s0, s1 = t.stride()
+    if s1 != 1 and pages > 1:
+        raise ValueError("page_table's rows must be contiguous")
+    return p, s0 if states > 1 else max(s0, pages), states, pages
 
 
-def _table_s0(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _cache_view(plan: PagedPlan, t, name: str) -> _CacheView:
+def _cache_view(plan: PagedPlan, view: _CacheView, t, name: str):
+    """Describe a paged cache tensor in `view`, one of the plan's."""
     p = _dev(t, plan.dtype, name)
-    if t.dim() != 4 or tuple(t.shape[1:]) != (plan.page_size, plan.kv_heads, plan.head_dim):
+    if t.dim() != 4 or t.shape[1:] != plan._cache_shape:
         raise ValueError(f"{name} must be [pages, {plan.page_size}, {plan.kv_heads}, "
                          f"{plan.head_dim}], got {tuple(t.shape)}")
-    s = t.stride()
-    if s[3] != 1:
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     # the stride of a dimension of one element says nothing
-    return _CacheView(p, t.shape[0], s[0] if t.shape[0] > 1 else 0, s[1],
-                      s[2] if plan.kv_heads > 1 else plan.head_dim)
+    pages = t.shape[0]
+    view.data, view.num_pages = p, pages
+    view.s_page, view.s_slot = s0 if pages > 1 else 0, s1
+    view.s_head = s2 if plan.kv_heads > 1 else plan.head_dim
 
 
 def _token_rows(plan: PagedPlan, t, heads: int, name: str):
-    """(pointer, token stride, head stride) of [tokens, heads, head_dim]."""
+    """(pointer, token stride, head stride, tokens) of [tokens, heads, head_dim]."""
     p = _dev(t, plan.dtype, name)
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != plan.head_dim:
         raise ValueError(f"{name} must be [tokens, {heads}, {plan.head_dim}], "
                          f"got {tuple(t.shape)}")
-    s = t.stride()
-    if s[2] != 1:
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return p, s[0] if t.shape[0] > 1 else 0, s[1] if heads > 1 else plan.head_dim
+    n = t.shape[0]
+    return p, s0 if n > 1 else 0, s1 if heads > 1 else plan.head_dim, n
 
 
 def markov_paged_layout(plan: PagedPlan, context_lens, query_lens, row_state_idx, page_table,
@@ -531,14 +549,13 @@ def markov_paged_layout(plan: PagedPlan, context_lens, query_lens, row_state_idx
         pages_held_out = pages_held
     if free_state_out is None:
         free_state_out = free_state
-    table = _page_table(page_table)
-    states = page_table.shape[0]
+    table, table_s0, states, pages = _page_table(page_table)
     i32, i64 = torch.int32, torch.int64
     code = lib().markov_paged_layout(
         plan.handle, _flat(context_lens, i32, rows, "context_lens"),
         _flat(query_lens, i32, rows, "query_lens"),
-        _flat(row_state_idx, i64, rows, "row_state_idx"), rows, table, _table_s0(page_table),
-        states, page_table.shape[1], _flat(pages_held, i32, states, "pages_held"),
+        _flat(row_state_idx, i64, rows, "row_state_idx"), rows, table, table_s0, states,
+        pages, _flat(pages_held, i32, states, "pages_held"),
         _flat(free_pages, i32, free_pages.numel(), "free_pages"), free_pages.numel(),
         _flat(free_state, i64, 2, "free_state"),
         _flat(pages_held_out, i32, states, "pages_held_out"),
@@ -554,15 +571,14 @@ def markov_paged_write(plan: PagedPlan, key, value, k_cache, v_cache, slots, str
     """Store key and value [tokens, kv_heads, head_dim] at their slots of the
     caches [pages, page_size, kv_heads, head_dim] (any strides with the last
     1, so a view of a heads-outside cache is one too); slot -1 is skipped."""
-    kp, k0, k1 = _token_rows(plan, key, plan.kv_heads, "key")
-    vp, v0, v1 = _token_rows(plan, value, plan.kv_heads, "value")
-    T = key.shape[0]
-    if value.shape[0] != T:
+    kp, k0, k1, T = _token_rows(plan, key, plan.kv_heads, "key")
+    vp, v0, v1, n = _token_rows(plan, value, plan.kv_heads, "value")
+    if n != T:
         raise ValueError("key and value must have the same tokens")
-    kc, vc = _cache_view(plan, k_cache, "k_cache"), _cache_view(plan, v_cache, "v_cache")
-    code = lib().markov_paged_write(plan.handle, kp, k0, k1, vp, v0, v1, ctypes.byref(kc),
-                                    ctypes.byref(vc), _flat(slots, torch.int64, T, "slots"), T,
-                                    _stream(stream))
+    _cache_view(plan, plan._k_view, k_cache, "k_cache")
+    _cache_view(plan, plan._v_view, v_cache, "v_cache")
+    code = lib().markov_paged_write(plan.handle, kp, k0, k1, vp, v0, v1, *plan._views,
+                                    _flat(slots, torch.int64, T, "slots"), T, _stream(stream))
     _check(code, "markov_paged_write")
 
 
@@ -575,20 +591,18 @@ def markov_paged_attention(plan: PagedPlan, q, k_cache, v_cache, page_table, row
     first `sinks`.  lse [tokens, q_heads] fp32 is computed when a tensor, or
     True to allocate one, is given.  Tokens of padding rows are not written."""
     rows = row_state_idx.shape[0]
-    qp, q0, q1 = _token_rows(plan, q, plan.q_heads, "q")
-    T = q.shape[0]
+    qp, q0, q1, T = _token_rows(plan, q, plan.q_heads, "q")
     if out is None:
         out = _new(stream, (T, plan.q_heads, plan.head_dim), plan.dtype, q.device)
-    op, o0, o1 = _token_rows(plan, out, plan.q_heads, "out")
-    if out.shape[0] != T:
+    op, o0, o1, n = _token_rows(plan, out, plan.q_heads, "out")
+    if n != T:
         raise ValueError("out must have q's tokens")
     if lse is True:
         lse = _new(stream, (T, plan.q_heads), torch.float32, q.device)
-    kc, vc = _cache_view(plan, k_cache, "k_cache"), _cache_view(plan, v_cache, "v_cache")
-    table = _page_table(page_table)
+    _cache_view(plan, plan._k_view, k_cache, "k_cache")
+    _cache_view(plan, plan._v_view, v_cache, "v_cache")
     code = lib().markov_paged_attention(
-        plan.handle, qp, q0, q1, ctypes.byref(kc), ctypes.byref(vc), table,
-        _table_s0(page_table), page_table.shape[0], page_table.shape[1],
+        plan.handle, qp, q0, q1, *plan._views, *_page_table(page_table),
         _flat(row_state_idx, torch.int64, rows, "row_state_idx"),
         _flat(query_start, torch.int32, rows + 1, "query_start"),
         _flat(seq_lens, torch.int32, rows, "seq_lens"), rows, T,
@@ -597,6 +611,20 @@ def markov_paged_attention(plan: PagedPlan, q, k_cache, v_cache, page_table, row
         _stream(stream))
     _check(code, "markov_paged_attention")
     return out, lse
+
+
+_LOGITS = {torch.bfloat16: MARKOV_BF16, torch.float32: MARKOV_F32}
+
+
+def _matrix(t, dtype: torch.dtype, rows: int, columns: int, name: str):
+    """(pointer, row stride) of [rows, columns] with contiguous rows."""
+    p = _dev(t, dtype, name)
+    if t.shape != (rows, columns):
+        raise ValueError(f"{name} must be [{rows}, {columns}], got {tuple(t.shape)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and columns > 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return p, s0 if rows > 1 else max(s0, columns)
 
 
 def markov_verify(plan: Plan, target_logits, draft_tokens, logit_cache, temperature, uniforms,
@@ -610,46 +638,31 @@ def markov_verify(plan: Plan, target_logits, draft_tokens, logit_cache, temperat
     with one position).  target_probs and draft_probs [rows, N], given
     together, receive each draft's probability under the two models."""
     rows, N, V = logit_cache.shape
-    dtypes = {torch.bfloat16: MARKOV_BF16, torch.float32: MARKOV_F32}
-    if target_logits.dtype not in dtypes or logit_cache.dtype not in dtypes:
+    td, cd = _LOGITS.get(target_logits.dtype), _LOGITS.get(logit_cache.dtype)
+    if td is None or cd is None:
         raise TypeError("target_logits and logit_cache must be bfloat16 or float32")
-    if (N, V) != (plan.num_steps, plan.vocab) or tuple(target_logits.shape) != (rows, N + 1, V):
+    if N != plan.num_steps or V != plan.vocab or target_logits.shape != (rows, N + 1, V):
         raise ValueError(f"logit_cache must be [rows, {plan.num_steps}, {plan.vocab}] and "
                          f"target_logits [rows, {plan.num_steps + 1}, {plan.vocab}]")
-    if target_logits.stride(2) != 1 or logit_cache.stride(2) != 1 or noise.stride(-1) != 1:
-        raise ValueError("the last dimension of target_logits, logit_cache and noise must be "
-                         "contiguous")
-    if tuple(draft_tokens.shape) != (rows, N) or tuple(uniforms.shape) != (rows, N) or \
-            tuple(noise.shape) != (rows, V):
-        raise ValueError("draft_tokens and uniforms must be [rows, N], noise [rows, V]")
-    dev = target_logits.device
     if tokens is None:
-        tokens = _new(stream, (rows, N + 1), torch.int64, dev)
+        tokens = _new(stream, (rows, N + 1), torch.int64, target_logits.device)
     if num_accepted is None:
-        num_accepted = _new(stream, (rows,), torch.int32, dev)
-    if tuple(tokens.shape) != (rows, N + 1):
-        raise ValueError("tokens must be [rows, N + 1]")
-    if (N > 1 and (draft_tokens.stride(1) != 1 or uniforms.stride(1) != 1)) or tokens.stride(1) != 1:
-        raise ValueError("the last dimension of draft_tokens, uniforms and tokens must be contiguous")
-
-    def s0(t):
-        return t.stride(0) if rows > 1 else max(t.stride(0), t.shape[-1])
-
+        num_accepted = _new(stream, (rows,), torch.int32, target_logits.device)
+    t0, t1, t2 = target_logits.stride()
+    c0, c1, c2 = logit_cache.stride()
+    if t2 != 1 or c2 != 1:
+        raise ValueError("the last dimension of target_logits and logit_cache must be contiguous")
+    f32, i64 = torch.float32, torch.int64
     code = lib().markov_verify(
-        plan.handle, _dev(target_logits, target_logits.dtype, "target_logits"),
-        dtypes[target_logits.dtype], target_logits.stride(0), target_logits.stride(1),
-        _dev(draft_tokens, torch.int64, "draft_tokens"), s0(draft_tokens),
-        _dev(logit_cache, logit_cache.dtype, "logit_cache"), dtypes[logit_cache.dtype],
-        logit_cache.stride(0), logit_cache.stride(1),
-        _flat(temperature, torch.float32, rows, "temperature"),
-        _dev(uniforms, torch.float32, "uniforms"), s0(uniforms),
-        _dev(noise, torch.float32, "noise"), s0(noise),
-        _flat(row_state_idx, torch.int64, rows, "row_state_idx"), rows,
-        _dev(tokens, torch.int64, "tokens"), s0(tokens),
+        plan.handle, _dev(target_logits, target_logits.dtype, "target_logits"), td, t0, t1,
+        *_matrix(draft_tokens, i64, rows, N, "draft_tokens"),
+        _dev(logit_cache, logit_cache.dtype, "logit_cache"), cd, c0, c1,
+        _flat(temperature, f32, rows, "temperature"), *_matrix(uniforms, f32, rows, N, "uniforms"),
+        *_matrix(noise, f32, rows, V, "noise"), _flat(row_state_idx, i64, rows, "row_state_idx"),
+        rows, *_matrix(tokens, i64, rows, N + 1, "tokens"),
         _flat(num_accepted, torch.int32, rows, "num_accepted"),
-        None if target_probs is None else _flat(target_probs, torch.float32, rows * N,
-                                                "target_probs"),
-        None if draft_probs is None else _flat(draft_probs, torch.float32, rows * N,
-                                               "draft_probs"), _stream(stream))
+        None if target_probs is None else _flat(target_probs, f32, rows * N, "target_probs"),
+        None if draft_probs is None else _flat(draft_probs, f32, rows * N, "draft_probs"),
+        _stream(stream))
     _check(code, "markov_verify")
     return tokens, num_accepted
