@@ -42,10 +42,9 @@ struct markov_plan {
     uint64_t *bwin = nullptr;
     uint32_t *bcnt = nullptr;
     bool batch_dirty = false;
-    // acceptance: softmax partials, and per row the verdict on its drafts, the
-    // best key and a counter (zero between calls)
+    // acceptance: softmax partials, and per row the best key and a counter
+    // (zero between calls)
     uint4 *vpart = nullptr;
-    void *verdicts = nullptr;
     uint64_t *vwin = nullptr;
     uint32_t *varr = nullptr;
     size_t tc_slots_n = 0;
@@ -77,7 +76,6 @@ void free_plan(markov_plan *p) {
     if (p->win_max) cudaFree(p->win_max);
     if (p->win_cnt) cudaFree(p->win_cnt);
     if (p->vpart) cudaFree(p->vpart);
-    if (p->verdicts) cudaFree(p->verdicts);
     if (p->vwin) cudaFree(p->vwin);
     if (p->varr) cudaFree(p->varr);
     if (p->ev_fork) cudaEventDestroy(p->ev_fork);
@@ -203,7 +201,6 @@ markov_status markov_plan_create(const markov_desc *desc, markov_plan **out) {
         cudaMemset(p->win_max, 0, kWinMaxN * sizeof(uint64_t)) != cudaSuccess ||
         cudaMemset(p->win_cnt, 0, kWinCntN * sizeof(uint32_t)) != cudaSuccess ||
         cudaMalloc(&p->vpart, (size_t)d.max_rows * (2 * d.num_steps + 1) * kVerifyMaxSegs * sizeof(uint4)) != cudaSuccess ||
-        cudaMalloc(&p->verdicts, (size_t)d.max_rows * kVerdictBytes) != cudaSuccess ||
         cudaMalloc(&p->vwin, d.max_rows * sizeof(uint64_t)) != cudaSuccess ||
         cudaMalloc(&p->varr, d.max_rows * sizeof(uint32_t)) != cudaSuccess ||
         cudaMemset(p->vwin, 0, d.max_rows * sizeof(uint64_t)) != cudaSuccess ||
@@ -563,7 +560,6 @@ markov_status markov_verify(markov_plan *p, const void *target_logits, markov_dt
     a.p = target_probs;
     a.q = draft_probs;
     a.part = p->vpart;
-    a.verdicts = p->verdicts;
     a.win = p->vwin;
     a.arrivals = p->varr;
     a.status = p->ctrl + 2;

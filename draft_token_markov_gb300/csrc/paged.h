@@ -86,16 +86,14 @@ struct VerifyArgs {
     int32_t *accepted;
     float *p, *q;
     uint4 *part;               // [rows * (2N + 1)][segs] softmax partials
-    void *verdicts;            // [rows] kVerdictBytes: what the first launch found
-    uint64_t *win;             // [rows] best key
+    uint64_t *win;             // [rows] best key; zero between calls
     uint32_t *arrivals;        // [rows] blocks done; zero between calls
     const uint32_t *status;
-    int segs, seg_len;         // of the statistics kernel
+    int segs, seg_len, stat_blocks;   // of the statistics kernel
     int pick_segs, pick_len;   // of the pick kernel
 };
 
 constexpr int kVerifyMaxSegs = 32;         // a lane each
-constexpr int kVerdictBytes = 32;
 
 cudaError_t launch_paged_layout(const LayoutArgs &a, cudaStream_t s);
 cudaError_t launch_paged_write(const WriteArgs &a, cudaStream_t s);

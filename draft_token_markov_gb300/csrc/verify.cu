@@ -1,15 +1,20 @@
 // verify.cu -- acceptance of drafts against the target's logits.
 //
-// Two launches.  The first reads every logit once: a block takes a segment
-// of one position's row (target or draft) and leaves its maximum m and
-// z = sum exp((l - m) / T); the block that finishes a request's last segment
-// joins them and walks the drafts.  The second, a programmatic dependent of
-// the first, takes the argmax of the residual's key over one position of each
-// request: one target row, one draft row, much of them still in L2, and the
-// request's noise, which does not wait for the first launch.
+// Two launches.  The first reads every logit once: its warps take segments of
+// a position's row (target or draft) and leave each one's maximum m and
+// z = sum exp((l - m) / T).  The second, a programmatic dependent of the first,
+// joins a request's partials in every one of its blocks (at most 33 rows of
+// 32), walks the drafts, and takes the argmax of the residual's key over its
+// ids of one position: one target row, one draft row, much of them still in
+// L2, and the request's noise.  That, the drafts and their logits do not wait
+// for the first launch.  (Joined in the first launch instead, by the warp that
+// came last, the fences at each segment's end took longer than its loads: 129
+// against 50 us for 64 requests of 8 drafts.)
 //
 // exp((l - m) / T) is ex2((l - m) * c) with c = log2(e) / T: l - m is exact
 // or rounded once, and an overflow of l / T cannot make it NaN.
+#include <climits>
+
 #include "paged.h"
 #include "common.cuh"
 
@@ -70,11 +75,12 @@ __device__ __forceinline__ uint64_t block_max(uint64_t x, uint64_t *shared) {
     return warp_max(x);
 }
 
-// The segment's best (logit, id) in the argmax order, whatever it holds.
+// The segment's best (logit, id) in the argmax order, whatever it holds; by
+// one warp.
 template <bool F32>
-__device__ __noinline__ uint64_t segment_key(const void *row, int64_t base, int lo, int hi, uint64_t *shared) {
+__device__ __noinline__ uint64_t segment_key(const void *row, int64_t base, int lo, int hi) {
     uint64_t best = 0;
-    for (int v = lo + threadIdx.x * 8; v < hi; v += kVerifyThreads * 8) {
+    for (int v = lo + (threadIdx.x & 31) * 8; v < hi; v += 256) {
         float x[8];
         load8<F32>(row, base + v, x);
 #pragma unroll
@@ -83,7 +89,7 @@ __device__ __noinline__ uint64_t segment_key(const void *row, int64_t base, int 
             best = k > best ? k : best;
         }
     }
-    return block_max(best, shared);
+    return warp_max(best);
 }
 
 // Two fp32 values in one register pair, and the packed arithmetic on them.
@@ -106,101 +112,122 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// A row's partial: m, z and the key.  For a row that is sampled the key says
-// only whether the maximum is finite, and where it is if it is not.  Both
-// kinds of row take kVectors vectors of 8 ids a turn, their loads in flight
-// together, and compare the running maximum once a turn; a NaN shows in a
-// sum, and then the segment is looked through again.
+// 8 consecutive logits as they lie, and their maximum (NaN if one is).
 template <bool F32>
-__device__ void segment_stats(const VerifyArgs &a, const void *row, int64_t base, float T, uint4 *out) {
-    constexpr int kVectors = F32 ? 2 : 4, kStep = kVerifyThreads * 8;
-    __shared__ uint64_t key_s[kVerifyThreads / 32];
-    __shared__ float m_s[kVerifyThreads / 32], z_s[kVerifyThreads / 32];
-    const int lo = blockIdx.x * a.seg_len, hi = min(a.V, lo + a.seg_len);
-    const bool sampled = samples(T);
-    const float c = sampled ? inv_temperature(T) : 0.0f;
-    float m = -INFINITY, z = 0.0f;
-    int at = lo;                                     // greedy: the turn of the maximum
-    for (int v = lo + threadIdx.x * 8; v < hi; v += kVectors * kStep) {
-        float x[kVectors][8], top = -INFINITY;
+struct Raw8 {
+    uint4 v[F32 ? 2 : 1];
+
+    // -inf where there are none
+    __device__ __forceinline__ void load(const void *row, int64_t at, bool there) {
+        constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(row) + at * (F32 ? 4 : 2));
 #pragma unroll
-        for (int k = 0; k < kVectors; ++k) {
-            if (v + k * kStep < hi) {
-                load8<F32>(row, base + v + k * kStep, x[k]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) x[k][j] = -INFINITY;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < kVectors; ++k)
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) top = fmaxf(fmaxf(top, x[k][j]), x[k][j + 1]);
-        if (top > m) {
-            z = m == -INFINITY ? z : z * ex2((m - top) * c);
-            m = top;
-            at = v;
-        }
-        uint64_t sum[2] = {0, 0};
-        if (sampled) {
-            const float ref = m == -INFINITY ? 0.0f : m;
-            const uint64_t neg = pack_f2(-ref, -ref), c2 = pack_f2(c, c);
-#pragma unroll
-            for (int k = 0; k < kVectors; ++k)
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    float e0, e1;
-                    split_f2(mul_f2(add_f2(pack_f2(x[k][j], x[k][j + 1]), neg), c2), e0, e1);
-                    sum[j / 2 & 1] = add_f2(sum[j / 2 & 1], pack_f2(ex2(e0), ex2(e1)));
-                }
-        } else {
-            // only for its NaNs (that of inf - inf costs a second look)
-#pragma unroll
-            for (int k = 0; k < kVectors; ++k)
-                if (v + k * kStep < hi)
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2)
-                        sum[j / 2 & 1] = add_f2(sum[j / 2 & 1], pack_f2(x[k][j], x[k][j + 1]));
-        }
-        float s0, s1;
-        split_f2(add_f2(sum[0], sum[1]), s0, s1);
-        z += s0 + s1;
+        for (int k = 0; k < (F32 ? 2 : 1); ++k) v[k] = there ? __ldg(p + k) : make_uint4(kNone, kNone, kNone, kNone);
     }
-    // join the warp, then the block
-    const float own = m;
+    // word j: ids 2 j and 2 j + 1 of BF16 logits, id j of fp32 ones
+    __device__ __forceinline__ uint32_t word(int j) const {
+        const uint4 &u = v[j >> 2];
+        return (j & 3) == 0 ? u.x : (j & 3) == 1 ? u.y : (j & 3) == 2 ? u.z : u.w;
+    }
+    __device__ __forceinline__ void pair(int j, float &lo, float &hi) const {
+        if (F32) {
+            lo = __uint_as_float(word(2 * j));
+            hi = __uint_as_float(word(2 * j + 1));
+        } else {
+            lo = __uint_as_float(word(j) << 16);
+            hi = __uint_as_float(word(j) & 0xffff0000u);
+        }
+    }
+};
+
+// Running maximum of words (two BF16 values or an fp32 one); NaN wins.
+template <bool F32>
+__device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b) {
+    uint32_t r;
+    if (F32)
+        asm("max.NaN.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    else
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// A thread's part of a segment: the maximum, the sum against it and, for a
+// greedy row, the turn in which the maximum came.
+struct Running {
+    float m, z;
+    int at;
+};
+
+constexpr int kTurnIds = 1024;             // ids that a warp takes a turn, 4 vectors of 8 a lane
+
+// One turn's vectors, the first from id v on.  Some four instructions an id
+// for a sampled row; a greedy one needs the maxima alone.  A NaN stays in z.
+template <bool F32>
+__device__ __forceinline__ void take_turn(const Raw8<F32> (&x)[4], int v, bool sampled, float c, Running &s) {
+    constexpr int kWords = F32 ? 8 : 4;
+    uint32_t w = x[0].word(0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) w = word_max<F32>(w, x[k].word(j));
+    float top = __uint_as_float(F32 ? w : w << 16);
+    if (!F32) top = __uint_as_float(word_max<true>(__float_as_uint(top), w & 0xffff0000u));
+    if (top != top) s.z = NAN;
+    if (top > s.m) {
+        if (s.m != -INFINITY) s.z *= ex2((s.m - top) * c);
+        s.m = top;
+        s.at = v;
+    }
+    if (!sampled) return;
+    const float ref = s.m == -INFINITY ? 0.0f : s.m;
+    const uint64_t neg = pack_f2(-ref, -ref), c2 = pack_f2(c, c);
+    uint64_t sum[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float e0, e1;
+            x[k].pair(j, e0, e1);
+            split_f2(mul_f2(add_f2(pack_f2(e0, e1), neg), c2), e0, e1);
+            sum[j & 1] = add_f2(sum[j & 1], pack_f2(ex2(e0), ex2(e1)));
+        }
+    float s0, s1;
+    split_f2(add_f2(sum[0], sum[1]), s0, s1);
+    s.z += s0 + s1;
+}
+
+// A segment's partial from its lanes': m, z and the key.  For a sampled row the
+// key says only whether the maximum is finite, and where it is if it is not.
+template <bool F32>
+__device__ void end_segment(const void *row, int64_t base, int lo, int hi, bool sampled, float c, const Running &s,
+                            uint4 *out) {
+    float m = s.m, z = s.z;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (own != -INFINITY) z *= ex2((own - m) * c);
+    if (s.m != -INFINITY) z *= ex2((s.m - m) * c);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if ((threadIdx.x & 31) == 0) {
-        m_s[threadIdx.x >> 5] = m;
-        z_s[threadIdx.x >> 5] = z;
-    }
-    __syncthreads();
-    m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kVerifyThreads / 32; ++w) m = fmaxf(m, m_s[w]);
-    z = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kVerifyThreads / 32; ++w) z += m_s[w] == -INFINITY ? z_s[w] : z_s[w] * ex2((m_s[w] - m) * c);
     uint64_t key = pack_key(m, (uint32_t)lo);
-    if (z != z || m == INFINITY || (sampled && z == INFINITY)) {
-        key = segment_key<F32>(row, base, lo, hi, key_s);
+    if (z != z || m == INFINITY || z == INFINITY) {
+        key = segment_key<F32>(row, base, lo, hi);
     } else if (!sampled && m != -INFINITY) {
         // the lowest id of the maximum, among the ids of its turn
-        uint64_t best = 0;
-        if (own == m) {
-#pragma unroll 1
-            for (int k = kVectors - 1; k >= 0; --k)
-#pragma unroll 1
-                for (int j = 7; j >= 0; --j)
-                    if (at + k * kStep < hi && load1<F32>(row, base + at + k * kStep + j) == m)
-                        best = pack_key(m, (uint32_t)(at + k * kStep + j));
-        }
-        key = block_max(best, key_s);
+        Raw8<F32> x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k].load(row, base + s.at + k * 256, s.at + k * 256 < hi);
+        int id = INT_MAX;
+#pragma unroll
+        for (int k = 3; k >= 0; --k)
+#pragma unroll
+            for (int j = 3; j >= 0; --j) {
+                float e0, e1;
+                x[k].pair(j, e0, e1);
+                if (e1 == m) id = s.at + k * 256 + 2 * j + 1;
+                if (e0 == m) id = s.at + k * 256 + 2 * j;
+            }
+        key = warp_max(s.m == m ? pack_key(m, (uint32_t)id) : 0ull);
     }
-    if (threadIdx.x == 0)
+    if ((threadIdx.x & 31) == 0)
         __stcg(out, make_uint4(__float_as_uint(m), __float_as_uint(z), (uint32_t)key, (uint32_t)(key >> 32)));
 }
 
@@ -212,45 +239,107 @@ struct Dist {
 
 __device__ __forceinline__ float prob(const Dist &d, float l, int v, float c) {
     if (d.id >= 0) return v == d.id ? 1.0f : 0.0f;
-    return ex2((l - d.m) * c) * d.inv_z;
+    // rounded: p - q is 0 where the two are equal, not a fused product's rest
+    return __fmul_rn(ex2((l - d.m) * c), d.inv_z);
 }
 
-// What the second launch has to know of a request: its distributions at the
-// position it draws, and that position; the row's winner word is cleared.
+// One segment: ids [lo, hi) of a row that starts at element `base`.
+template <bool F32>
+__device__ __forceinline__ void take_segment(const void *row, int64_t base, int lo, int hi, bool sampled, float c,
+                                             uint4 *out) {
+    const int lane8 = (threadIdx.x & 31) * 8;
+    Running s{-INFINITY, 0.0f, lo + lane8};
+    Raw8<F32> x[4], y[4];
+    auto load = [&](int v, Raw8<F32> (&x)[4]) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k].load(row, base + v + k * 256, v + k * 256 < hi);
+    };
+    // two turns a round, each loaded while the other is taken
+    load(lo + lane8, x);
+#pragma unroll 1
+    for (int v = lo + lane8; v - lane8 < hi; v += 2 * kTurnIds) {
+        const bool second = v - lane8 + kTurnIds < hi;
+        if (second) load(v + kTurnIds, y);
+        take_turn<F32>(x, v, sampled, c, s);
+        if (!second) break;
+        if (v - lane8 + 2 * kTurnIds < hi) load(v + 2 * kTurnIds, x);
+        take_turn<F32>(y, v + kTurnIds, sampled, c, s);
+    }
+    end_segment<F32>(row, base, lo, hi, sampled, c, s, out);
+}
+
+// The segments of the call, row = request * (2 N + 1) + position, are dealt to
+// the warps in turn; a warp's loads pause only between two of them, and the
+// 32 warps of a multiprocessor do so at different times.
+template <bool TF32, bool CF32>
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_stats_kernel(VerifyArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (__ldcg(a.status) != 0u) return;
+    const int per = 2 * a.N + 1;
+    const int tasks = a.rows * per * a.segs, warps = gridDim.x * (kVerifyThreads / 32);
+#pragma unroll 1
+    for (int task = blockIdx.x * (kVerifyThreads / 32) + (threadIdx.x >> 5); task < tasks; task += warps) {
+        const int row = task / a.segs, b = row / per, i = row - b * per;
+        if (a.idx[b] < 0) continue;
+        const int lo = (task - row * a.segs) * a.seg_len, hi = min(a.V, lo + a.seg_len);
+        const float T = a.temperature[b];
+        const bool sampled = samples(T);
+        const float c = sampled ? inv_temperature(T) : 0.0f;
+        const bool draft = i > a.N;
+        const void *from = draft ? a.cache : a.target;
+        const int64_t base = draft ? b * a.cache_s0 + (i - a.N - 1) * a.cache_s1 : b * a.target_s0 + i * a.target_s1;
+        if (TF32 == CF32)
+            take_segment<TF32>(from, base, lo, hi, sampled, c, a.part + task);
+        else if (draft)
+            take_segment<CF32>(from, base, lo, hi, sampled, c, a.part + task);
+        else
+            take_segment<TF32>(from, base, lo, hi, sampled, c, a.part + task);
+    }
+}
+
+// What the pick has to know of a request: its distributions at the position it
+// draws, and that position.
 struct Verdict {
     Dist p, q;
     int n;
-    int pad;
 };
-static_assert(sizeof(Verdict) == kVerdictBytes, "plan scratch");
 
-// By the block that finished the last of the request's segments: its 2 N + 1
-// distributions, the walk over the drafts and what is known by now of the
-// outputs.
+// A thread's draft, and its logits; what does not wait for the first launch.
+struct Draft {
+    int64_t x;
+    float lp, lq, u;
+};
+
 template <bool TF32, bool CF32>
-__device__ void decide(const VerifyArgs &a, int b, float T) {
+__device__ __forceinline__ Draft load_draft(const VerifyArgs &a, int b) {
+    Draft d{-1, 0.0f, 0.0f, 0.0f};
+    const int i = threadIdx.x;
+    if (i < a.N) {
+        d.x = a.draft[b * a.draft_s0 + i];
+        d.u = a.uniforms[b * a.uni_s0 + i];
+        if (d.x >= 0 && d.x < a.V) {
+            d.lp = load1<TF32>(a.target, b * a.target_s0 + i * a.target_s1 + d.x);
+            d.lq = load1<CF32>(a.cache, b * a.cache_s0 + i * a.cache_s1 + d.x);
+        }
+    }
+    return d;
+}
+
+// By a whole block: the request's distributions from their partials, the walk
+// over its drafts; with `write`, what is known by now of the outputs.
+__device__ __forceinline__ Verdict walk(const VerifyArgs &a, int b, float T, const Draft &d, bool write) {
     constexpr int kWarps = kVerifyThreads / 32, kTurns = (2 * kMaxSteps + 1 + kWarps - 1) / kWarps;
     __shared__ Dist dist[2 * kMaxSteps + 1];
-    __shared__ float p_s[kMaxSteps], q_s[kMaxSteps], u_s[kMaxSteps];
+    __shared__ uint32_t accepted_s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, N = a.N, per = 2 * N + 1;
     const float c = samples(T) ? inv_temperature(T) : 0.0f;
-    // every load of the block first: partials, drafts and their logits
+    // a warp a position in turn, a lane a segment
     uint4 part[kTurns];
 #pragma unroll
     for (int k = 0; k < kTurns; ++k) {
         part[k] = make_uint4(0xff800000u, 0u, 0u, 0u);
         if (warp + k * kWarps < per && lane < a.segs)
             part[k] = __ldcg(a.part + ((int64_t)b * per + warp + k * kWarps) * a.segs + lane);
-    }
-    int64_t x = -1;
-    float lp = 0.0f, lq = 0.0f;
-    if (tid < N) {
-        x = a.draft[b * a.draft_s0 + tid];
-        u_s[tid] = a.uniforms[b * a.uni_s0 + tid];
-        if (x >= 0 && x < a.V) {
-            lp = load1<TF32>(a.target, b * a.target_s0 + tid * a.target_s1 + x);
-            lq = load1<CF32>(a.cache, b * a.cache_s0 + tid * a.cache_s1 + x);
-        }
     }
 #pragma unroll
     for (int k = 0; k < kTurns; ++k) {
@@ -270,55 +359,34 @@ __device__ void decide(const VerifyArgs &a, int b, float T) {
         }
     }
     __syncthreads();
-    if (tid < N) {
-        const bool in = x >= 0 && x < a.V;
-        p_s[tid] = in ? prob(dist[tid], lp, (int)x, c) : 0.0f;
-        q_s[tid] = in ? prob(dist[N + 1 + tid], lq, (int)x, c) : 0.0f;
+    float p = 0.0f, q = 0.0f;
+    if (warp == 0) {
+        if (d.x >= 0 && d.x < a.V) {
+            p = prob(dist[lane], d.lp, (int)d.x, c);
+            q = prob(dist[N + 1 + lane], d.lq, (int)d.x, c);
+        }
+        // the drafts before the first refusal
+        const uint32_t refused = __ballot_sync(0xffffffffu, !(lane < N && d.u * q < p));
+        if (lane == 0) accepted_s = __ffs(refused) - 1;
     }
     __syncthreads();
-    int n = 0;
-    while (n < N && u_s[n] * q_s[n] < p_s[n]) ++n;
-    if (tid < N && a.p) {
-        a.p[(int64_t)b * N + tid] = p_s[tid];
-        a.q[(int64_t)b * N + tid] = q_s[tid];
+    const int n = (int)accepted_s;
+    const Verdict v{dist[n], dist[n < N ? N + 1 + n : n], n};
+    if (write) {
+        if (tid < N && a.p) {
+            a.p[(int64_t)b * N + tid] = p;
+            a.q[(int64_t)b * N + tid] = q;
+        }
+        if (tid == 0) a.accepted[b] = n;
+        if (tid <= N) {
+            // where p is one-hot there is nothing to draw
+            int64_t *token = a.tokens + b * a.tok_s0 + tid;
+            if (tid < n) *token = d.x;
+            else if (tid > n) *token = -1;
+            else if (v.p.id >= 0) *token = v.p.id;
+        }
     }
-    const Dist P = dist[n];
-    if (tid <= N) {
-        // where p is one-hot there is nothing to draw
-        int64_t *token = a.tokens + b * a.tok_s0 + tid;
-        if (tid < n) *token = x;
-        else if (tid > n) *token = -1;
-        else if (P.id >= 0) *token = P.id;
-    }
-    if (tid == 0) {
-        a.accepted[b] = n;
-        Verdict v{P, n < N ? dist[N + 1 + n] : P, n, 0};
-        reinterpret_cast<Verdict *>(a.verdicts)[b] = v;
-        a.win[b] = 0;
-    }
-}
-
-template <bool TF32, bool CF32>
-__global__ void __launch_bounds__(kVerifyThreads) verify_stats_kernel(VerifyArgs a) {
-    __shared__ uint32_t last_s;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int per = 2 * a.N + 1, row = blockIdx.y, b = row / per, i = row - b * per;
-    if (a.idx[b] < 0 || __ldcg(a.status) != 0u) return;
-    uint4 *out = a.part + (int64_t)row * a.segs + blockIdx.x;
-    const float T = a.temperature[b];
-    if (i <= a.N)
-        segment_stats<TF32>(a, a.target, b * a.target_s0 + i * a.target_s1, T, out);
-    else
-        segment_stats<CF32>(a, a.cache, b * a.cache_s0 + (i - a.N - 1) * a.cache_s1, T, out);
-    if (threadIdx.x == 0) {
-        __threadfence();
-        const uint32_t blocks = (uint32_t)(per * a.segs);
-        last_s = atomicAdd(a.arrivals + b, 1u) == blocks - 1;
-        if (last_s) a.arrivals[b] = 0;               // the second launch counts from here
-        __threadfence();
-    }
-    __syncthreads();
-    if (last_s) decide<TF32, CF32>(a, b, T);
+    return v;
 }
 
 template <bool TF32, bool CF32>
@@ -326,105 +394,130 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(VerifyArgs 
     __shared__ uint64_t key_s[kVerifyThreads / 32];
     __shared__ uint32_t last_s;
     const int b = blockIdx.y, N = a.N, tid = threadIdx.x;
-    const float *noise = a.noise + b * a.noise_s0;
-    const int lo = blockIdx.x * a.pick_len, hi = min(a.V, lo + a.pick_len);
     const bool padding = a.idx[b] < 0;
     const float T = a.temperature[b];
     const float c = samples(T) ? inv_temperature(T) : 0.0f;
-    // an input, and the largest: on its way before the first launch is done
-    float first[8];
-    if (!padding && samples(T) && lo + tid * 8 < hi) load8<true>(noise, lo + tid * 8, first);
+    const float *noise = a.noise + b * a.noise_s0;
+    const int lo = blockIdx.x * a.pick_len, hi = min(a.V, lo + a.pick_len);
+    Raw8<true> first;
+    first.load(noise, lo + tid * 8, !padding && samples(T) && lo + tid * 8 < hi);
+    Draft d{-1, 0.0f, 0.0f, 0.0f};
+    if (!padding) d = load_draft<TF32, CF32>(a, b);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (padding || __ldcg(a.status) != 0u) return;
-    const uint4 *said = reinterpret_cast<const uint4 *>(reinterpret_cast<const Verdict *>(a.verdicts) + b);
-    const uint4 v0 = __ldcg(said), v1 = __ldcg(said + 1);
-    const Dist P{__uint_as_float(v0.x), __uint_as_float(v0.y), (int)v0.z};
-    const Dist Q{__uint_as_float(v0.w), __uint_as_float(v1.x), (int)v1.y};
-    const int n = (int)v1.z;
+    const Verdict verdict = walk(a, b, T, d, blockIdx.x == 0);
+    const int n = verdict.n;
+    const Dist P = verdict.p, Q = verdict.q;
     if (P.id >= 0) return;                           // its token is out
     const int64_t t_base = b * a.target_s0 + n * a.target_s1, c_base = b * a.cache_s0 + n * a.cache_s1;
 
-    // the best key over [lo, hi): of ln(p - q) + g, or of ln p + g with whole
+    // The best key over [lo, hi): of ln(p - q) + g, or of ln p + g with whole.
+    // The fast logarithm (within 1e-4 here) tells which few ids, near the
+    // warp's best, need the exact one.
     auto best_of = [&](int lo, int hi, bool whole, bool again) {
+        constexpr int kStep = kVerifyThreads * 8;
         uint64_t best = 0;
-        float mine = -INFINITY;
-        for (int v = lo + tid * 8; v < hi; v += kVerifyThreads * 8) {
-            float x[8], y[8], g[8];
-            load8<TF32>(a.target, t_base + v, x);
-            if (!whole) load8<CF32>(a.cache, c_base + v, y);
-            if (!again && v < lo + kVerifyThreads * 8) {
+        float near = -INFINITY;
+        Raw8<TF32> x;
+        Raw8<CF32> y;
+        Raw8<true> g;
+        auto load = [&](int v, bool noise_too) {
+            x.load(a.target, t_base + v, v < hi);
+            y.load(a.cache, c_base + v, !whole && v < hi);
+            if (noise_too) g.load(noise, v, v < hi);
+        };
+        g = first;
+        load(lo + tid * 8, again);
+#pragma unroll 1
+        for (int v0 = lo; v0 < hi; v0 += kStep) {
+            const int v = v0 + tid * 8;
+            float key[8], r[8], z[8], top = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) g[j] = first[j];
-            } else {
-                load8<true>(noise, v, g);
+            for (int j = 0; j < 4; ++j) {
+                float p0, p1, q0, q1;
+                x.pair(j, p0, p1);
+                y.pair(j, q0, q1);
+                g.pair(j, z[2 * j], z[2 * j + 1]);
+                r[2 * j] = prob(P, p0, v + 2 * j, c);
+                r[2 * j + 1] = prob(P, p1, v + 2 * j + 1, c);
+                if (!whole) {
+                    r[2 * j] -= prob(Q, q0, v + 2 * j, c);
+                    r[2 * j + 1] -= prob(Q, q1, v + 2 * j + 1, c);
+                }
             }
+            if (v0 + kStep < hi) load(v + kStep, true);        // the next ones on their way
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float r = prob(P, x[j], v + j, c);
-                if (!whole) r -= prob(Q, y[j], v + j, c);
-                // the fast logarithm (within 1e-5 here) tells which few ids
-                // need the exact one
-                if (r > 0.0f && __logf(r) + g[j] >= mine - 1e-3f) {
-                    const float key = logf(r) + g[j];
-                    if (key > mine || best == 0) {
-                        mine = key;
-                        best = pack_key(key, (uint32_t)(v + j));
+                r[j] = v < hi ? fmaxf(r[j], 0.0f) : 0.0f;
+                key[j] = __logf(r[j]) + z[j];
+                top = fmaxf(top, key[j]);
+            }
+            const uint32_t warp_top = __reduce_max_sync(0xffffffffu, ordered_key(top));
+            near = fmaxf(near, key_from_ordered(warp_top) - 1e-3f);
+            if (top >= near) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (r[j] > 0.0f && key[j] >= near) {
+                        const uint64_t k = pack_key(logf(r[j]) + z[j], (uint32_t)(v + j));
+                        best = k > best ? k : best;
                     }
-                }
             }
         }
         return block_max(best, key_s);
     };
     const uint64_t best = best_of(lo, hi, n == N, false);
+    __shared__ uint64_t win_s;
     if (tid == 0) {
         if (best) atomicMax(reinterpret_cast<unsigned long long *>(a.win + b), (unsigned long long)best);
         __threadfence();
-        last_s = atomicAdd(a.arrivals + b, 1u) == gridDim.x - 1;
+        const bool last = atomicAdd(a.arrivals + b, 1u) == gridDim.x - 1;
+        last_s = last;
+        if (last) {
+            __threadfence();
+            win_s = ld_cg_u64(a.win + b);
+            a.win[b] = 0;
+            a.arrivals[b] = 0;
+        }
     }
     __syncthreads();
     if (!last_s) return;
-    __threadfence();
-    uint64_t win = ld_cg_u64(a.win + b);
+    uint64_t win = win_s;
     if (win == 0) win = best_of(0, a.V, true, true);   // p <= q everywhere
-    if (tid == 0) {
-        a.tokens[b * a.tok_s0 + n] = win ? packed_id(win) : 0;
-        a.arrivals[b] = 0;
-    }
+    if (tid == 0) a.tokens[b * a.tok_s0 + n] = win ? packed_id(win) : 0;
 }
 
 template <bool TF32, bool CF32>
 static cudaError_t launch_verify_typed(const VerifyArgs &a, cudaStream_t s) {
-    verify_stats_kernel<TF32, CF32><<<dim3(a.segs, a.rows * (2 * a.N + 1)), kVerifyThreads, 0, s>>>(a);
+    verify_stats_kernel<TF32, CF32><<<a.stat_blocks, kVerifyThreads, 0, s>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.pick_segs, a.rows);
     cfg.blockDim = dim3(kVerifyThreads);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    cfg.gridDim = dim3(a.pick_segs, a.rows);
     return cudaLaunchKernelEx(&cfg, verify_pick_kernel<TF32, CF32>, a);
 }
 
-// Segments of V ids for `rows` rows: about `blocks` blocks, at least one
-// vector of 8 ids a thread.
-static void segments(int V, int rows, int blocks, int *segs, int *len) {
-    const int round = kVerifyThreads * 8;
-    int n = (blocks + rows - 1) / rows;
-    const int most = (V + round - 1) / round;
-    if (n > most) n = most;
-    if (n > kVerifyMaxSegs) n = kVerifyMaxSegs;
-    if (n < 1) n = 1;
-    *len = ((V + n - 1) / n + 7) / 8 * 8;
-    *segs = (V + *len - 1) / *len;
-}
-
 cudaError_t launch_verify(VerifyArgs a, bool target_f32, bool cache_f32, int sms, cudaStream_t s) {
-    segments(a.V, a.rows * (2 * a.N + 1), 24 * sms, &a.segs, &a.seg_len);
-    segments(a.V, a.rows, 12 * sms, &a.pick_segs, &a.pick_len);
+    // whole turns, at most kVerifyMaxSegs segments a row; as many blocks as
+    // there is room for
+    const int turns = (a.V + kTurnIds - 1) / kTurnIds;
+    a.seg_len = (turns + kVerifyMaxSegs - 1) / kVerifyMaxSegs * kTurnIds;
+    a.segs = (a.V + a.seg_len - 1) / a.seg_len;
+    const int64_t tasks = (int64_t)a.rows * (2 * a.N + 1) * a.segs, warps = kVerifyThreads / 32;
+    a.stat_blocks = (int)((tasks + warps - 1) / warps < 4 * sms ? (tasks + warps - 1) / warps : 4 * sms);
+    // the pick: blocks for one wave, a vector of 8 ids a thread at least
+    const int round = kVerifyThreads * 8, most = (a.V + round - 1) / round;
+    int n = 4 * sms / a.rows;
+    if (n < 1) n = 1;
+    if (n > most) n = most;
+    a.pick_len = ((a.V + n - 1) / n + 7) / 8 * 8;
+    a.pick_segs = (a.V + a.pick_len - 1) / a.pick_len;
     if (target_f32)
         return cache_f32 ? launch_verify_typed<true, true>(a, s) : launch_verify_typed<true, false>(a, s);
     return cache_f32 ? launch_verify_typed<false, true>(a, s) : launch_verify_typed<false, false>(a, s);
