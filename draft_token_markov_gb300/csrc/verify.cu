@@ -21,6 +21,7 @@
 namespace dtm {
 
 constexpr int kVerifyThreads = 256;
+constexpr int kSegment = 1024;             // ids; a multiple of a warp's turn
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -158,16 +159,18 @@ struct Running {
     int at;
 };
 
-constexpr int kTurnIds = 1024;             // ids that a warp takes a turn, 4 vectors of 8 a lane
+// vectors of 8 ids that a lane takes a turn: 64 bytes, the next 64 meanwhile
+template <bool F32>
+constexpr int kTurnVectors = F32 ? 2 : 4;
 
 // One turn's vectors, the first from id v on.  Some four instructions an id
 // for a sampled row; a greedy one needs the maxima alone.  A NaN stays in z.
 template <bool F32>
-__device__ __forceinline__ void take_turn(const Raw8<F32> (&x)[4], int v, bool sampled, float c, Running &s) {
+__device__ __forceinline__ void take_turn(const Raw8<F32> (&x)[kTurnVectors<F32>], int v, bool sampled, float c, Running &s) {
     constexpr int kWords = F32 ? 8 : 4;
     uint32_t w = x[0].word(0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kTurnVectors<F32>; ++k)
 #pragma unroll
         for (int j = 0; j < kWords; ++j) w = word_max<F32>(w, x[k].word(j));
     float top = __uint_as_float(F32 ? w : w << 16);
@@ -183,7 +186,7 @@ __device__ __forceinline__ void take_turn(const Raw8<F32> (&x)[4], int v, bool s
     const uint64_t neg = pack_f2(-ref, -ref), c2 = pack_f2(c, c);
     uint64_t sum[2] = {0, 0};
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kTurnVectors<F32>; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float e0, e1;
@@ -212,12 +215,12 @@ __device__ void end_segment(const void *row, int64_t base, int lo, int hi, bool 
         key = segment_key<F32>(row, base, lo, hi);
     } else if (!sampled && m != -INFINITY) {
         // the lowest id of the maximum, among the ids of its turn
-        Raw8<F32> x[4];
+        Raw8<F32> x[kTurnVectors<F32>];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k].load(row, base + s.at + k * 256, s.at + k * 256 < hi);
+        for (int k = 0; k < kTurnVectors<F32>; ++k) x[k].load(row, base + s.at + k * 256, s.at + k * 256 < hi);
         int id = INT_MAX;
 #pragma unroll
-        for (int k = 3; k >= 0; --k)
+        for (int k = kTurnVectors<F32> - 1; k >= 0; --k)
 #pragma unroll
             for (int j = 3; j >= 0; --j) {
                 float e0, e1;
@@ -249,21 +252,22 @@ __device__ __forceinline__ void take_segment(const void *row, int64_t base, int 
                                              uint4 *out) {
     const int lane8 = (threadIdx.x & 31) * 8;
     Running s{-INFINITY, 0.0f, lo + lane8};
-    Raw8<F32> x[4], y[4];
-    auto load = [&](int v, Raw8<F32> (&x)[4]) {
+    constexpr int kV = kTurnVectors<F32>, kTurn = kV * 256;
+    Raw8<F32> x[kV], y[kV];
+    auto load = [&](int v, Raw8<F32> (&x)[kV]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k].load(row, base + v + k * 256, v + k * 256 < hi);
+        for (int k = 0; k < kV; ++k) x[k].load(row, base + v + k * 256, v + k * 256 < hi);
     };
     // two turns a round, each loaded while the other is taken
     load(lo + lane8, x);
 #pragma unroll 1
-    for (int v = lo + lane8; v - lane8 < hi; v += 2 * kTurnIds) {
-        const bool second = v - lane8 + kTurnIds < hi;
-        if (second) load(v + kTurnIds, y);
+    for (int v = lo + lane8; v - lane8 < hi; v += 2 * kTurn) {
+        const bool second = v - lane8 + kTurn < hi;
+        if (second) load(v + kTurn, y);
         take_turn<F32>(x, v, sampled, c, s);
         if (!second) break;
-        if (v - lane8 + 2 * kTurnIds < hi) load(v + 2 * kTurnIds, x);
-        take_turn<F32>(y, v + kTurnIds, sampled, c, s);
+        if (v - lane8 + 2 * kTurn < hi) load(v + 2 * kTurn, x);
+        take_turn<F32>(y, v + kTurn, sampled, c, s);
     }
     end_segment<F32>(row, base, lo, hi, sampled, c, s, out);
 }
@@ -504,10 +508,10 @@ static cudaError_t launch_verify_typed(const VerifyArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_verify(VerifyArgs a, bool target_f32, bool cache_f32, int sms, cudaStream_t s) {
-    // whole turns, at most kVerifyMaxSegs segments a row; as many blocks as
+    // segments of whole turns, at most kVerifyMaxSegs segments a row; as many blocks as
     // there is room for
-    const int turns = (a.V + kTurnIds - 1) / kTurnIds;
-    a.seg_len = (turns + kVerifyMaxSegs - 1) / kVerifyMaxSegs * kTurnIds;
+    const int turns = (a.V + kSegment - 1) / kSegment;
+    a.seg_len = (turns + kVerifyMaxSegs - 1) / kVerifyMaxSegs * kSegment;
     a.segs = (a.V + a.seg_len - 1) / a.seg_len;
     const int64_t tasks = (int64_t)a.rows * (2 * a.N + 1) * a.segs, warps = kVerifyThreads / 32;
     a.stat_blocks = (int)((tasks + warps - 1) / warps < 4 * sms ? (tasks + warps - 1) / warps : 4 * sms);
