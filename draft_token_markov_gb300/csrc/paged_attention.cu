@@ -68,7 +68,7 @@ struct PaShape {
     // tiles, slot 1's m and l, barriers, the schedule
     static constexpr int kExchange = 2 * kQBytes + kStages * kKvBytes;
     static constexpr int kBars = kExchange + 2 * kPaTile * 4;
-    static constexpr int kMisc = kBars + 8 * (2 * kStages + 15 + 2 * kRing);
+    static constexpr int kMisc = kBars + 8 * (2 * kStages + 13 + 2 * kRing);
     static constexpr int kSmem = kMisc + 512;
 };
 
@@ -253,34 +253,60 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     return bf16x2_rn(lo, hi);
 }
 
-// Four MMAs, their operands `da` and `db` (in the descriptors' 16-byte units;
-// TMEM columns for an A there) apart.  Called by the whole warp, an elected
-// lane issues.
-__device__ __forceinline__ void mma4_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{ .reg .pred p, q; .reg .b64 a1, a2, a3, b1, b2, b3;\n"
-        "setp.ne.u32 q, %4, 0; elect.sync _|p, 0xffffffff;\n"
-        "add.s64 a1, %1, 2; add.s64 a2, %1, 4; add.s64 a3, %1, 6;\n"
-        "add.s64 b1, %2, 2; add.s64 b2, %2, 4; add.s64 b3, %2, 6;\n"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, q;\n"
-        "setp.eq.u32 q, 0, 0;\n"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, q;\n"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, q;\n"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, q; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+// The MMAs of one product, issued by an elected lane of the whole warp, in one
+// block with one election: 4 (D = 64) or 8 steps of 16 along the scores' inner
+// dimension, 8 along a tile's keys.  Operands advance in the descriptors'
+// 16-byte units, the A operand in TMEM in columns.
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    if (D == 64) {
+        asm volatile(
+            "{ .reg .pred p, f, t; .reg .b64 a1, a2, a3, b1, b2, b3;\n"
+            "setp.ne.u32 f, 0, 0; setp.eq.u32 t, 0, 0; elect.sync _|p, 0xffffffff;\n"
+            "add.s64 a1, %1, 2; add.s64 a2, %1, 4; add.s64 a3, %1, 6;\n"
+            "add.s64 b1, %2, 2; add.s64 b2, %2, 4; add.s64 b3, %2, 6;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
+    } else {
+        asm volatile(
+            "{ .reg .pred p, f, t; .reg .b64 a1, a2, a3, a4, a5, a6, a7, b1, b2, b3, b4, b5, b6, b7;\n"
+            "setp.ne.u32 f, 0, 0; setp.eq.u32 t, 0, 0; elect.sync _|p, 0xffffffff;\n"
+            "add.s64 a1, %1, 2; add.s64 a2, %1, 4; add.s64 a3, %1, 6; add.s64 a4, %1, 1024;\n"
+            "add.s64 a5, %1, 1026; add.s64 a6, %1, 1028; add.s64 a7, %1, 1030;\n"
+            "add.s64 b1, %2, 2; add.s64 b2, %2, 4; add.s64 b3, %2, 6; add.s64 b4, %2, 1024;\n"
+            "add.s64 b5, %2, 1026; add.s64 b6, %2, 1028; add.s64 b7, %2, 1030;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, f;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b4, %3, t;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b5, %3, t;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a6, b6, %3, t;\n"
+            "@p tcgen05.mma.cta_group::1.kind::f16 [%0], a7, b7, %3, t; }" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
+            : "memory");
+    }
 }
-__device__ __forceinline__ void mma4_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{ .reg .pred p, q; .reg .b32 a1, a2, a3; .reg .b64 b1, b2, b3;\n"
-        "setp.ne.u32 q, %4, 0; elect.sync _|p, 0xffffffff;\n"
-        "add.s32 a1, %1, 8; add.s32 a2, %1, 16; add.s32 a3, %1, 24;\n"
-        "add.s64 b1, %2, 128; add.s64 b2, %2, 256; add.s64 b3, %2, 384;\n"
+        "{ .reg .pred p, q, t; .reg .b32 a1, a2, a3, a4, a5, a6, a7; .reg .b64 b1, b2, b3, b4, b5, b6, b7;\n"
+        "setp.ne.u32 q, %4, 0; setp.eq.u32 t, 0, 0; elect.sync _|p, 0xffffffff;\n"
+        "add.s32 a1, %1, 8; add.s32 a2, %1, 16; add.s32 a3, %1, 24; add.s32 a4, %1, 32;\n"
+        "add.s32 a5, %1, 40; add.s32 a6, %1, 48; add.s32 a7, %1, 56;\n"
+        "add.s64 b1, %2, 128; add.s64 b2, %2, 256; add.s64 b3, %2, 384; add.s64 b4, %2, 512;\n"
+        "add.s64 b5, %2, 640; add.s64 b6, %2, 768; add.s64 b7, %2, 896;\n"
         "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, q;\n"
-        "setp.eq.u32 q, 0, 0;\n"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, q;\n"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, q;\n"
-        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, q; }" ::"r"(d),
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b4, %3, t;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b5, %3, t;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a6], b6, %3, t;\n"
+        "@p tcgen05.mma.cta_group::1.kind::f16 [%0], [a7], b7, %3, t; }" ::"r"(d),
         "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
@@ -358,9 +384,9 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t kv_full = tc::smem_u32(base + S::kBars), kv_empty = kv_full + 8 * S::kStages;
     const uint32_t q_full = kv_empty + 8 * S::kStages, q_empty = q_full + 16, s_full = q_full + 32,
-                   p_full = q_full + 48, pv_done = q_full + 80,
-                   merge_full = q_full + 96, merge_free = q_full + 104, leave = q_full + 112,
-                   item_full = q_full + 120, item_empty = item_full + 8 * kRing;
+                   p_full = q_full + 48, pv_done = q_full + 64,
+                   merge_full = q_full + 80, merge_free = q_full + 88, leave = q_full + 96,
+                   item_full = q_full + 104, item_empty = item_full + 8 * kRing;
     if (tid == 0) {
         sh.abort = 0;
         for (int i = 0; i < S::kStages; ++i) {
@@ -371,8 +397,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             tc::mbar_init(q_full + 8 * i, 1);
             tc::mbar_init(q_empty + 8 * i, 1);
             tc::mbar_init(s_full + 8 * i, 1);
-            tc::mbar_init(p_full + 16 * i, 4);       // the slot's warps, the halves of P
-            tc::mbar_init(p_full + 16 * i + 8, 4);
+            tc::mbar_init(p_full + 8 * i, 4);        // the slot's warps
             tc::mbar_init(pv_done + 8 * i, 1);
         }
         tc::mbar_init(merge_full, 4);                // slot 1's warps
@@ -620,78 +645,117 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         // ---------------------------------------------------- MMA issue
         // the whole warp, so that control flow and descriptors stay uniform;
         // an elected lane issues
-        uint32_t at = 0, q_phase = 0, p_phase = 0;   // a bit a slot
+        uint32_t q_phase = 0, p_phase = 0;           // a bit a slot
         bool ok = true;
-        const uint32_t q_addr = tc::smem_u32(q_smem), kv_addr = tc::smem_u32(kv_smem);
         constexpr uint32_t kIdescS = pa_idesc<F16>(kPaTile, false), kIdescO = pa_idesc<F16>(D, true);
-        auto loaded = [&](uint32_t k) { return all_wait(kv_full + 8 * stage_of(k), phase_of(k), 0x200); };
-        auto scores = [&](int slot, int q_tile, uint32_t k) {
-            const uint32_t q0 = q_addr + q_tile * S::kQBytes, k0 = kv_addr + stage_of(k) * S::kKvBytes;
-#pragma unroll
-            for (int i = 0; i < S::kHalves; ++i)
-                mma4_smem(tmem + slot * kPaTile, tc::sw128_desc(q0 + i * S::kHalf),
-                          tc::sw128_desc(k0 + i * S::kHalf), kIdescS, i > 0);
+        constexpr uint32_t kStep = S::kKvBytes / 16;
+        const uint64_t q_desc = tc::sw128_desc(tc::smem_u32(q_smem)), k_desc = tc::sw128_desc(tc::smem_u32(kv_smem)),
+                       v_desc = sw128_mn_desc(tc::smem_u32(kv_smem), S::kHalf);
+        const uint32_t t_o = tmem + 2 * kPaTile;
+        // a place in the ring of key and value tiles
+        struct Place {
+            uint32_t stage, phase;
+            __device__ __forceinline__ Place after(int n) const {
+                Place p{stage + n, phase};
+                if (p.stage >= S::kStages) { p.stage -= S::kStages; p.phase ^= 1; }
+                return p;
+            }
+        };
+        auto loaded = [&](Place k) { return all_wait(kv_full + 8 * k.stage, k.phase, 0x200); };
+        auto scores = [&](int slot, int q_tile, Place k) {
+            mma_scores<D>(tmem + slot * kPaTile, q_desc + q_tile * (S::kQBytes / 16), k_desc + k.stage * kStep, kIdescS);
             tc::commit_elect(s_full + 8 * slot);
         };
-        auto values = [&](int slot, uint32_t v, int half, bool accumulate) {
-            mma4_tmem(tmem + 2 * kPaTile + slot * D, tmem + slot * kPaTile + half * 32,
-                      sw128_mn_desc(kv_addr + stage_of(v) * S::kKvBytes + half * 4 * 2048, S::kHalf), kIdescO,
-                      accumulate);
+        // O += P V, once the slot's P is there
+        auto values = [&](int slot, Place v, bool accumulate) {
+            if (!all_wait(p_full + 8 * slot, p_phase >> slot & 1, 0x220 + slot)) return false;
+            p_phase ^= 1u << slot;
+            tc::fence_after_sync();
+            mma_values(t_o + slot * D, tmem + slot * kPaTile, v_desc + v.stage * kStep, kIdescO, accumulate);
+            return true;
         };
-        auto release = [&](uint32_t k) { tc::commit_elect(kv_empty + 8 * stage_of(k)); };
+        auto release = [&](Place k) { tc::commit_elect(kv_empty + 8 * k.stage); };
+        auto queries = [&](int tile) {
+            const bool r = all_wait(q_full + 8 * tile, q_phase >> tile & 1, 0x210 + tile);
+            q_phase ^= 1u << tile;
+            return r;
+        };
+        Place k{0, 0};                               // the next key tile for scores
         for (uint32_t n = 0; ok; ++n) {
             ok = item_wait(n);
             const int tokens = item(n).tokens, steps = item(n).steps;
             if (!ok || tokens == 0) break;
             item_done(n);
             if (steps <= 0) continue;                // nothing seen: the output is written without MMAs
-            const bool two = tokens > a.tile_tokens; // row tiles
-            // the first scores
-#pragma unroll 1
-            for (int s = 0; ok && s < 2; ++s) {
-                if (!two && s == steps) break;
-                const uint32_t k = at + (two ? 0 : 2 * s);
-                ok = loaded(k);
-                if (ok && (two || s == 0)) {
-                    ok = all_wait(q_full + 8 * s, q_phase >> s & 1, 0x210 + s);
-                    q_phase ^= 1u << s;
-                }
+            // Either way a slot's turn is: its P comes, O += P V, the next
+            // scores over P's place (MMAs run in the order of their issue).
+            Place v = k.after(1);
+            if (tokens > a.tile_tokens) {
+                // two row tiles, a slot each, every key tile for both
+                ok = queries(0) && loaded(k);
                 if (!ok) break;
                 tc::fence_after_sync();
-                scores(s, two ? s : 0, k);
-                if (!two || s == 1) release(k);
-                if (two ? steps == 1 : s + 1 == min(steps, 2) && steps <= 2) tc::commit_elect(q_empty + (two ? 8 * s : 0));
-            }
+                scores(0, 0, k);
+                ok = queries(1);
+                if (!ok) break;
+                tc::fence_after_sync();
+                scores(1, 1, k);
+                release(k);
+                k = k.after(2);
 #pragma unroll 1
-            for (int j = 0; ok && j < steps; ++j) {
-                const uint32_t v = at + 2 * j + 1;
-                const int ahead = two ? 1 : 2;       // key tiles to the slot's next scores
-#pragma unroll 1
-                for (int s = two ? 0 : j & 1, e = two ? 2 : s + 1; ok && s < e; ++s) {
-                    ok = loaded(v);
-#pragma unroll 1
-                    for (int half = 0; ok && half < 2; ++half) {
-                        ok = all_wait(p_full + 16 * s + 8 * half, p_phase >> s & 1, 0x220 + s);
-                        if (!ok) break;
-                        tc::fence_after_sync();
-                        values(s, v, half, j >= ahead || half > 0);
-                    }
+                for (int j = 1; j < steps; ++j) {
+                    ok = loaded(v) && values(0, v, j > 1) && loaded(k);
                     if (!ok) break;
-                    p_phase ^= 1u << s;
-                    tc::commit_elect(pv_done + 8 * s);
-                    if (s == e - 1) release(v);
-                    if (j + ahead < steps) {
-                        const uint32_t k = at + 2 * (j + ahead);
+                    scores(0, 0, k);
+                    ok = values(1, v, j > 1);
+                    if (!ok) break;
+                    release(v);
+                    scores(1, 1, k);
+                    release(k);
+                    v = v.after(2);
+                    k = k.after(2);
+                }
+                if (!ok) break;
+                tc::commit_elect(q_empty);
+                tc::commit_elect(q_empty + 8);
+                ok = loaded(v);
+#pragma unroll 1
+                for (int s = 0; ok && s < 2; ++s) {
+                    ok = values(s, v, steps > 1);
+                    if (ok) tc::commit_elect(pv_done + 8 * s);
+                }
+                release(v);
+            } else {
+                // one: the key tiles in turn
+                ok = queries(0);
+#pragma unroll 1
+                for (int j = 0; ok && j < steps && j < 2; ++j) {
+                    ok = loaded(k);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    scores(j, 0, k);
+                    release(k);
+                    k = k.after(2);
+                }
+                if (steps <= 2) tc::commit_elect(q_empty);
+#pragma unroll 1
+                for (int j = 0; ok && j < steps; ++j) {
+                    ok = loaded(v) && values(j & 1, v, j > 1);
+                    if (!ok) break;
+                    release(v);                      // before the wait for keys: the loads may need the place
+                    v = v.after(2);
+                    if (j + 2 < steps) {
                         ok = loaded(k);
                         if (!ok) break;
-                        tc::fence_after_sync();
-                        scores(s, two ? s : 0, k);
-                        if (s == e - 1) release(k);
-                        if (j + ahead + 1 == steps) tc::commit_elect(q_empty + (two ? 8 * s : 0));
+                        scores(j & 1, 0, k);
+                        release(k);
+                        if (j + 3 == steps) tc::commit_elect(q_empty);
+                        k = k.after(2);
+                    } else {
+                        tc::commit_elect(pv_done + 8 * (j & 1));
                     }
                 }
             }
-            at += 2 * steps;
         }
         if (sh.abort) {
             // gave up: no MMA may be in flight when the block leaves
@@ -819,28 +883,21 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                             p[e] = pack2<F16>(p0, p1);
                         }
                         tc::st_32x32b_x16(t_s + 16 * k, p);
-                        if (k == 1) {                 // half of P: its MMAs may start
-                            tc::wait_st();
-                            tc::fence_before_sync();
-                            arrive(p_full + 16 * slot);
-                        }
                     }
                     float s0, s1;
                     split2(add2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;
                     tc::wait_st();
-                } else {
-                    arrive(p_full + 16 * slot);
                 }
                 any = true;
                 tc::fence_before_sync();
-                arrive(p_full + 16 * slot + 8);
-                pv_phase ^= 1;                        // one more PV to come
+                arrive(p_full + 8 * slot);
             }
             if (!ok) break;
             at += 2 * steps;
             if (any) {
-                ok = all_wait(pv_done + 8 * slot, pv_phase ^ 1, 0x430 + slot);
+                ok = all_wait(pv_done + 8 * slot, pv_phase, 0x430 + slot);
+                pv_phase ^= 1;
                 if (!ok) break;
                 tc::fence_after_sync();
             }
