@@ -21,8 +21,9 @@
 // and its odd ones in slot 1, and the two are joined at its end (O of both
 // slots lies in the same TMEM lanes).
 //
-// Work.  An item weighs kWeight and one for each of its key tiles, two where
-// it has two row tiles (a slot's turn then does one of them, not half of both).
+// Work.  An item weighs one for each of its key tiles, two where it has two
+// row tiles (a slot's turn then does one of them, not half of both), and a few
+// more for its start and end.
 // The items of the call, in order of request, key head and rows, lie end to
 // end, and the whole is cut into one range of equal weight a block, whatever
 // the lengths; a key tile belongs to the block that its last unit falls to.  A
@@ -56,7 +57,11 @@ constexpr int kPaThreads = 384;
 constexpr int kRing = 4;                     // items that are known ahead
 constexpr int kPaTile = 128;                 // keys of a tile, and rows
 constexpr float kLazy = 8.0f;
-constexpr int kWeight = 4;                   // an item's start and end, in single key tiles
+// an item's start and end, in key tiles of one row tile (the largest block
+// of a mixed batch measured 110, 94, 85, 87, 92 us at 2, 4, 6, 8, 11 for both
+// kinds; batches of single row tiles, which stream keys meanwhile, lose 1% for
+// each)
+constexpr int kWeightOne = 3, kWeightTwo = 7;
 
 template <int D>
 struct PaShape {
@@ -119,16 +124,20 @@ __device__ __forceinline__ void pa_span(const AttnArgs &a, const PaReq &q, int m
     it.steps = it.sink_tiles + nw;
 }
 
-// An item's weight, and how many of its key tiles begin before an offset.
+// An item's weight: its start and end, its key tiles.
 __device__ __forceinline__ int pa_tile_weight(const AttnArgs &a, const PaItem &it) {
     return it.tokens > a.tile_tokens ? 2 : 1;
 }
-__device__ __forceinline__ uint32_t pa_weight(const AttnArgs &a, const PaItem &it) {
-    return kWeight + max(it.steps, 1) * pa_tile_weight(a, it);
+__device__ __forceinline__ int pa_ends_weight(const AttnArgs &a, const PaItem &it) {
+    return it.tokens > a.tile_tokens ? kWeightTwo : kWeightOne;
 }
+__device__ __forceinline__ uint32_t pa_weight(const AttnArgs &a, const PaItem &it) {
+    return pa_ends_weight(a, it) + max(it.steps, 1) * pa_tile_weight(a, it);
+}
+// How many of its key tiles end before an offset.
 __device__ __forceinline__ int pa_tile_at(const AttnArgs &a, const PaItem &it, uint32_t off) {
-    if (off <= kWeight) return 0;
-    return min((int)(off - kWeight) / pa_tile_weight(a, it), max(it.steps, 1));
+    const int past = (int)off - pa_ends_weight(a, it);
+    return past <= 0 ? 0 : min(past / pa_tile_weight(a, it), max(it.steps, 1));
 }
 __device__ __noinline__ uint32_t pa_units(const AttnArgs &a, PaReq q, int m) {
     PaItem it;
@@ -529,7 +538,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     it.h = h;
                     it.c0 = it.c1 = blockIdx.x;
                     if (it.j0 > 0 || j1 < all) {
-                        it.c0 = split.block_of(u + kWeight + weight - 1);
+                        it.c0 = split.block_of(u + pa_ends_weight(a, it) + weight - 1);
                         it.c1 = split.block_of(u + units - 1);
                     }
                     it.steps = min(j1, it.steps) - it.j0;    // 0 where nothing is seen
