@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(THREADS) paged_layout_kernel(LayoutArgs a) {
     __shared__ int taken_s;
     __shared__ uint32_t last_s;
     const int tid = threadIdx.x;
-    if (ld_acquire_u32(a.status) != 0u) return;
+    if (__ldcg(a.status) != 0u) return;
     if (tid == 0) taken_s = 0;
 
     const int64_t C = a.ring_size;
@@ -192,32 +192,44 @@ cudaError_t launch_paged_layout(const LayoutArgs &a, cudaStream_t s) {
 // ------------------------------------------------------------------- write
 //
 // A copy of 16-byte vectors; bound by memory (or, for a draft step's tokens,
-// by the launch).  A thread moves one vector of the keys and the same one of
-// the values, so two loads are in flight from it.
+// by the launch).  A thread moves two vectors of the keys and the same two of
+// the values, a grid's width apart: four loads are in flight from it.
 
 constexpr int kWriteThreads = 256;
 
 __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(WriteArgs a) {
-    if (ld_acquire_u32(a.status) != 0u) return;
+    if (__ldcg(a.status) != 0u) return;
     const int64_t total = ((int64_t)a.T * a.heads) << a.vec_shift;
     const int64_t step = (int64_t)gridDim.x * kWriteThreads;
-    for (int64_t i = (int64_t)blockIdx.x * kWriteThreads + threadIdx.x; i < total; i += step) {
-        const int d = (int)(i & ((1 << a.vec_shift) - 1));
-        const uint32_t th = (uint32_t)(i >> a.vec_shift);
-        const uint32_t t = th / (uint32_t)a.heads, h = th - t * (uint32_t)a.heads;
-        const uint4 k = __ldg(a.k.src + t * a.k.src_s0 + h * a.k.src_s1 + d);
-        const uint4 v = __ldg(a.v.src + t * a.v.src_s0 + h * a.v.src_s1 + d);
-        const int64_t slot = __ldg(a.slots + t);
-        if (slot < 0 || slot >= a.num_slots) continue;
-        const int64_t page = slot >> a.page_shift, at = slot & ((1 << a.page_shift) - 1);
-        a.k.dst[page * a.k.s_page + at * a.k.s_slot + h * a.k.s_head + d] = k;
-        a.v.dst[page * a.v.s_page + at * a.v.s_slot + h * a.v.s_head + d] = v;
+    for (int64_t i0 = (int64_t)blockIdx.x * kWriteThreads + threadIdx.x; i0 < total; i0 += 2 * step) {
+        uint4 k[2], v[2];
+        int64_t slot[2] = {-1, -1};
+        uint32_t h[2];
+        int d[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int64_t i = i0 + e * step;
+            if (i >= total) break;
+            const uint32_t th = (uint32_t)(i >> a.vec_shift), t = th / (uint32_t)a.heads;
+            d[e] = (int)(i & ((1 << a.vec_shift) - 1));
+            h[e] = th - t * (uint32_t)a.heads;
+            slot[e] = __ldg(a.slots + t);
+            k[e] = __ldcs(a.k.src + t * a.k.src_s0 + h[e] * a.k.src_s1 + d[e]);
+            v[e] = __ldcs(a.v.src + t * a.v.src_s0 + h[e] * a.v.src_s1 + d[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (slot[e] < 0 || slot[e] >= a.num_slots) continue;
+            const int64_t page = slot[e] >> a.page_shift, at = slot[e] & ((1 << a.page_shift) - 1);
+            a.k.dst[page * a.k.s_page + at * a.k.s_slot + h[e] * a.k.s_head + d[e]] = k[e];
+            a.v.dst[page * a.v.s_page + at * a.v.s_slot + h[e] * a.v.s_head + d[e]] = v[e];
+        }
     }
 }
 
 cudaError_t launch_paged_write(const WriteArgs &a, cudaStream_t s) {
     const int64_t total = ((int64_t)a.T * a.heads) << a.vec_shift;
-    int64_t blocks = (total + kWriteThreads - 1) / kWriteThreads;
+    int64_t blocks = (total + 2 * kWriteThreads - 1) / (2 * kWriteThreads);
     if (blocks > 65535) blocks = 65535;
     paged_write_kernel<<<(int)blocks, kWriteThreads, 0, s>>>(a);
     return cudaGetLastError();
