@@ -525,7 +525,9 @@ markov_status markov_paged_write(markov_paged_plan *plan, const void *key, int64
  * window, foreign pages) may hold anything, NaN included, and table entries
  * for them are not read; page ids outside [0, num_pages) read as zeros.
  * Keys that one token of the row sees and another does not may be anything
- * too, values there must be finite.  Two launches.  EINVAL for a bad shape,
+ * too, values there must be finite.  A call of 2^31 and more key tiles (128
+ * keys of a key head, for up to 256 rows of query heads) computes nothing and
+ * records MARKOV_EUNSUPPORTED for markov_paged_plan_status.  Two launches.  EINVAL for a bad shape,
  * stride or alignment, a table row of more than 2^30 keys, or 2^30 and more
  * tokens times q_heads / kv_heads. */
 markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int64_t q_s0,

@@ -359,6 +359,42 @@ def test_many_ragged_rows(gpu_lib, mean):
     both(gpu_lib, Case(reqs, 4, 2, 64, 8, torch.float16 if mean else torch.bfloat16, seed=13, mean=mean))
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(128, 1, 64), (100, 1, 128), (129 * 1, 3, 64), (256, 2, 64)])
+def test_large_groups(gpu_lib, hq, hkv, d):
+    """Groups that fill a row tile, leave some of it, or all but one row."""
+    both(gpu_lib, Case([(50, 3), (200, 1), (0, 2)], hq, hkv, d, 16, seed=hq))
+
+
+def test_a_thousand_rows(gpu_lib):
+    rng = np.random.default_rng(2)
+    reqs = [(int(c), 1) for c in rng.integers(0, 40, 1000)]
+    reqs[700] = (5000, 3)
+    both(gpu_lib, Case(reqs, 2, 1, 64, 8, seed=19, padding=(0, 31, 32, 999)))
+
+
+def test_window_and_first_tokens_far_apart(gpu_lib):
+    """Key tiles of the first tokens and of the window, with many between."""
+    c = Case([(3000, 9), (5000, 1), (2500, 300)], 4, 2, 128, 32, seed=20)
+    both(gpu_lib, c, window=130, sinks=200)
+    both(gpu_lib, c, window=1, sinks=129)
+
+
+def test_more_key_tiles_than_are_counted(gpu_lib):
+    """2^31 key tiles of work: refused on the device, nothing is written."""
+    api = gpu_lib
+    plan = api.PagedPlan(256, 256, 64, 256, torch.bfloat16, max_rows=1)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cache = torch.zeros((1, 256, 256, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((1, 256, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, SENT)
+    api.markov_paged_attention(plan, q, cache, cache.clone(), torch.full((1, 1 << 22), -1, **i32),
+                               torch.zeros(1, dtype=torch.int64, device="cuda"), torch.tensor([0, 1], **i32),
+                               torch.tensor([1 << 30], **i32), out=out)
+    assert api.markov_paged_plan_status(plan) == 2 and bool((out == SENT).all())
+    assert api.markov_paged_plan_status(plan) == 0
+    plan.close()
+
+
 def test_one_long_row_is_split(gpu_lib):
     """One token over a long cache, where blocks share the row."""
     for dtype, d, reqs in ((torch.bfloat16, 128, [(20000, 1)]), (torch.float16, 64, [(9000, 9), (17, 1)])):
