@@ -99,18 +99,26 @@ struct PaReq {
     int state;                 // its table row, -1 for none
 };
 
-__device__ __noinline__ PaReq pa_request(const AttnArgs &a, int r) {
+// A row's lengths as the caller gave them.
+struct PaRaw {
+    int64_t state;
+    int qs, qe, len;
+};
+
+__device__ __forceinline__ PaRaw pa_load(const AttnArgs &a, int r) {
+    return PaRaw{__ldg(a.idx + r), __ldg(a.query_start + r), __ldg(a.query_start + r + 1), __ldg(a.seq_lens + r)};
+}
+
+__device__ __forceinline__ PaReq pa_request(const AttnArgs &a, const PaRaw &w) {
     PaReq q;
-    const int64_t s = __ldg(a.idx + r);
-    q.qs = __ldg(a.query_start + r);
-    const int n = __ldg(a.query_start + r + 1) - q.qs;
-    int len = __ldg(a.seq_lens + r);
-    if (len < 0) len = 0;
-    q.np = s < 0 || q.qs < 0 || q.qs >= a.T || n < 0 ? 0 : min(n, a.T - q.qs);
-    q.pos0 = len - n;
-    q.state = s < a.num_states ? (int)s : -1;
+    q.qs = w.qs;
+    const int n = w.qe - w.qs;
+    q.np = w.state < 0 || q.qs < 0 || q.qs >= a.T || n < 0 ? 0 : min(n, a.T - q.qs);
+    q.pos0 = max(w.len, 0) - n;
+    q.state = w.state < a.num_states ? (int)w.state : -1;
     return q;
 }
+__device__ __noinline__ PaReq pa_request(const AttnArgs &a, int r) { return pa_request(a, pa_load(a, r)); }
 
 // The m-th pair of row tiles of a request: its keys and its key tiles (none
 // where nothing is seen; it counts as one unit then).
@@ -423,11 +431,11 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         tc::mbar_init_fence();
     }
     // the scan's first loads are on their way while the block sets up
-    PaReq q{0, 0, 0, 0};
+    PaRaw raw{-1, 0, 0, 0};
     uint32_t pending = 0;
     if (warp == 11) {
         pending = __ldcg(a.status);                  // a pending status: nothing is done
-        if (lane < a.rows) q = pa_request(a, lane);
+        if (lane < a.rows) raw = pa_load(a, lane);
     }
     if (warp >= 9 && lane == 0) {
         const CUtensorMap *map = warp == 9 ? &kmap : warp == 10 ? &vmap : &qmap;
@@ -459,30 +467,38 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     if (warp == 11) {
         // ------------------------------------------- the walk, query loads
         PaItem it;
-        int64_t total = 0;
-        // the rows' units before and with each, where key tiles will be
+        uint64_t total = 0;
+        bool over = false;
+        // the rows' units before and with each, where key tiles will be (of
+        // 32 rows and less a lane keeps its own)
         uint32_t *units_to = reinterpret_cast<uint32_t *>(kv_smem);
+        const bool few = a.rows <= 32;
+        PaReq q{0, 0, 0, 0};
+        uint32_t own = 0, incl = 0;
 #pragma unroll 1
         for (int r0 = 0; r0 < a.rows; r0 += 32) {
             if (r0 > 0) {
-                q.np = 0;
-                if (r0 + lane < a.rows) q = pa_request(a, r0 + lane);
+                raw.state = -1;
+                if (r0 + lane < a.rows) raw = pa_load(a, r0 + lane);
             }
+            q = pa_request(a, raw);
             const int pairs = pa_pairs(a, q);
-            int64_t x = 0;
+            uint64_t x = 0;
 #pragma unroll 1
             for (int m = 0; m < pairs; ++m) x += pa_units(a, q, m);
             x *= a.kv_heads;
+            over |= x >> 27 != 0;                    // 32 rows' sum stays below 2^32
+            own = incl = (uint32_t)x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-                if (lane >= o) x += y;
+                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
             }
-            units_to[r0 + lane] = (uint32_t)(total + x);
-            total += __shfl_sync(0xffffffffu, x, 31);
+            if (!few) units_to[r0 + lane] = (uint32_t)total + incl;
+            total += __shfl_sync(0xffffffffu, incl, 31);
         }
         __syncwarp();
-        if (total > INT32_MAX) {                     // units are counted in 32 bits
+        if (__any_sync(0xffffffffu, over) || total > INT32_MAX) {     // units are counted in 32 bits
             if (lane == 0 && !pending) set_status(a.status, 2u /* MARKOV_EUNSUPPORTED */, 0x600);
             total = 0;
         }
@@ -493,24 +509,32 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         if (blockIdx.x < split.blocks) {
             const uint32_t u0 = u_begin = split.first(blockIdx.x);
             u_end = split.first(blockIdx.x + 1);
-            for (int r0 = 0;; r0 += 32) {
-                const int x = r0 + lane;
-                const bool here = x < a.rows && u0 < units_to[x] && (x == 0 || u0 >= units_to[x - 1]);
-                const uint32_t found = __ballot_sync(0xffffffffu, here);
-                if (found) { r = r0 + __ffs(found) - 1; break; }
-            }
-            const uint32_t before = r ? units_to[r - 1] : 0u, head = (units_to[r] - before) / a.kv_heads;
-            if (a.rows <= 32) {                      // a lane has it
+            uint32_t before, units;                  // of the row that holds the first unit
+            if (few) {
+                r = __ffs(__ballot_sync(0xffffffffu, u0 < incl && u0 >= incl - own)) - 1;
+                before = __shfl_sync(0xffffffffu, incl - own, r);
+                units = __shfl_sync(0xffffffffu, own, r);
                 q.np = __shfl_sync(0xffffffffu, q.np, r);
                 q.qs = __shfl_sync(0xffffffffu, q.qs, r);
                 q.pos0 = __shfl_sync(0xffffffffu, q.pos0, r);
                 q.state = __shfl_sync(0xffffffffu, q.state, r);
             } else {
+#pragma unroll 1
+                for (int r0 = 0;; r0 += 32) {
+                    const int x = r0 + lane;
+                    const bool here = x < a.rows && u0 < units_to[x] && (x == 0 || u0 >= units_to[x - 1]);
+                    const uint32_t found = __ballot_sync(0xffffffffu, here);
+                    if (found) { r = r0 + __ffs(found) - 1; break; }
+                }
+                before = r ? units_to[r - 1] : 0u;
+                units = units_to[r] - before;
                 q = pa_request(a, r);
             }
             pairs = pa_pairs(a, q);
+            const uint32_t head = units / a.kv_heads;
             h = (u0 - before) / head;
             u = before + h * head;
+#pragma unroll 1
             for (;; ++m) {
                 const uint32_t units = pa_units(a, q, m);
                 if (u0 - u < units) break;
