@@ -229,7 +229,7 @@ markov_status markov_paged_write(markov_paged_plan *p, const void *key, int64_t 
                                  int64_t value_s1, const markov_cache_view *k_cache,
                                  const markov_cache_view *v_cache, const int64_t *slots,
                                  int32_t num_tokens, void *stream) {
-    if (!p || num_tokens < 0) return MARKOV_EINVAL;
+    if (!p || num_tokens < 0 || (int64_t)num_tokens * p->d.kv_heads > INT32_MAX) return MARKOV_EINVAL;
     if (num_tokens == 0) return MARKOV_OK;
     if (!valid_rows(key, key_s0, key_s1, p->d) || !valid_rows(value, value_s0, value_s1, p->d) ||
         !valid_view(k_cache, p->d) || !valid_view(v_cache, p->d) || !slots ||

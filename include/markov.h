@@ -499,7 +499,8 @@ typedef struct markov_cache_view {
 /* Store keys and values [num_tokens, kv_heads, head_dim] at their slots.
  * key / value: element (t, h, d) at t * s0 + h * s1 + d, strides multiples
  * of 8, 16-byte aligned.  Tokens whose slot is negative or not below
- * num_pages * page_size are skipped; slots are distinct. */
+ * num_pages * page_size are skipped; slots are distinct.  EINVAL where
+ * num_tokens * kv_heads does not fit 31 bits. */
 markov_status markov_paged_write(markov_paged_plan *plan, const void *key, int64_t key_s0,
                                  int64_t key_s1, const void *value, int64_t value_s0,
                                  int64_t value_s1, const markov_cache_view *k_cache,
