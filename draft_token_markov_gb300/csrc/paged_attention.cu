@@ -389,6 +389,16 @@ __device__ __forceinline__ float pa_lse(float m, float l, float c) {
 }
 
 // ------------------------------------------------------------------ kernel
+//
+// Bounds.  Single tokens and draft chunks read each key and value once: 64 rows
+// of 2000 to 16000 keys (64 / 8 heads of 128) take 260 us for 1.66 GB, 94% of
+// the copy rate.  Short calls are bound by their start and end: 8 rows of 9
+// tokens over 1000 to 16000 keys (147 MB, 22 us at the copy rate) take 41 us.
+// Long chunks are bound by the chain of a slot, scores - softmax - values, some
+// 3000 cycles for 2 x 128 rows x 128 keys against 2048 of MMAs: 2048 tokens
+// over 8192 keys (32 / 8 heads of 128) take 220 us with the tensor pipe 65%
+// active (of 216 us, 199 were left without the exponentials, 209 without the
+// maxima).
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kPaThreads, 1)
@@ -1065,7 +1075,8 @@ constexpr int kJoinThreads = 256;
 
 // Block (b, g): 32 rows of the item that begins in block b and is cut, g =
 // slot * 4 + their quarter of the tile.  A thread has a row and some vectors of
-// four columns; four parts' loads are in flight together.
+// four columns; four parts' loads are in flight together.  4 to 5 us of a call:
+// latency, of the launch, the parts and their sums (512 threads: no faster).
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ AttnArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
