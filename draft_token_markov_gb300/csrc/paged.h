@@ -18,6 +18,7 @@ struct LayoutArgs {
     int32_t *table;
     int64_t table_s0;
     int num_states, width, page_shift;
+    int64_t room;              // tokens that a row may have: positions are 32 bits
     const int32_t *held;
     int32_t *ring;
     int64_t ring_size;

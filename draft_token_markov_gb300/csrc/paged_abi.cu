@@ -204,6 +204,8 @@ markov_status markov_paged_layout(markov_paged_plan *p, const int32_t *context_l
     a.num_states = num_states;
     a.width = table_width;
     a.page_shift = p->page_shift;
+    a.room = (int64_t)table_width << p->page_shift;
+    if (a.room > INT32_MAX) a.room = INT32_MAX;
     a.held = pages_held;
     a.ring = free_pages;
     a.ring_size = ring_size;

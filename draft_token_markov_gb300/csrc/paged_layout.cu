@@ -85,8 +85,7 @@ __global__ void __launch_bounds__(THREADS) paged_layout_kernel(LayoutArgs a) {
         c = a.context[tid];
         q = a.query[tid];
         const int64_t si = a.idx[tid];
-        if (si >= 0 && si < a.num_states && c >= 0 && q >= 0 &&
-            (int64_t)c + q <= ((int64_t)a.width << a.page_shift)) {
+        if (si >= 0 && si < a.num_states && c >= 0 && q >= 0 && (int64_t)c + q <= a.room) {
             h = a.held[si];
             n = (int)(((int64_t)c + q + (1 << a.page_shift) - 1) >> a.page_shift);
             if (h >= 0 && h <= a.width) {

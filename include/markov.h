@@ -472,9 +472,9 @@ markov_status markov_paged_plan_inject_status(markov_paged_plan *plan, markov_st
  *                 page_size + offset; 0 and -1 for the tokens of padding and
  *                 refused rows and past the last row's.
  * A row is refused, its state left as it is, when its context or query
- * length is negative, its state is not below num_states, the row's pages
- * exceed table_width, or the pages that it and the rows before it need
- * exceed the free count (rows after it that need none are still granted).
+ * length is negative, their sum is above 2^31 - 1, its state is not below
+ * num_states, the row's pages exceed table_width, or the pages that it and the
+ * rows before it need exceed the free count (rows after it that need none are still granted).
  * EINVAL for bad sizes or a missing pointer. */
 markov_status markov_paged_layout(markov_paged_plan *plan, const int32_t *context_lens,
                                   const int32_t *query_lens, const int64_t *row_state_idx,
