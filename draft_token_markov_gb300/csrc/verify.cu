@@ -29,9 +29,12 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// log2(e) / T, finite (a T so small that it overflows is the limit T -> 0).
+// log2(e) / T, finite (a T so small that it overflows is the limit T -> 0) and
+// not 0 (T = inf: any difference of two finite logits times the least subnormal
+// is 0 in 2^x, and -inf, of masked ids and of those past the end, stays -inf
+// where 0 * -inf would be NaN).
 __device__ __forceinline__ float inv_temperature(float T) {
-    return fminf(__fdiv_rn(1.4426950408889634f, T), 3.0e38f);
+    return fmaxf(fminf(__fdiv_rn(1.4426950408889634f, T), 3.0e38f), 1.401298464e-45f);
 }
 
 // 8 consecutive logits as fp32.

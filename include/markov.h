@@ -549,8 +549,8 @@ markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int
  * and every draft before it was.  At the first refusal j the row's own token
  * is the argmax over v of ln max(p_j(v) - q_j(v), 0) + noise[b, v] (of ln
  * p_j(v) + noise where no v has p_j > q_j); with all accepted it is the
- * argmax of ln p_N(v) + noise[b, v]; the lowest id among equals.  T <= 0 or
- * NaN, and a position whose largest logit is NaN or infinite: the
+ * argmax of ln p_N(v) + noise[b, v]; the lowest id among equals.  T = +inf:
+ * uniform over the ids whose logit is not -inf.  T <= 0 or NaN, and a position whose largest logit is NaN or infinite: the
  * distribution is one-hot at that logit's id (the lowest NaN id, else the
  * lowest id of the maximum, as the draft was drawn), and noise is not read
  * where p is one-hot.
