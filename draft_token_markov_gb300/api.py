@@ -463,9 +463,14 @@ def markov_paged_plan_inject_status(plan: PagedPlan, code: int, where: int = 0):
 
 
 def _new(stream, shape, dtype, device):
-    """An output allocated here; the allocator learns of a call's other stream."""
+    """An output allocated here; the allocator learns of a call's other stream,
+    a torch stream or a raw handle."""
     t = torch.empty(shape, dtype=dtype, device=device)
-    if isinstance(stream, torch.cuda.Stream):
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = _stream(stream)
+            stream = (torch.cuda.ExternalStream(handle, device=device) if handle
+                      else torch.cuda.default_stream(device))
         # its memory may still be in use by earlier work of the current stream
         stream.wait_stream(torch.cuda.current_stream(device))
         t.record_stream(stream)
