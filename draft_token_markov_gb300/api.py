@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import threading
 
 import torch
 
@@ -410,6 +411,18 @@ def markov_selftest_wait(which: int, timeout_us: int, stream=None) -> int:
 
 # ---------------------------------------------------------------- verify step
 
+class _Views(threading.local):
+    """The two caches of a call, described in place: the library reads them
+    without the interpreter's lock, so each host thread has its own."""
+
+    def __init__(self):
+        self.k, self.v = _CacheView(), _CacheView()
+        self.refs = ctypes.byref(self.k), ctypes.byref(self.v)
+
+
+_views = _Views()
+
+
 class PagedPlan:
     """What the paged calls need besides their arguments, allocated once.
     dtype (bfloat16 or float16) is that of queries, keys, values and outputs."""
@@ -431,9 +444,6 @@ class PagedPlan:
         self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, head_dim
         self.page_size, self.dtype, self.max_rows, self.device = page_size, dtype, max_rows, device
         self._cache_shape = torch.Size((page_size, kv_heads, head_dim))
-        # the two caches of a call, described in place
-        self._k_view, self._v_view = _CacheView(), _CacheView()
-        self._views = ctypes.byref(self._k_view), ctypes.byref(self._v_view)
 
     @property
     def handle(self):
@@ -501,7 +511,7 @@ def _page_table(t):
 
 
 def _cache_view(plan: PagedPlan, view: _CacheView, t, name: str):
-    """Describe a paged cache tensor in `view`, one of the plan's."""
+    """Describe a paged cache tensor in `view`, one of the thread's."""
     p = _dev(t, plan.dtype, name)
     if t.dim() != 4 or t.shape[1:] != plan._cache_shape:
         raise ValueError(f"{name} must be [pages, {plan.page_size}, {plan.kv_heads}, "
@@ -580,9 +590,9 @@ def markov_paged_write(plan: PagedPlan, key, value, k_cache, v_cache, slots, str
     vp, v0, v1, n = _token_rows(plan, value, plan.kv_heads, "value")
     if n != T:
         raise ValueError("key and value must have the same tokens")
-    _cache_view(plan, plan._k_view, k_cache, "k_cache")
-    _cache_view(plan, plan._v_view, v_cache, "v_cache")
-    code = lib().markov_paged_write(plan.handle, kp, k0, k1, vp, v0, v1, *plan._views,
+    _cache_view(plan, _views.k, k_cache, "k_cache")
+    _cache_view(plan, _views.v, v_cache, "v_cache")
+    code = lib().markov_paged_write(plan.handle, kp, k0, k1, vp, v0, v1, *_views.refs,
                                     _flat(slots, torch.int64, T, "slots"), T, _stream(stream))
     _check(code, "markov_paged_write")
 
@@ -604,10 +614,10 @@ def markov_paged_attention(plan: PagedPlan, q, k_cache, v_cache, page_table, row
         raise ValueError("out must have q's tokens")
     if lse is True:
         lse = _new(stream, (T, plan.q_heads), torch.float32, q.device)
-    _cache_view(plan, plan._k_view, k_cache, "k_cache")
-    _cache_view(plan, plan._v_view, v_cache, "v_cache")
+    _cache_view(plan, _views.k, k_cache, "k_cache")
+    _cache_view(plan, _views.v, v_cache, "v_cache")
     code = lib().markov_paged_attention(
-        plan.handle, qp, q0, q1, *plan._views, *_page_table(page_table),
+        plan.handle, qp, q0, q1, *_views.refs, *_page_table(page_table),
         _flat(row_state_idx, torch.int64, rows, "row_state_idx"),
         _flat(query_start, torch.int32, rows + 1, "query_start"),
         _flat(seq_lens, torch.int32, rows, "seq_lens"), rows, T,
