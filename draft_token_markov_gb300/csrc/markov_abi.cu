@@ -526,6 +526,15 @@ markov_status markov_verify(markov_plan *p, const void *target_logits, markov_dt
         !row_state_idx || !tokens || !num_accepted || !target_probs != !draft_probs)
         return MARKOV_EINVAL;
     if (rows < 1 || rows > p->d.max_rows) return MARKOV_EINVAL;
+    // the stride of a dimension of one element says nothing
+    if (N == 1) cache_s1 = V;
+    if (rows == 1) {
+        target_s0 = (N + 1) * target_s1;
+        cache_s0 = N * cache_s1;
+        draft_s0 = uni_s0 = N;
+        tok_s0 = N + 1;
+        noise_s0 = V;
+    }
     if (target_s1 < V || target_s0 < N * target_s1 + V) return MARKOV_EINVAL;
     if (cache_s1 < V || cache_s0 < (N - 1) * cache_s1 + V) return MARKOV_EINVAL;
     if (draft_s0 < N || uni_s0 < N || tok_s0 < N + 1 || noise_s0 < V) return MARKOV_EINVAL;

@@ -568,6 +568,7 @@ markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int
  *   num_accepted  int32 [rows]: accepted drafts, 0 .. N;
  *   target_probs, draft_probs: fp32 [rows, N] p_i(x_i) and q_i(x_i), row
  *                 stride N, or both NULL.
+ * The stride of a dimension of one element (rows or N of 1) is not looked at.
  * Padding rows (row_state_idx[b] < 0) are not written.  Two launches.  EINVAL
  * for a bad shape, stride, alignment or dtype. */
 markov_status markov_verify(markov_plan *plan, const void *target_logits,
