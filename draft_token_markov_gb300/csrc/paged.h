@@ -67,6 +67,7 @@ struct AttnArgs {
     void *joins;               // [blocks]: the item that begins in a block and goes on
     uint32_t *status;
     uint64_t timeout_ns;
+    uint64_t walk_ns;          // the same with the time that the walk to the first item may take
 };
 
 struct VerifyArgs {

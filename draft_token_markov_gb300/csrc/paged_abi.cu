@@ -317,6 +317,8 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     a.joins = p->joins;
     a.status = p->ctrl;
     a.timeout_ns = (uint64_t)p->d.timeout_ms * 1000000ull;
+    // a pair of row tiles takes the walk a fraction of a microsecond, twice
+    a.walk_ns = a.timeout_ns + (uint64_t)((int64_t)num_tokens * a.group / 256 + rows + 1) * 1000ull;
     if (launch_paged_attention(a, qmap, kmap, vmap, p->d.head_dim, p->d.dtype == MARKOV_F16, p->blocks,
                                (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();

@@ -66,6 +66,9 @@ constexpr float kLazy = 8.0f;
 // kinds; batches of single row tiles, which stream keys meanwhile, lose 1% for
 // each)
 constexpr int kWeightOne = 3, kWeightTwo = 7;
+// What a unit of work may take at most (it takes 0.3 to 2 us), where a wait is
+// for whole items and not for a step of one.
+constexpr uint64_t kUnitNs = 20000;
 
 template <int D>
 struct PaShape {
@@ -457,9 +460,12 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
     // a wait that some lane gives up is given up by the warp
-    auto all_wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
+    auto all_wait = [&](uint32_t bar, uint32_t parity, uint32_t where, uint64_t limit_ns) {
         if (__all_sync(0xffffffffu, tc::mbar_test(bar, parity))) return true;
-        return (bool)__all_sync(0xffffffffu, pa_wait_on(bar, parity, where, a.timeout_ns, &sh.abort));
+        return (bool)__all_sync(0xffffffffu, pa_wait_on(bar, parity, where, limit_ns, &sh.abort));
+    };
+    auto step_wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
+        return all_wait(bar, parity, where, a.timeout_ns);
     };
     auto arrive = [&](uint32_t bar) {
         __syncwarp();
@@ -470,7 +476,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     auto phase_of = [](uint32_t at) { return (at / S::kStages) & 1; };
     // the n-th item; its fields are read from shared memory where they are used
     auto item = [&](uint32_t n) -> const volatile PaItem & { return sh.ring[n % kRing]; };
-    auto item_wait = [&](uint32_t n) { return all_wait(item_full + 8 * (n % kRing), (n / kRing) & 1, 0x500); };
+    auto item_wait = [&](uint32_t n) { return all_wait(item_full + 8 * (n % kRing), (n / kRing) & 1, 0x500, a.walk_ns); };
     auto item_done = [&](uint32_t n) { arrive(item_empty + 8 * (n % kRing)); };
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -556,9 +562,10 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         PaJoin join{0, 0, 0, 0, 0};
         int q_token = 0, q_head = 0, q_tiles = 0;    // the queries of the item published last
         bool ok = true;
+        uint64_t limit_ns = a.timeout_ns;            // with the time that the items published so far may take
         for (uint32_t n = 0; ok; ++n) {
             int token = q_token, head = q_head, tiles = q_tiles;
-            ok = all_wait(item_empty + 8 * (n % kRing), (n / kRing & 1) ^ 1, 0x510);
+            ok = all_wait(item_empty + 8 * (n % kRing), (n / kRing & 1) ^ 1, 0x510, limit_ns);
             if (!ok) break;
             q_tiles = 0;
             bool more = false;
@@ -570,6 +577,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 const int j1 = u_end - u < units ? pa_tile_at(a, it, u_end - u) : all;
                 more = it.j0 < j1;                   // not a tile of it: another block's
                 if (more) {
+                    limit_ns += (uint64_t)(j1 - it.j0) * weight * kUnitNs;
                     it.qs = q.qs;
                     it.pos0 = q.pos0;
                     it.state = q.state;
@@ -615,7 +623,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             }
 #pragma unroll 1
             for (int s = 0; s < tiles; ++s, token += a.tile_tokens) {
-                ok = all_wait(q_empty + 8 * s, (q_phase >> s & 1) ^ 1, 0x300 + s);
+                ok = all_wait(q_empty + 8 * s, (q_phase >> s & 1) ^ 1, 0x300 + s, limit_ns);
                 if (!ok) break;
                 q_phase ^= 1u << s;
                 if (lane == 0) {
@@ -664,7 +672,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 if (j + 1 < j1) next = page_of(j + 1);
                 const int slot0 = (j < sinks ? j : w0 + j - sinks) * kPaTile & (page - 1);
                 const uint32_t stage = stage_of(at), phase = phase_of(at), full = kv_full + 8 * stage;
-                ok = all_wait(kv_empty + 8 * stage, phase ^ 1, 0x100 + stage);
+                ok = step_wait(kv_empty + 8 * stage, phase ^ 1, 0x100 + stage);
                 if (!ok) break;
                 if (lane == 0) tc::mbar_expect_tx(full, S::kKvBytes);
                 __syncwarp();
@@ -708,14 +716,14 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 return p;
             }
         };
-        auto loaded = [&](Place k) { return all_wait(kv_full + 8 * k.stage, k.phase, 0x200); };
+        auto loaded = [&](Place k) { return step_wait(kv_full + 8 * k.stage, k.phase, 0x200); };
         auto scores = [&](int slot, int q_tile, Place k) {
             mma_scores<D>(tmem + slot * kPaTile, q_desc + q_tile * (S::kQBytes / 16), k_desc + k.stage * kStep, kIdescS);
             tc::commit_elect(s_full + 8 * slot);
         };
         // O += P V, once the slot's P is there
         auto values = [&](int slot, Place v, bool accumulate) {
-            if (!all_wait(p_full + 8 * slot, p_phase >> slot & 1, 0x220 + slot)) return false;
+            if (!step_wait(p_full + 8 * slot, p_phase >> slot & 1, 0x220 + slot)) return false;
             p_phase ^= 1u << slot;
             tc::fence_after_sync();
             mma_values(t_o + slot * D, tmem + slot * kPaTile, v_desc + v.stage * kStep, kIdescO, accumulate);
@@ -723,7 +731,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
         };
         auto release = [&](Place k) { tc::commit_elect(kv_empty + 8 * k.stage); };
         auto queries = [&](int tile) {
-            const bool r = all_wait(q_full + 8 * tile, q_phase >> tile & 1, 0x210 + tile);
+            const bool r = step_wait(q_full + 8 * tile, q_phase >> tile & 1, 0x210 + tile);
             q_phase ^= 1u << tile;
             return r;
         };
@@ -843,14 +851,14 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     const int sink_tiles = it.sink_tiles;
                     key0 = (key0 < sink_tiles ? key0 : it.w0 + key0 - sink_tiles) * kPaTile;
                 }
-                ok = all_wait(s_full + 8 * slot, s_phase, 0x400 + slot);
+                ok = step_wait(s_full + 8 * slot, s_phase, 0x400 + slot);
                 if (!ok) break;
                 s_phase ^= 1;
                 tc::fence_after_sync();
                 // value rows that nobody sees: zeros
                 if (key0 + kPaTile > end || (key0 < first && key0 + kPaTile > kept)) {
                     const uint32_t v = at + 2 * i + 1;
-                    ok = all_wait(kv_full + 8 * stage_of(v), phase_of(v), 0x420 + slot);
+                    ok = step_wait(kv_full + 8 * stage_of(v), phase_of(v), 0x420 + slot);
                     if (!ok) break;
                     const int key = key0 + row;
                     if (key >= end || (key < first && key >= kept)) {
@@ -865,7 +873,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     tc::fence_proxy_async_smem();
                 }
                 if (owed) {                           // before this slot's O is written again
-                    ok = all_wait(merge_free, merge_phase, 0x460);
+                    ok = step_wait(merge_free, merge_phase, 0x460);
                     if (!ok) break;
                     merge_phase ^= 1;
                     owed = false;
@@ -944,7 +952,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             if (!ok) break;
             at += 2 * steps;
             if (any) {
-                ok = all_wait(pv_done + 8 * slot, pv_phase, 0x430 + slot);
+                ok = step_wait(pv_done + 8 * slot, pv_phase, 0x430 + slot);
                 pv_phase ^= 1;
                 if (!ok) break;
                 tc::fence_after_sync();
@@ -965,7 +973,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             float f0 = any ? 1.0f : 0.0f, f1 = 0.0f;
             const bool merge = !two && steps > 1;
             if (merge) {
-                ok = all_wait(merge_full, merge_phase, 0x470);
+                ok = step_wait(merge_full, merge_phase, 0x470);
                 if (!ok) break;
                 merge_phase ^= 1;
                 tc::fence_after_sync();

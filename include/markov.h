@@ -422,7 +422,8 @@ typedef struct markov_paged_desc {
     int32_t max_rows;     /* request rows of a call, 1 .. 1024 */
     int32_t dtype;        /* of queries, keys, values and outputs: MARKOV_BF16 or MARKOV_F16 */
     int32_t device;
-    int32_t timeout_ms;   /* bounds every in-kernel wait (0 selects 1000 ms) */
+    int32_t timeout_ms;   /* bounds every in-kernel wait for a step (0 selects 1000 ms);
+                             waits for larger pieces of work have that much more */
 } markov_paged_desc;
 
 typedef struct markov_paged_plan markov_paged_plan;

@@ -1,8 +1,11 @@
 """The paged calls at the ends of their documented ranges."""
+import math
+
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
+SENT = 123.0
 
 
 def test_layout_of_lengths_past_31_bits(gpu_lib):
@@ -26,4 +29,48 @@ def test_layout_of_lengths_past_31_bits(gpu_lib):
     assert pos.tolist() == [0, 0, last - 2, last - 1]
     assert slots.tolist() == [-1, -1, 5 * page + 253, 5 * page + 254]
     assert held.tolist() == [width - 1] * 2 and free.tolist() == [0, 4] and ring.tolist() == [0, 1, 2, 3]
+    plan.close()
+
+
+def attend_absent_pages(api, keys, timeout_ms=0):
+    """One token, 256 key heads of 64, over `keys` keys in pages that are not
+    there: they read as zeros, so the outputs are zeros and lse is ln(keys)."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = api.PagedPlan(256, 256, 64, 256, torch.bfloat16, max_rows=1, timeout_ms=timeout_ms)
+    cache = torch.ones((1, 256, 256, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((1, 256, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, SENT), torch.full((1, 256), SENT, device="cuda")
+    api.markov_paged_attention(plan, q, cache, cache, torch.full((1, keys // 256), -1, **i32),
+                               torch.zeros(1, dtype=torch.int64, device="cuda"), torch.tensor([0, 1], **i32),
+                               torch.tensor([keys], **i32), out=out, lse=lse)
+    status = api.markov_paged_plan_status(plan)
+    plan.close()
+    return status, out, lse
+
+
+def test_items_that_take_longer_than_the_wait_limit(gpu_lib):
+    """A block's next item waits for the one before it: several milliseconds
+    of work, which is not a wait that went wrong."""
+    keys = 1 << 20
+    status, out, lse = attend_absent_pages(gpu_lib, keys, timeout_ms=1)
+    assert status == 0
+    assert bool((out == 0).all())
+    assert float((lse.double() - math.log(keys)).abs().max()) <= 1e-5 * math.log(keys)
+
+
+def test_a_walk_that_takes_longer_than_the_wait_limit(gpu_lib):
+    """32768 pairs of row tiles in one request are counted before the first
+    item is known; its tokens see nothing."""
+    api = gpu_lib
+    T = 65536
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = api.PagedPlan(128, 1, 64, 16, torch.bfloat16, max_rows=1, timeout_ms=1)
+    cache = torch.zeros((1, 16, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.ones((T, 128, 64), dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, SENT), torch.full((T, 128), SENT, device="cuda")
+    api.markov_paged_attention(plan, q, cache, cache, torch.zeros((1, 1), **i32),
+                               torch.zeros(1, dtype=torch.int64, device="cuda"), torch.tensor([0, T], **i32),
+                               torch.tensor([0], **i32), out=out, lse=lse)
+    assert api.markov_paged_plan_status(plan) == 0
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
     plan.close()
