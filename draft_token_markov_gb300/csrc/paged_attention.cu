@@ -154,10 +154,11 @@ __device__ __forceinline__ int pa_tile_at(const AttnArgs &a, const PaItem &it, u
     const int past = (int)off - pa_ends_weight(a, it);
     return past <= 0 ? 0 : min(past / pa_tile_weight(a, it), max(it.steps, 1));
 }
-__device__ __noinline__ uint32_t pa_units(const AttnArgs &a, PaReq q, int m) {
+// The weight of an item and its key tiles.
+__device__ __noinline__ uint2 pa_units(const AttnArgs &a, PaReq q, int m) {
     PaItem it;
     pa_span(a, q, m, it);
-    return pa_weight(a, it);
+    return make_uint2(pa_weight(a, it), it.steps);
 }
 
 __device__ __forceinline__ int pa_pairs(const AttnArgs &a, const PaReq &q) {
@@ -171,18 +172,21 @@ struct PaShared {
 };
 
 // The call's units cut into ranges of equal length, the first `rem` one longer.
+// Units are counted in 64 bits (an item's fit 32): 2^31 key tiles, which is what
+// a call may have, weigh more than 2^32.
 struct PaSplit {
-    uint32_t blocks, base, rem;
+    uint64_t base;
+    uint32_t blocks, rem;
 
-    __device__ __forceinline__ void cut(uint32_t total, uint32_t grid) {
-        blocks = min(grid, total / 2);               // a range holds a tile of either weight
+    __device__ __forceinline__ void cut(uint64_t total, uint32_t grid) {
+        blocks = (uint32_t)min((uint64_t)grid, total / 2);   // a range holds a tile of either weight
         base = blocks ? total / blocks : 0;
-        rem = total - base * blocks;
+        rem = (uint32_t)(total - base * blocks);
     }
-    __device__ __forceinline__ uint32_t first(uint32_t c) const { return c * base + min(c, rem); }
-    __device__ __forceinline__ uint32_t block_of(uint32_t u) const {
-        const uint32_t longer = rem * (base + 1);
-        return u < longer ? u / (base + 1) : rem + (u - longer) / base;
+    __device__ __forceinline__ uint64_t first(uint32_t c) const { return c * base + min(c, rem); }
+    __device__ __forceinline__ int block_of(uint64_t u) const {
+        const uint64_t longer = rem * (base + 1);
+        return (int)(u < longer ? u / (base + 1) : rem + (u - longer) / base);
     }
 };
 
@@ -483,14 +487,13 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     if (warp == 11) {
         // ------------------------------------------- the walk, query loads
         PaItem it;
-        uint64_t total = 0;
-        bool over = false;
+        uint64_t total = 0, tiles = 0;               // the call's units, this lane's rows' key tiles
         // the rows' units before and with each, where key tiles will be (of
         // 32 rows and less a lane keeps its own)
-        uint32_t *units_to = reinterpret_cast<uint32_t *>(kv_smem);
+        uint64_t *units_to = reinterpret_cast<uint64_t *>(kv_smem);
         const bool few = a.rows <= 32;
         PaReq q{0, 0, 0, 0};
-        uint32_t own = 0, incl = 0;
+        uint64_t own = 0, incl = 0;
 #pragma unroll 1
         for (int r0 = 0; r0 < a.rows; r0 += 32) {
             if (r0 > 0) {
@@ -499,33 +502,41 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             }
             q = pa_request(a, raw);
             const int pairs = pa_pairs(a, q);
-            uint64_t x = 0;
+            uint64_t x = 0, y = 0;
 #pragma unroll 1
-            for (int m = 0; m < pairs; ++m) x += pa_units(a, q, m);
-            x *= a.kv_heads;
-            over |= x >> 27 != 0;                    // 32 rows' sum stays below 2^32
-            own = incl = (uint32_t)x;
+            for (int m = 0; m < pairs; ++m) {
+                const uint2 units = pa_units(a, q, m);
+                x += units.x;
+                y += units.y;
+            }
+            own = incl = x * a.kv_heads;
+            tiles += y * a.kv_heads;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+                const uint64_t y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
-            if (!few) units_to[r0 + lane] = (uint32_t)total + incl;
+            if (!few) units_to[r0 + lane] = total + incl;
             total += __shfl_sync(0xffffffffu, incl, 31);
         }
         __syncwarp();
-        if (__any_sync(0xffffffffu, over) || total > INT32_MAX) {     // units are counted in 32 bits
-            if (lane == 0 && !pending) set_status(a.status, 2u /* MARKOV_EUNSUPPORTED */, 0x600);
-            total = 0;
+        if (total >> 31) {                           // fewer key tiles than units
+#pragma unroll 1
+            for (int o = 16; o > 0; o >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+            if (tiles >> 31) {
+                if (lane == 0 && !pending) set_status(a.status, 2u /* MARKOV_EUNSUPPORTED */, 0x600);
+                total = 0;
+            }
         }
         PaSplit split;
-        split.cut(pending ? 0u : (uint32_t)total, gridDim.x);
-        uint32_t u = 0, u_begin = 0, u_end = 0;      // the current item's first unit, the range
+        split.cut(pending ? 0u : total, gridDim.x);
+        uint64_t u = 0, u_end = 0;                   // the current item's first unit, the range's end
+        uint32_t skip = 0;                           // units of the first item before the range
         int r = 0, h = 0, m = 0, pairs = 0;
         if (blockIdx.x < split.blocks) {
-            const uint32_t u0 = u_begin = split.first(blockIdx.x);
+            const uint64_t u0 = split.first(blockIdx.x);
             u_end = split.first(blockIdx.x + 1);
-            uint32_t before, units;                  // of the row that holds the first unit
+            uint64_t before, units;                  // of the row that holds the first unit
             if (few) {
                 r = __ffs(__ballot_sync(0xffffffffu, u0 < incl && u0 >= incl - own)) - 1;
                 before = __shfl_sync(0xffffffffu, incl - own, r);
@@ -542,20 +553,21 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     const uint32_t found = __ballot_sync(0xffffffffu, here);
                     if (found) { r = r0 + __ffs(found) - 1; break; }
                 }
-                before = r ? units_to[r - 1] : 0u;
+                before = r ? units_to[r - 1] : 0;
                 units = units_to[r] - before;
                 q = pa_request(a, r);
             }
             pairs = pa_pairs(a, q);
-            const uint32_t head = units / a.kv_heads;
-            h = (u0 - before) / head;
+            const uint64_t head = units / a.kv_heads;
+            h = (int)((u0 - before) / head);
             u = before + h * head;
 #pragma unroll 1
             for (;; ++m) {
-                const uint32_t units = pa_units(a, q, m);
+                const uint32_t units = pa_units(a, q, m).x;
                 if (u0 - u < units) break;
                 u += units;
             }
+            skip = (uint32_t)(u0 - u);
         }
         tc::fence_proxy_async_smem();                // units_to is read; TMA writes come
         uint32_t q_phase = 0;                        // a bit a slot
@@ -573,8 +585,8 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 pa_span(a, q, m, it);
                 const uint32_t units = pa_weight(a, it), weight = pa_tile_weight(a, it);
                 const int all = max(it.steps, 1);
-                it.j0 = u_begin > u ? pa_tile_at(a, it, u_begin - u) : 0;
-                const int j1 = u_end - u < units ? pa_tile_at(a, it, u_end - u) : all;
+                it.j0 = pa_tile_at(a, it, skip);
+                const int j1 = u_end - u < units ? pa_tile_at(a, it, (uint32_t)(u_end - u)) : all;
                 more = it.j0 < j1;                   // not a tile of it: another block's
                 if (more) {
                     limit_ns += (uint64_t)(j1 - it.j0) * weight * kUnitNs;
@@ -595,6 +607,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     }
                 }
                 u += units;
+                skip = 0;
                 if (++m == pairs) {
                     m = 0;
                     if (++h == a.kv_heads) {

@@ -48,6 +48,16 @@ def attend_absent_pages(api, keys, timeout_ms=0):
     return status, out, lse
 
 
+def test_a_request_of_2_to_the_27_key_tiles(gpu_lib):
+    """A sixteenth of the documented bound, in one request."""
+    keys = 1 << 26
+    status, out, lse = attend_absent_pages(gpu_lib, keys)
+    assert status == 0
+    assert bool((out == 0).all())
+    # sums of ones are exact here; the logarithm is within a few units of fp32
+    assert float((lse.double() - math.log(keys)).abs().max()) <= 1e-5 * math.log(keys)
+
+
 def test_items_that_take_longer_than_the_wait_limit(gpu_lib):
     """A block's next item waits for the one before it: several milliseconds
     of work, which is not a wait that went wrong."""
