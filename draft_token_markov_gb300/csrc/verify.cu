@@ -315,6 +315,12 @@ struct Verdict {
     int n;
 };
 
+// The drafts and their probabilities, kept for the outputs.
+struct Drafts {
+    int64_t x[kMaxSteps];
+    float p[kMaxSteps], q[kMaxSteps];
+};
+
 // A thread's draft, and its logits; what does not wait for the first launch.
 struct Draft {
     int64_t x;
@@ -337,8 +343,8 @@ __device__ __forceinline__ Draft load_draft(const VerifyArgs &a, int b) {
 }
 
 // By a whole block: the request's distributions from their partials, the walk
-// over its drafts; with `write`, what is known by now of the outputs.
-__device__ __forceinline__ Verdict walk(const VerifyArgs &a, int b, float T, const Draft &d, bool write) {
+// over its drafts.
+__device__ __forceinline__ Verdict walk(const VerifyArgs &a, int b, float T, const Draft &d, Drafts &drafts) {
     constexpr int kWarps = kVerifyThreads / 32, kTurns = (2 * kMaxSteps + 1 + kWarps - 1) / kWarps;
     __shared__ Dist dist[2 * kMaxSteps + 1];
     __shared__ uint32_t accepted_s;
@@ -370,8 +376,8 @@ __device__ __forceinline__ Verdict walk(const VerifyArgs &a, int b, float T, con
         }
     }
     __syncthreads();
-    float p = 0.0f, q = 0.0f;
     if (warp == 0) {
+        float p = 0.0f, q = 0.0f;
         if (d.x >= 0 && d.x < a.V) {
             p = prob(dist[lane], d.lp, (int)d.x, c);
             q = prob(dist[N + 1 + lane], d.lq, (int)d.x, c);
@@ -379,34 +385,27 @@ __device__ __forceinline__ Verdict walk(const VerifyArgs &a, int b, float T, con
         // the drafts before the first refusal
         const uint32_t refused = __ballot_sync(0xffffffffu, !(lane < N && d.u * q < p));
         if (lane == 0) accepted_s = __ffs(refused) - 1;
+        if (lane < N) {
+            drafts.x[lane] = d.x;
+            drafts.p[lane] = p;
+            drafts.q[lane] = q;
+        }
     }
     __syncthreads();
     const int n = (int)accepted_s;
-    const Verdict v{dist[n], dist[n < N ? N + 1 + n : n], n};
-    if (write) {
-        if (tid < N && a.p) {
-            a.p[(int64_t)b * N + tid] = p;
-            a.q[(int64_t)b * N + tid] = q;
-        }
-        if (tid == 0) a.accepted[b] = n;
-        if (tid <= N) {
-            // where p is one-hot there is nothing to draw
-            int64_t *token = a.tokens + b * a.tok_s0 + tid;
-            if (tid < n) *token = d.x;
-            else if (tid > n) *token = -1;
-            else if (v.p.id >= 0) *token = v.p.id;
-        }
-    }
-    return v;
+    return Verdict{dist[n], dist[n < N ? N + 1 + n : n], n};
 }
 
 // Block (g, b): ids [g pick_len, (g + 1) pick_len) of request b.  At the size
 // above: 3 us until it starts, 2.4 us for the joined partials and the walk, 8 us
-// for its ids (43 MB of logits and noise, in part from L2).
+// for its ids (43 MB of logits and noise, in part from L2).  The block that ends
+// last writes all outputs, so that tokens may lie where the drafts do: every
+// block has read those by then.
 template <bool TF32, bool CF32>
 __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(VerifyArgs a) {
     __shared__ uint64_t key_s[kVerifyThreads / 32];
     __shared__ uint32_t last_s;
+    __shared__ Drafts drafts;
     const int b = blockIdx.y, N = a.N, tid = threadIdx.x;
     const bool padding = a.idx[b] < 0;
     const float T = a.temperature[b];
@@ -419,10 +418,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(VerifyArgs 
     if (!padding) d = load_draft<TF32, CF32>(a, b);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (padding || __ldcg(a.status) != 0u) return;
-    const Verdict verdict = walk(a, b, T, d, blockIdx.x == 0);
+    const Verdict verdict = walk(a, b, T, d, drafts);
     const int n = verdict.n;
     const Dist P = verdict.p, Q = verdict.q;
-    if (P.id >= 0) return;                           // its token is out
     const int64_t t_base = b * a.target_s0 + n * a.target_s1, c_base = b * a.cache_s0 + n * a.cache_s1;
 
     // The best key over [lo, hi): of ln(p - q) + g, or of ln p + g with whole.
@@ -479,7 +477,8 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(VerifyArgs 
         }
         return block_max(best, key_s);
     };
-    const uint64_t best = best_of(lo, hi, n == N, false);
+    // where p is one-hot there is nothing to draw
+    const uint64_t best = P.id < 0 ? best_of(lo, hi, n == N, false) : 0;
     __shared__ uint64_t win_s;
     if (tid == 0) {
         if (best) atomicMax(reinterpret_cast<unsigned long long *>(a.win + b), (unsigned long long)best);
@@ -495,9 +494,18 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(VerifyArgs 
     }
     __syncthreads();
     if (!last_s) return;
-    uint64_t win = win_s;
-    if (win == 0) win = best_of(0, a.V, true, true);   // p <= q everywhere
-    if (tid == 0) a.tokens[b * a.tok_s0 + n] = win ? packed_id(win) : 0;
+    int token = P.id;
+    if (token < 0) {
+        uint64_t win = win_s;
+        if (win == 0) win = best_of(0, a.V, true, true);   // p <= q everywhere
+        token = win ? packed_id(win) : 0;
+    }
+    if (tid < N && a.p) {
+        a.p[(int64_t)b * N + tid] = drafts.p[tid];
+        a.q[(int64_t)b * N + tid] = drafts.q[tid];
+    }
+    if (tid == 0) a.accepted[b] = n;
+    if (tid <= N) a.tokens[b * a.tok_s0 + tid] = tid < n ? drafts.x[tid] : tid == n ? token : -1;
 }
 
 template <bool TF32, bool CF32>

@@ -565,7 +565,8 @@ markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int
  *                 position), row stride noise_s0 a multiple of 4, 16-byte
  *                 aligned;
  *   tokens        int64 [rows, N + 1], row stride tok_s0: the accepted
- *                 drafts, the row's own token, then -1;
+ *                 drafts, the row's own token, then -1; may begin each row
+ *                 where draft_tokens' does (with the same stride);
  *   num_accepted  int32 [rows]: accepted drafts, 0 .. N;
  *   target_probs, draft_probs: fp32 [rows, N] p_i(x_i) and q_i(x_i), row
  *                 stride N, or both NULL.

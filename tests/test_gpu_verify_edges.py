@@ -66,3 +66,36 @@ def test_infinite_temperature(gpu_lib, dtype, V):
     for b in (0, 2, 4):
         assert np.allclose(p[b], 2 / V, rtol=5e-5) and np.allclose(q[b], 2 / V, rtol=5e-5)
         assert (got[0][b][:3] % 2 == 1).all() and got[1][b] == 3 and got[0][b][3] % 2 == 1
+
+
+def test_tokens_in_the_drafts_place(gpu_lib):
+    """One buffer [rows, N + 1] that holds the drafts and takes the tokens, while
+    other work keeps a row's blocks from starting together."""
+    api = gpu_lib
+    R, N, V = 64, 8, 129280
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rnd = lambda *shape: torch.randn(shape, generator=g, device="cuda")  # noqa: E731
+    draft = (3 * rnd(R, N, V)).to(torch.bfloat16)
+    target = torch.cat([draft, draft[:, :1]], 1)
+    rows = torch.arange(R, device="cuda")
+    T, noise = torch.ones(R, device="cuda"), -torch.log(-torch.log(
+        torch.rand((R, V), generator=g, device="cuda").clamp(1e-9, 1 - 1e-7)))
+    drafts = torch.randint(1, V, (R, N), generator=g, device="cuda")
+    u = torch.zeros((R, N), device="cuda")
+    # half of the rows are refused by a one-hot target at once, the others take all
+    target[::2, 0, 0] = math.inf
+    plan = api.Plan(V, 64, N, R)
+    want, want_n = api.markov_verify(plan, target, drafts, draft, T, u, noise, rows)
+    assert want_n[::2].eq(0).all() and want_n[1::2].eq(N).all() and want[::2, 0].eq(0).all()
+    other, x = torch.cuda.Stream(), rnd(8192, 8192).to(torch.bfloat16)
+    other.wait_stream(torch.cuda.current_stream())
+    for k in range(30):
+        with torch.cuda.stream(other):
+            x @ x
+        buf = torch.cat([drafts, torch.full((R, 1), -9, device="cuda")], 1)
+        toks, n = api.markov_verify(plan, target, buf[:, :N], draft, T, u, noise, rows, tokens=buf)
+        assert torch.equal(toks, want) and torch.equal(n, want_n), k
+        toks, n = api.markov_verify(plan, target, drafts, draft, T, u, noise, rows)
+        assert torch.equal(toks, want) and torch.equal(n, want_n), k
+    assert api.markov_plan_status(plan) == 0
+    plan.close()
