@@ -553,8 +553,8 @@ markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int
  * argmax of ln p_N(v) + noise[b, v]; the lowest id among equals.  T = +inf:
  * uniform over the ids whose logit is not -inf.  T <= 0 or NaN, and a position whose largest logit is NaN or infinite: the
  * distribution is one-hot at that logit's id (the lowest NaN id, else the
- * lowest id of the maximum, as the draft was drawn), and noise is not read
- * where p is one-hot.
+ * lowest id of the maximum, as the draft was drawn), and the noise has no
+ * influence where p is one-hot.
  *   target_logits [rows, N + 1, V] of target_dtype, strides in elements;
  *   logit_cache   [rows, N, V] of cache_dtype, as markov_chain_sample wrote
  *                 it; both 16-byte aligned with 16-byte multiples as strides;

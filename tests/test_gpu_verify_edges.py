@@ -68,6 +68,23 @@ def test_infinite_temperature(gpu_lib, dtype, V):
         assert (got[0][b][:3] % 2 == 1).all() and got[1][b] == 3 and got[0][b][3] % 2 == 1
 
 
+def test_noise_where_one_id_has_it_all(gpu_lib):
+    """Greedy rows, and rows whose token comes from a one-hot target: whatever
+    the noise is, NaN included."""
+    s = base.make(4, 3, 20000, seed=4, temps=(0.0, 1.0))
+    s["u"][1], s["u"][3] = 0.0, 0.0                           # what p allows is accepted
+    s["target"][1, 1, 777] = math.nan                         # refused there
+    s["target"][3, 3, 5] = math.inf                           # all accepted, then this one
+    s["tokens"][1, 1] = 5
+    want = base.run(gpu_lib, s)
+    base.check(s, want)
+    assert list(want[1][[1, 3]]) == [1, 3] and want[0][1][1] == 777 and want[0][3][3] == 5
+    for bad in (math.nan, math.inf, -math.inf):
+        s["noise"][:] = bad
+        got = base.run(gpu_lib, s)
+        assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
 def test_tokens_in_the_drafts_place(gpu_lib):
     """One buffer [rows, N + 1] that holds the drafts and takes the tokens, while
     other work keeps a row's blocks from starting together."""
