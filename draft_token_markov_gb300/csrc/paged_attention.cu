@@ -192,28 +192,6 @@ struct PaSplit {
 
 // ----------------------------------------------------------------- helpers
 
-// The rest of a bounded wait.  One that gives up raises the block's abort
-// flag, at which every role leaves at its next wait; the block records the
-// status as it ends.
-__device__ __forceinline__ bool pa_wait_on(uint32_t bar, uint32_t parity, uint32_t where, uint64_t timeout_ns,
-                                           volatile uint32_t *abort) {
-    // a test sleeps for some microseconds at most; the timer, whose reading
-    // costs hundreds of cycles, is looked at every 16th time
-    uint64_t deadline = 0;
-    for (uint32_t i = 1; !tc::mbar_test_sleep(bar, parity); ++i) {
-        if (*abort) return false;
-        if (i % 16 == 0) {
-            const uint64_t now = tc::now_ns();
-            if (deadline == 0) deadline = now + timeout_ns;
-            if (now > deadline) {
-                *abort = where;
-                return false;
-            }
-        }
-    }
-    return true;
-}
-
 // B operand, MN-major, 128-byte swizzle: 64 elements of N contiguous, the
 // next 64 `lbo` bytes on; 8 rows of K 128 bytes apart, the next 8 1024 on.
 __device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr, uint32_t lbo) {
@@ -466,7 +444,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
     // a wait that some lane gives up is given up by the warp
     auto all_wait = [&](uint32_t bar, uint32_t parity, uint32_t where, uint64_t limit_ns) {
         if (__all_sync(0xffffffffu, tc::mbar_test(bar, parity))) return true;
-        return (bool)__all_sync(0xffffffffu, pa_wait_on(bar, parity, where, limit_ns, &sh.abort));
+        return (bool)__all_sync(0xffffffffu, tc::mbar_wait_or_abort(bar, parity, where, limit_ns, &sh.abort));
     };
     auto step_wait = [&](uint32_t bar, uint32_t parity, uint32_t where) {
         return all_wait(bar, parity, where, a.timeout_ns);

@@ -85,6 +85,28 @@ __device__ __forceinline__ bool mbar_wait_for(uint32_t bar, uint32_t parity, uin
     return mbar_wait(bar, parity, now_ns() + timeout_ns);
 }
 
+// The rest of a bounded wait.  One that gives up raises the block's abort
+// flag, at which every role leaves at its next wait; the block records the
+// status as it ends.
+__device__ __forceinline__ bool mbar_wait_or_abort(uint32_t bar, uint32_t parity, uint32_t where, uint64_t timeout_ns,
+                                                   volatile uint32_t *abort) {
+    // a test sleeps for some microseconds at most; the timer, whose reading
+    // costs hundreds of cycles, is looked at every 16th time
+    uint64_t deadline = 0;
+    for (uint32_t i = 1; !mbar_test_sleep(bar, parity); ++i) {
+        if (*abort) return false;
+        if (i % 16 == 0) {
+            const uint64_t now = now_ns();
+            if (deadline == 0) deadline = now + timeout_ns;
+            if (now > deadline) {
+                *abort = where;
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
 // Warp maximum of a 64-bit key in two 32-bit reductions (high word, then
 // the low word among the lanes holding the highest high word).
 __device__ __forceinline__ uint64_t warp_max_u64(uint64_t x) {

@@ -316,7 +316,8 @@ int64_t markov_plan_query(const markov_plan *plan, int32_t key);
  * markov_selftest_wait runs one of the kernels' bounded waits on a wait that
  * nothing can complete, in a one-CTA kernel on `stream`, with a limit of
  * timeout_us microseconds (1 .. 1e6): which 0 is the chain's grid barrier,
- * which 1 an mbarrier wait of the tcgen05 chain.  It synchronizes the stream
+ * which 1 an mbarrier wait of the tcgen05 chain, which 2 two waits of the paged
+ * attention, of which the first to give up ends the other.  It synchronizes the stream
  * and returns the status the kernel recorded: MARKOV_ETIMEOUT when the wait
  * gave up as designed, MARKOV_OK if it (wrongly) completed.  The kernel
  * never traps and leaves the context usable.  Its scratch is a static device
