@@ -52,6 +52,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "paged.h"
 #include "tc.cuh"
 
@@ -238,17 +239,6 @@ __device__ __forceinline__ void ld_32x32b_x32(uint32_t taddr, float *r) {
         : "memory");
 }
 
-__device__ __forceinline__ void st_32x32b_x32(uint32_t taddr, const uint32_t *u) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
-        "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15]), "r"(u[16]),
-        "r"(u[17]), "r"(u[18]), "r"(u[19]), "r"(u[20]), "r"(u[21]), "r"(u[22]), "r"(u[23]), "r"(u[24]),
-        "r"(u[25]), "r"(u[26]), "r"(u[27]), "r"(u[28]), "r"(u[29]), "r"(u[30]), "r"(u[31])
-        : "memory");
-}
-
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if (F16) {
@@ -320,32 +310,6 @@ __device__ __forceinline__ void mma_values(uint32_t d, uint32_t a, uint64_t b, u
 // The lowest n bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t ones(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
-// Two fp32 values in one register pair, and the packed arithmetic on them.
-__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void split2(uint64_t x, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ float pa_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 // An item's part from a block, for one slot: [D / 4][128 rows] vectors of
@@ -899,7 +863,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     const bool grow = top > m && (m == -INFINITY || (top - m) * c > lazy);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float mn = fmaxf(m, top);
-                        const float f = m == -INFINITY ? 0.0f : pa_ex2((m - mn) * c);
+                        const float f = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
                         m = mn;
                         if (any) {
                             // the last PV is done: S's commit came after it
@@ -925,7 +889,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                         for (int e = 0; e < 16; ++e) {
                             float x0, x1;
                             split2(fma2(f32x2(s[32 * k + 2 * e], s[32 * k + 2 * e + 1]), c2, mc2), x0, x1);
-                            const float p0 = pa_ex2(x0), p1 = pa_ex2(x1);
+                            const float p0 = ex2(x0), p1 = ex2(x1);
                             sum[e & 1] = add2(sum[e & 1], f32x2(p0, p1));
                             p[e] = pack2<F16>(p0, p1);
                         }
@@ -970,8 +934,8 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                 tc::fence_after_sync();
                 const float m1 = exchange[row], l1 = exchange[kPaTile + row];
                 const float mn = fmaxf(m, m1);
-                f0 = m == -INFINITY ? 0.0f : pa_ex2((m - mn) * c);
-                f1 = m1 == -INFINITY ? 0.0f : pa_ex2((m1 - mn) * c);
+                f0 = m == -INFINITY ? 0.0f : ex2((m - mn) * c);
+                f1 = m1 == -INFINITY ? 0.0f : ex2((m1 - mn) * c);
                 m = mn;
                 l = l * f0 + l1 * f1;
             }
@@ -1106,7 +1070,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) mn = fmaxf(mn, pm[e]);
-        const float f = M == -INFINITY ? 0.0f : pa_ex2((M - mn) * c);
+        const float f = M == -INFINITY ? 0.0f : ex2((M - mn) * c);
         M = mn;
         L *= f;
 #pragma unroll
@@ -1114,7 +1078,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (b0 + e > j.c1) continue;
-            const float g = pm[e] == -INFINITY ? 0.0f : pa_ex2((pm[e] - M) * c);
+            const float g = pm[e] == -INFINITY ? 0.0f : ex2((pm[e] - M) * c);
             L += pl[e] * g;
 #pragma unroll
             for (int k = 0; k < kVec; ++k) {

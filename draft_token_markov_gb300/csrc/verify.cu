@@ -15,19 +15,15 @@
 // or rounded once, and an overflow of l / T cannot make it NaN.
 #include <climits>
 
-#include "paged.h"
 #include "common.cuh"
+#include "f32x2.cuh"
+#include "paged.h"
+#include "tc.cuh"
 
 namespace dtm {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kSegment = 1024;             // ids; a multiple of a warp's turn
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // log2(e) / T, finite (a T so small that it overflows is the limit T -> 0) and
 // not 0 (T = inf: any difference of two finite logits times the least subnormal
@@ -62,21 +58,14 @@ __device__ __forceinline__ float load1(const void *row, int64_t at) {
     return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(row) + at) << 16);
 }
 
-__device__ __forceinline__ uint64_t warp_max(uint64_t x) {
-    const uint32_t hi = (uint32_t)(x >> 32), lo = (uint32_t)x;
-    const uint32_t hm = __reduce_max_sync(0xffffffffu, hi);
-    const uint32_t lm = __reduce_max_sync(0xffffffffu, hi == hm ? lo : 0u);
-    return ((uint64_t)hm << 32) | lm;
-}
-
 // A block's maximum key; every thread gets it.
 __device__ __forceinline__ uint64_t block_max(uint64_t x, uint64_t *shared) {
-    x = warp_max(x);
+    x = tc::warp_max_u64(x);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = x;
     __syncthreads();
     x = shared[threadIdx.x & (kVerifyThreads / 32 - 1)];
-    return warp_max(x);
+    return tc::warp_max_u64(x);
 }
 
 // The segment's best (logit, id) in the argmax order, whatever it holds; by
@@ -93,27 +82,7 @@ __device__ __noinline__ uint64_t segment_key(const void *row, int64_t base, int 
             best = k > best ? k : best;
         }
     }
-    return warp_max(best);
-}
-
-// Two fp32 values in one register pair, and the packed arithmetic on them.
-__device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void split_f2(uint64_t x, float &lo, float &hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
-}
-__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
+    return tc::warp_max_u64(best);
 }
 
 // 8 consecutive logits as they lie, and their maximum (NaN if one is).
@@ -186,7 +155,7 @@ __device__ __forceinline__ void take_turn(const Raw8<F32> (&x)[kTurnVectors<F32>
     }
     if (!sampled) return;
     const float ref = s.m == -INFINITY ? 0.0f : s.m;
-    const uint64_t neg = pack_f2(-ref, -ref), c2 = pack_f2(c, c);
+    const uint64_t neg = f32x2(-ref, -ref), c2 = f32x2(c, c);
     uint64_t sum[2] = {0, 0};
 #pragma unroll
     for (int k = 0; k < kTurnVectors<F32>; ++k)
@@ -194,11 +163,11 @@ __device__ __forceinline__ void take_turn(const Raw8<F32> (&x)[kTurnVectors<F32>
         for (int j = 0; j < 4; ++j) {
             float e0, e1;
             x[k].pair(j, e0, e1);
-            split_f2(mul_f2(add_f2(pack_f2(e0, e1), neg), c2), e0, e1);
-            sum[j & 1] = add_f2(sum[j & 1], pack_f2(ex2(e0), ex2(e1)));
+            split2(mul2(add2(f32x2(e0, e1), neg), c2), e0, e1);
+            sum[j & 1] = add2(sum[j & 1], f32x2(ex2(e0), ex2(e1)));
         }
     float s0, s1;
-    split_f2(add_f2(sum[0], sum[1]), s0, s1);
+    split2(add2(sum[0], sum[1]), s0, s1);
     s.z += s0 + s1;
 }
 
@@ -231,7 +200,7 @@ __device__ void end_segment(const void *row, int64_t base, int lo, int hi, bool 
                 if (e1 == m) id = s.at + k * 256 + 2 * j + 1;
                 if (e0 == m) id = s.at + k * 256 + 2 * j;
             }
-        key = warp_max(s.m == m ? pack_key(m, (uint32_t)id) : 0ull);
+        key = tc::warp_max_u64(s.m == m ? pack_key(m, (uint32_t)id) : 0ull);
     }
     if ((threadIdx.x & 31) == 0)
         __stcg(out, make_uint4(__float_as_uint(m), __float_as_uint(z), (uint32_t)key, (uint32_t)(key >> 32)));
@@ -368,7 +337,7 @@ __device__ __forceinline__ Verdict walk(const VerifyArgs &a, int b, float T, con
         float Z = m == -INFINITY ? 0.0f : __uint_as_float(part[k].y) * ex2((m - M) * c);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) Z += __shfl_xor_sync(0xffffffffu, Z, o);
-        const uint64_t key = warp_max(((uint64_t)part[k].w << 32) | part[k].z);
+        const uint64_t key = tc::warp_max_u64(((uint64_t)part[k].w << 32) | part[k].z);
         if (lane == 0) {
             const uint32_t o = packed_ordered(key);
             const bool finite = o != 0xffffffffu && isfinite(key_from_ordered(o));
