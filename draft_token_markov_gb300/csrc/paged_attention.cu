@@ -13,11 +13,13 @@
 //                       A operand; V as it lies in the cache (MN-major B)
 // with c = scale log2 e.  The maximum that p is taken against moves, and O is
 // rescaled in TMEM, when a row's grows; in items of two row tiles only when it
-// has grown by more than 2^8 (kLazy), the sums being exact all the same: 5% of
-// a long chunk's time.  With few rows p is kept against the true maximum, so
-// that the weight that counts most is 1, without its rounding (1% of a decode
-// step's time; the output's error 1.39 instead of 1.41 times that of its own
-// rounding at worst).
+// has grown by more than 2^8 (kLazy), the sums being exact all the same: 220 us
+// against 258 us with 0 for 2048 tokens over 8192, 85 against 95 us for a mixed
+// batch, for an output error of 1.38 instead of 1.13 times that of its own
+// rounding.  With few rows p is kept against the true maximum, so that the
+// weight that counts most is 1, without its rounding (0.5% of a decode step's
+// time, 2% and 3% of drafts' and short windows'; the output's error 1.39 instead
+// of 1.41 times that of its own rounding at worst).
 //
 // Two slots, each with its S, its O and a warpgroup, take turns on the tensor
 // core: while one is in its MMAs the other is in its softmax.  An item of two
@@ -62,10 +64,11 @@ constexpr int kPaThreads = 384;
 constexpr int kRing = 4;                     // items that are known ahead
 constexpr int kPaTile = 128;                 // keys of a tile, and rows
 constexpr float kLazy = 8.0f;
-// an item's start and end, in key tiles of one row tile (the largest block
-// of a mixed batch measured 110, 94, 85, 87, 92 us at 2, 4, 6, 8, 11 for both
-// kinds; batches of single row tiles, which stream keys meanwhile, lose 1% for
-// each)
+// an item's start and end, in key tiles of one row tile.  In us, for 16 rows of
+// 1-500 tokens (7 query heads a key head), 24 rows of 1-300 (8) and 32 rows of
+// 5 drafts: 3 and 7 take 85.0, 81.3, 42.5; with another weight of one tile, 2:
+// 87.8, 86.5, 42.7, 5: 88.7, 79.8, 44.7; with another of two, 5: 89.2, 82.2,
+// 42.6, 9: 86.6, 84.0, 42.6, 11: 90.6, 81.9, 42.6; 6 for both: 84.4, 83.4, 46.3
 constexpr int kWeightOne = 3, kWeightTwo = 7;
 // What a unit of work may take at most (it takes 0.3 to 2 us), where a wait is
 // for whole items and not for a step of one.
@@ -342,7 +345,9 @@ __device__ __forceinline__ float pa_lse(float m, float l, float c) {
 // Bounds.  Single tokens and draft chunks read each key and value once: 64 rows
 // of 2000 to 16000 keys (64 / 8 heads of 128) take 260 us for 1.66 GB, 94% of
 // the copy rate.  Short calls are bound by their start and end: 8 rows of 9
-// tokens over 1000 to 16000 keys (147 MB, 22 us at the copy rate) take 41 us.
+// tokens over 1000 to 16000 keys (147 MB, 22 us at the copy rate) take 41 us,
+// 32 rows of 9 with 1004 keys in sight (71 MB, fp16, heads of 64) 35 us with the
+// tensor pipe 15% active.
 // Long chunks are bound by the chain of a slot, scores - softmax - values, some
 // 3000 cycles for 2 x 128 rows x 128 keys against 2048 of MMAs: 2048 tokens
 // over 8192 keys (32 / 8 heads of 128) take 220 us with the tensor pipe 65%

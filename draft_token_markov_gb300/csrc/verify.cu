@@ -247,9 +247,12 @@ __device__ __forceinline__ void take_segment(const void *row, int64_t base, int 
 // The segments of the call, row = request * (2 N + 1) + position, are dealt to
 // the warps in turn; a warp's loads pause only between two of them, and the
 // 32 warps of a multiprocessor do so at different times.  Bound by memory: 246
-// MB (64 requests of 8 drafts, V = 129280, an eighth of them padding) in 39 us,
-// 45.7 us with cold caches; the warps end 24 to 40 us after the start, as they
-// have five to eight segments.  (Taken from a counter instead, asked for a segment
+// MB (64 requests of 8 drafts, V = 129280, an eighth of them padding) in 44.6 us
+// (5.5 TB/s); the warps' ends lie 16 us apart, as they have five to eight
+// segments, those of padding rows, which cost nothing, among them.  fp32 logits
+// and caches: 492 MB in 77.6 us (6.3 TB/s).  With one of each type both forms are in
+// the loop and spill some registers: 76.5 us for the 362 MB of a BF16 target and
+// an fp32 cache.  (Taken from a counter instead, asked for a segment
 // ahead, the whole call took 66.7 us against 61.7 us.)
 template <bool TF32, bool CF32>
 __global__ void __launch_bounds__(kVerifyThreads, 4) verify_stats_kernel(VerifyArgs a) {
@@ -366,10 +369,11 @@ __device__ __forceinline__ Verdict walk(const VerifyArgs &a, int b, float T, con
 }
 
 // Block (g, b): ids [g pick_len, (g + 1) pick_len) of request b.  At the size
-// above: 3 us until it starts, 2.4 us for the joined partials and the walk, 8 us
-// for its ids (43 MB of logits and noise, in part from L2).  The block that ends
-// last writes all outputs, so that tokens may lie where the drafts do: every
-// block has read those by then.
+// above, 17 us of the call: some 3 us until it starts, 2.4 us for the joined
+// partials and the walk, 8 us for its ids (43 MB of logits and noise, in part
+// from L2); the rest is not attributed.  The block that ends last writes all
+// outputs, so that tokens may lie where the drafts do: every block has read
+// those by then.
 template <bool TF32, bool CF32>
 __global__ void __launch_bounds__(kVerifyThreads) verify_pick_kernel(VerifyArgs a) {
     __shared__ uint64_t key_s[kVerifyThreads / 32];

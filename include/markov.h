@@ -530,9 +530,9 @@ markov_status markov_paged_write(markov_paged_plan *plan, const void *key, int64
  * Keys that one token of the row sees and another does not may be anything
  * too, values there must be finite.  A call of 2^31 and more key tiles (128
  * keys of a key head, for up to 256 rows of query heads) computes nothing and
- * records MARKOV_EUNSUPPORTED for markov_paged_plan_status.  Two launches.  EINVAL for a bad shape,
- * stride or alignment, a table row of more than 2^30 keys, or 2^30 and more
- * tokens times q_heads / kv_heads. */
+ * records MARKOV_EUNSUPPORTED for markov_paged_plan_status.  Two launches.
+ * EINVAL for a bad shape, stride or alignment, a table row of more than 2^30
+ * keys, or 2^30 and more tokens times q_heads / kv_heads. */
 markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int64_t q_s0,
                                      int64_t q_s1, const markov_cache_view *k_cache,
                                      const markov_cache_view *v_cache, const int32_t *page_table,
@@ -551,11 +551,12 @@ markov_status markov_paged_attention(markov_paged_plan *plan, const void *q, int
  * and every draft before it was.  At the first refusal j the row's own token
  * is the argmax over v of ln max(p_j(v) - q_j(v), 0) + noise[b, v] (of ln
  * p_j(v) + noise where no v has p_j > q_j); with all accepted it is the
- * argmax of ln p_N(v) + noise[b, v]; the lowest id among equals.  T = +inf:
- * uniform over the ids whose logit is not -inf.  T <= 0 or NaN, and a position whose largest logit is NaN or infinite: the
- * distribution is one-hot at that logit's id (the lowest NaN id, else the
- * lowest id of the maximum, as the draft was drawn), and the noise has no
- * influence where p is one-hot.
+ * argmax of ln p_N(v) + noise[b, v]; the lowest id among equals.  Probabilities
+ * are fp32: one below its range counts as 0.  T = +inf: uniform over the ids
+ * whose logit is not -inf.  T <= 0 or NaN, and a position whose largest logit
+ * is NaN or infinite: the distribution is one-hot at that logit's id (the
+ * lowest NaN id, else the lowest id of the maximum, as the draft was drawn),
+ * and the noise has no influence where p is one-hot.
  *   target_logits [rows, N + 1, V] of target_dtype, strides in elements;
  *   logit_cache   [rows, N, V] of cache_dtype, as markov_chain_sample wrote
  *                 it; both 16-byte aligned with 16-byte multiples as strides;
