@@ -306,8 +306,8 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     a.tile_tokens = 128 / a.group;
     a.group_inv = (65536 + a.group - 1) / a.group;
     a.scale2 = std::fmax(std::fabs(scale) * 1.4426950408889634f, 1e-30f);
-    // a row has fewer keys than kMaxRoom
-    a.window = window >= kMaxRoom ? 0 : window;
+    a.window = window;
+    // a row has no more keys than kMaxRoom
     a.sinks = sinks < kMaxRoom ? sinks : (int)kMaxRoom;
     a.out = static_cast<uint16_t *>(out);
     a.out_s0 = out_s0;

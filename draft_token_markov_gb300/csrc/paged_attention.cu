@@ -127,6 +127,11 @@ __device__ __forceinline__ PaReq pa_request(const AttnArgs &a, const PaRaw &w) {
 }
 __device__ __noinline__ PaReq pa_request(const AttnArgs &a, int r) { return pa_request(a, pa_load(a, r)); }
 
+// The first key of the window of a token at `pos`.
+__device__ __forceinline__ int pa_window(const AttnArgs &a, int pos) {
+    return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+
 // The m-th pair of row tiles of a request: its keys and its key tiles (none
 // where nothing is seen; it counts as one unit then).
 __device__ __forceinline__ void pa_span(const AttnArgs &a, const PaReq &q, int m, PaItem &it) {
@@ -134,7 +139,7 @@ __device__ __forceinline__ void pa_span(const AttnArgs &a, const PaReq &q, int m
     it.tokens = min(q.np - it.t0, 2 * a.tile_tokens);
     const int p0 = q.pos0 + it.t0, p1 = p0 + it.tokens - 1;
     it.end = q.state < 0 ? 0 : max(0, min(p1 + 1, a.room));
-    it.first = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+    it.first = pa_window(a, p0);
     it.kept = min(min(a.sinks, it.first), it.end);
     it.w0 = it.first / kPaTile;
     const int nw = it.first < it.end ? (it.end + kPaTile - 1) / kPaTile - it.w0 : 0;
@@ -800,7 +805,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             // a tile is seen whole by the warp's rows when its last key is
             // not past the first one's and its first within the last one's window
             const int whole_end = min(__shfl_sync(0xffffffffu, pos, 0) + 1, a.room);
-            const int whole_first = a.window > 0 ? __shfl_sync(0xffffffffu, pos, 31) - a.window + 1 : 0;
+            const int whole_first = pa_window(a, __shfl_sync(0xffffffffu, pos, 31));
             const int end = it.end, first = it.first, kept = it.kept;
             const float lazy = two ? kLazy : 0.0f;
             float m = -INFINITY, l = 0.0f;
@@ -850,7 +855,7 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
                     }
                     if (key0 + kPaTile > whole_end || (key0 < whole_first && key0 + kPaTile > a.sinks)) {
                         const int hi = min(pos + 1, a.room) - key0, sk = min(a.sinks - key0, hi);
-                        const int lo = a.window > 0 ? pos - a.window + 1 - key0 : 0;
+                        const int lo = pa_window(a, pos) - key0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t seen = (ones(hi - 32 * k) & ~ones(lo - 32 * k)) | ones(sk - 32 * k);

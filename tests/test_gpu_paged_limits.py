@@ -4,6 +4,8 @@ import math
 import pytest
 import torch
 
+from tests import test_gpu_paged as paged
+
 pytestmark = pytest.mark.gpu
 SENT = 123.0
 
@@ -84,3 +86,13 @@ def test_a_walk_that_takes_longer_than_the_wait_limit(gpu_lib):
     assert api.markov_paged_plan_status(plan) == 0
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
     plan.close()
+
+
+@pytest.mark.parametrize("window,sinks", [(1 << 30, 0), ((1 << 30) + 100, 5), ((1 << 31) - 1, 0)])
+def test_windows_past_30_bits(gpu_lib, window, sinks):
+    """A length beyond the table's keys, of which a window of 2^30 keys and more
+    still hides the first ones."""
+    for behind in (40, 130, 300):
+        c = paged.Case([(383, 1), (380, 4)], 4, 2, 64, 16, seed=behind, width_extra=0)
+        c.lens[:] = min(window + behind, (1 << 31) - 1)
+        paged.both(gpu_lib, c, window=window, sinks=sinks)
