@@ -798,9 +798,10 @@ paged_attention_kernel(const __grid_constant__ AttnArgs a, const __grid_constant
             if (!ok || it.tokens == 0) break;
             const bool two = it.tokens > a.tile_tokens;
             const int t0 = it.t0 + (two ? slot * a.tile_tokens : 0);
-            const int rows = min(it.tokens + it.t0 - t0, a.tile_tokens) * a.group;
+            const int tokens = min(it.tokens + it.t0 - t0, a.tile_tokens), rows = tokens * a.group;
             const int steps = it.steps, ahead = two ? 1 : 2;
-            const int tok = row * a.group_inv >> 16, pos = it.pos0 + t0 + tok;
+            // rows past the tokens take the last one's position: theirs may not fit
+            const int tok = row * a.group_inv >> 16, pos = it.pos0 + t0 + min(tok, tokens - 1);
             const bool busy = (warp & 3) * 32 < rows;
             // a tile is seen whole by the warp's rows when its last key is
             // not past the first one's and its first within the last one's window

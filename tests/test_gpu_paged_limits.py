@@ -96,3 +96,13 @@ def test_windows_past_30_bits(gpu_lib, window, sinks):
         c = paged.Case([(383, 1), (380, 4)], 4, 2, 64, 16, seed=behind, width_extra=0)
         c.lens[:] = min(window + behind, (1 << 31) - 1)
         paged.both(gpu_lib, c, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("window,sinks", [(5, 3), (200, 130), (7, 0), (0, 0)])
+def test_the_last_positions_that_there_are(gpu_lib, window, sinks):
+    """Lengths up to 2^31 - 1 over a short table: of a window nothing is left but
+    the first tokens, in whole key tiles too."""
+    for n in (1, 3):
+        c = paged.Case([(512 - n, n), (300, 2)], 4, 4, 64, 16, seed=n, width_extra=0)
+        c.lens[0] = (1 << 31) - 1
+        paged.both(gpu_lib, c, window=window, sinks=sinks)
