@@ -416,8 +416,8 @@ class _Views(threading.local):
     without the interpreter's lock, so each host thread has its own."""
 
     def __init__(self):
-        self.k, self.v = _CacheView(), _CacheView()
-        self.refs = ctypes.byref(self.k), ctypes.byref(self.v)
+        k, v = _CacheView(), _CacheView()
+        self.both = k, v, (ctypes.byref(k), ctypes.byref(v))
 
 
 _views = _Views()
@@ -590,9 +590,10 @@ def markov_paged_write(plan: PagedPlan, key, value, k_cache, v_cache, slots, str
     vp, v0, v1, n = _token_rows(plan, value, plan.kv_heads, "value")
     if n != T:
         raise ValueError("key and value must have the same tokens")
-    _cache_view(plan, _views.k, k_cache, "k_cache")
-    _cache_view(plan, _views.v, v_cache, "v_cache")
-    code = lib().markov_paged_write(plan.handle, kp, k0, k1, vp, v0, v1, *_views.refs,
+    k_view, v_view, views = _views.both
+    _cache_view(plan, k_view, k_cache, "k_cache")
+    _cache_view(plan, v_view, v_cache, "v_cache")
+    code = lib().markov_paged_write(plan.handle, kp, k0, k1, vp, v0, v1, *views,
                                     _flat(slots, torch.int64, T, "slots"), T, _stream(stream))
     _check(code, "markov_paged_write")
 
@@ -614,10 +615,11 @@ def markov_paged_attention(plan: PagedPlan, q, k_cache, v_cache, page_table, row
         raise ValueError("out must have q's tokens")
     if lse is True:
         lse = _new(stream, (T, plan.q_heads), torch.float32, q.device)
-    _cache_view(plan, _views.k, k_cache, "k_cache")
-    _cache_view(plan, _views.v, v_cache, "v_cache")
+    k_view, v_view, views = _views.both
+    _cache_view(plan, k_view, k_cache, "k_cache")
+    _cache_view(plan, v_view, v_cache, "v_cache")
     code = lib().markov_paged_attention(
-        plan.handle, qp, q0, q1, *_views.refs, *_page_table(page_table),
+        plan.handle, qp, q0, q1, *views, *_page_table(page_table),
         _flat(row_state_idx, torch.int64, rows, "row_state_idx"),
         _flat(query_start, torch.int32, rows + 1, "query_start"),
         _flat(seq_lens, torch.int32, rows, "seq_lens"), rows, T,
