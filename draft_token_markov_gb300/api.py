@@ -12,6 +12,7 @@ import ctypes
 import os
 import re
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -52,6 +53,18 @@ class _CacheView(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
                 ("s_page", ctypes.c_int64), ("s_slot", ctypes.c_int64),
                 ("s_head", ctypes.c_int64)]
+
+
+class _E4m3View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("num_pages", "s_page", "s_slot", "s_head")] + [
+        ("scales", ctypes.c_void_p)] + [(n, ctypes.c_int64) for n in ("ss_page", "ss_block", "ss_head")] + [
+        ("block", ctypes.c_int32)]
+
+
+class _RotaryDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("head_dim", "rot_dim", "interleaved", "scaling", "device")] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "original_len", "low", "high", "amplitude")] + [
+        ("frequencies", ctypes.POINTER(ctypes.c_double))]
 
 
 def header_symbols() -> list[str]:
@@ -114,6 +127,18 @@ def _declare(L):
         "markov_verify": (i32, [P, P, i32, i64, i64, P, i64, P, i32, i64, i64, P, P, i64, P, i64,
                                 P, i32, P, i64, P, P, P, P]),
         "markov_selftest_wait": (i32, [i32, i32, P]),
+        "markov_rotary_plan_create": (i32, [c.POINTER(_RotaryDesc), c.POINTER(P)]),
+        "markov_rotary_plan_destroy": (None, [P]),
+        "markov_rotary": (i32, [P, P, i64, i64, i32, P, i64, i64, i32, i32, P, i32, P, i64, i64, P, i64, i64,
+                                P]),
+        "markov_paged_write_e4m3": (i32, [P, P, i64, i64, P, i64, i64, c.POINTER(_E4m3View),
+                                          c.POINTER(_E4m3View), P, i32, i32, P]),
+        "markov_paged_read_e4m3": (i32, [P, c.POINTER(_E4m3View), c.POINTER(_E4m3View), P, i64, i32, i32, P,
+                                         P, P, i32, i32, P, i64, i64, P, i64, i64, P]),
+        "markov_paged_attention_e4m3": (i32, [P, P, i64, i64, c.POINTER(_E4m3View), c.POINTER(_E4m3View), P,
+                                              i64, i32, i32, P, P, P, i32, i32, f32, i32, i32, P, i64, i64,
+                                              P, P]),
+        "markov_logprobs": (i32, [P, i32, i64, i32, i32, P, P, i32, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -418,6 +443,8 @@ class _Views(threading.local):
     def __init__(self):
         k, v = _CacheView(), _CacheView()
         self.both = k, v, (ctypes.byref(k), ctypes.byref(v))
+        k, v = _E4m3View(), _E4m3View()
+        self.e4m3 = k, v, (ctypes.byref(k), ctypes.byref(v))
 
 
 _views = _Views()
@@ -683,3 +710,267 @@ def markov_verify(plan: Plan, target_logits, draft_tokens, logit_cache, temperat
         _stream(stream))
     _check(code, "markov_verify")
     return tokens, num_accepted
+
+
+# ------------------------------------- rotary positions, e4m3 caches, log probabilities
+
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3, "wavelength": 4, "given": 5}
+
+
+class RotaryPlan:
+    """The frequencies of rotary positions, computed once.  scaling is one of
+    "none", "linear", "base", "parts", "wavelength" (include/markov.h has their
+    formulas) or "given", with frequencies [rot_dim / 2] in radians a position.
+    amplitude None: 0.1 ln(factor) + 1 with "parts", else 1."""
+
+    def __init__(self, head_dim: int, rot_dim: int | None = None, theta: float = 10000.0,
+                 interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
+                 original_len: float = 0.0, low: float = 1.0, high: float = 32.0,
+                 amplitude: float | None = None, frequencies=None, device: int | None = None):
+        if scaling not in ROTARY_SCALINGS:
+            raise ValueError(f"scaling must be one of {', '.join(ROTARY_SCALINGS)}")
+        rot_dim = head_dim if rot_dim is None else rot_dim
+        if (scaling == "given") != (frequencies is not None):
+            raise ValueError("frequencies belong to scaling 'given'")
+        given = None
+        if frequencies is not None:
+            f = [float(x) for x in frequencies]
+            if len(f) != rot_dim // 2:
+                raise ValueError(f"frequencies must have {rot_dim // 2} elements, got {len(f)}")
+            given = (ctypes.c_double * len(f))(*f)
+        if amplitude is not None and not amplitude > 0:
+            raise ValueError("amplitude must be positive")
+        if device is None:
+            device = torch.cuda.current_device()
+        d = _RotaryDesc(head_dim, rot_dim, int(interleaved), ROTARY_SCALINGS[scaling], device, theta, factor,
+                        original_len, low, high, 0.0 if amplitude is None else amplitude, given)
+        h = ctypes.c_void_p()
+        _check(lib().markov_rotary_plan_create(ctypes.byref(d), ctypes.byref(h)), "markov_rotary_plan_create")
+        self._h = h
+        self.head_dim, self.rot_dim, self.device = head_dim, rot_dim, device
+
+    @property
+    def handle(self):
+        return self._h
+
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().markov_rotary_plan_destroy(self._h)
+            self._h = None
+
+    def __del__(self):  # pragma: no cover
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+_FLOATS = {torch.bfloat16: MARKOV_BF16, torch.float16: MARKOV_F16, torch.float32: MARKOV_F32}
+
+
+def _heads(t, like, head_dim: int, name: str):
+    """(pointer, token stride, head stride, heads) of [tokens, heads, head_dim]."""
+    p = _dev(t, like.dtype, name)
+    if t.dim() != 3 or t.shape[0] != like.shape[0] or t.shape[2] != head_dim:
+        raise ValueError(f"{name} must be [{like.shape[0]}, heads, {head_dim}], got {tuple(t.shape)}")
+    n, heads, _ = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return p, s0 if n > 1 else 0, s1 if heads > 1 else head_dim, heads
+
+
+def markov_rotary(plan: RotaryPlan, q, k, positions, q_out=None, k_out=None, stream=None):
+    """Turn queries q [tokens, q_heads, head_dim] and keys k [tokens, k_heads,
+    head_dim] (bfloat16, float16 or float32; either may be None) by positions
+    [tokens] int32; returns (q_out, k_out), allocated when not given.  In place
+    with q_out=q and k_out=k."""
+    like = q if q is not None else k
+    if like is None:
+        raise ValueError("q or k must be given")
+    if not isinstance(like, torch.Tensor) or like.dtype not in _FLOATS:
+        raise TypeError("q and k must be bfloat16, float16 or float32")
+    if like.dim() != 3:
+        raise ValueError(f"q and k must be [tokens, heads, {plan.head_dim}], got {tuple(like.shape)}")
+    sides = []
+    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{name}_out without {name}")
+            sides.append(((None, 0, 0, 0), (None, 0, 0), None))
+            continue
+        a = _heads(x, like, plan.head_dim, name)
+        if y is None:
+            y = _new(stream, x.shape, x.dtype, x.device)
+        b = _heads(y, like, plan.head_dim, f"{name}_out")
+        if b[3] != a[3]:
+            raise ValueError(f"{name}_out must be of {name}'s shape")
+        sides.append((a, b[:3], y))
+    T = like.shape[0]
+    (qa, qb, q_out), (ka, kb, k_out) = sides
+    code = lib().markov_rotary(plan.handle, *qa, *ka, _FLOATS[like.dtype],
+                               _flat(positions, torch.int32, T, "positions"), T, *qb, *kb, _stream(stream))
+    _check(code, "markov_rotary")
+    return q_out, k_out
+
+
+def _e4m3_view(plan: PagedPlan, view: _E4m3View, t, scales, name: str):
+    """Describe an e4m3 cache and its scales in `view`, one of the thread's."""
+    view.data = _dev(t, torch.float8_e4m3fn, f"{name}_cache")
+    if t.dim() != 4 or t.shape[1:] != plan._cache_shape:
+        raise ValueError(f"{name}_cache must be [pages, {plan.page_size}, {plan.kv_heads}, {plan.head_dim}], "
+                         f"got {tuple(t.shape)}")
+    view.scales = _dev(scales, torch.float32, f"{name}_scales")
+    pages = t.shape[0]
+    if (scales.dim() != 3 or scales.shape[0] != pages or scales.shape[2] != plan.kv_heads or
+            scales.shape[1] < 1 or plan.page_size % scales.shape[1]):
+        raise ValueError(f"{name}_scales must be [{pages}, blocks of a page, {plan.kv_heads}], got {tuple(scales.shape)}")
+    s0, s1, s2, s3 = t.stride()
+    if s3 != 1:
+        raise ValueError(f"the last dimension of {name}_cache must be contiguous")
+    # the stride of a dimension of one element says nothing
+    blocks = scales.shape[1]
+    view.num_pages = pages
+    view.s_page, view.s_slot = s0 if pages > 1 else 0, s1
+    view.s_head = s2 if plan.kv_heads > 1 else plan.head_dim
+    c0, c1, c2 = scales.stride()
+    view.ss_page = c0 if pages > 1 else 0
+    view.ss_block = c1 if blocks > 1 else 0
+    view.ss_head = c2 if plan.kv_heads > 1 else 0
+    view.block = plan.page_size // blocks
+
+
+def _e4m3_views(plan: PagedPlan, k_cache, v_cache, k_scales, v_scales):
+    k_view, v_view, views = _views.e4m3
+    _e4m3_view(plan, k_view, k_cache, k_scales, "k")
+    _e4m3_view(plan, v_view, v_cache, v_scales, "v")
+    return views
+
+
+def markov_paged_write_e4m3(plan: PagedPlan, key, value, k_cache, v_cache, k_scales, v_scales, slots,
+                            keep_scales: bool = False, stream=None):
+    """Quantise key and value [tokens, kv_heads, head_dim] into the caches
+    [pages, page_size, kv_heads, head_dim] of float8_e4m3fn at their slots; slot
+    -1 is skipped.  k_scales and v_scales [pages, blocks of a page, kv_heads]
+    fp32 follow the values (a block whose first slot is written starts anew,
+    another's scale grows where it has to, its entries with it), or are used as
+    they are with keep_scales.  The tokens of one block must be neighbours, as
+    markov_paged_layout gives them."""
+    kp, k0, k1, T = _token_rows(plan, key, plan.kv_heads, "key")
+    vp, v0, v1, n = _token_rows(plan, value, plan.kv_heads, "value")
+    if n != T:
+        raise ValueError("key and value must have the same tokens")
+    code = lib().markov_paged_write_e4m3(plan.handle, kp, k0, k1, vp, v0, v1,
+                                         *_e4m3_views(plan, k_cache, v_cache, k_scales, v_scales),
+                                         _flat(slots, torch.int64, T, "slots"), T, int(bool(keep_scales)),
+                                         _stream(stream))
+    _check(code, "markov_paged_write_e4m3")
+
+
+def markov_paged_read_e4m3(plan: PagedPlan, k_cache, v_cache, k_scales, v_scales, page_table, row_state_idx,
+                           query_start, seq_lens, num_tokens: int, key=None, value=None, stream=None):
+    """Read the last query_start[b + 1] - query_start[b] of each row's seq_lens[b]
+    cached tokens back in the plan's dtype; returns (key, value) [num_tokens,
+    kv_heads, head_dim].  Tokens of padding rows are not written."""
+    rows, T = row_state_idx.shape[0], int(num_tokens)
+    shape = (T, plan.kv_heads, plan.head_dim)
+    if key is None:
+        key = _new(stream, shape, plan.dtype, k_cache.device)
+    if value is None:
+        value = _new(stream, shape, plan.dtype, k_cache.device)
+    kp, k0, k1, n = _token_rows(plan, key, plan.kv_heads, "key")
+    vp, v0, v1, n2 = _token_rows(plan, value, plan.kv_heads, "value")
+    if n != T or n2 != T:
+        raise ValueError(f"key and value must have {T} tokens")
+    code = lib().markov_paged_read_e4m3(
+        plan.handle, *_e4m3_views(plan, k_cache, v_cache, k_scales, v_scales), *_page_table(page_table),
+        _flat(row_state_idx, torch.int64, rows, "row_state_idx"),
+        _flat(query_start, torch.int32, rows + 1, "query_start"),
+        _flat(seq_lens, torch.int32, rows, "seq_lens"), rows, T, kp, k0, k1, vp, v0, v1, _stream(stream))
+    _check(code, "markov_paged_read_e4m3")
+    return key, value
+
+
+def markov_paged_attention_e4m3(plan: PagedPlan, q, k_cache, v_cache, k_scales, v_scales, page_table,
+                                row_state_idx, query_start, seq_lens, scale: float | None = None,
+                                window: int = 0, sinks: int = 0, out=None, lse=None, stream=None):
+    """markov_paged_attention over caches of float8_e4m3fn whose elements stand
+    for their value times the scale of their block and head (k_scales and
+    v_scales [pages, blocks of a page, kv_heads] fp32; expanded ones share a
+    scale); returns (out, lse)."""
+    rows = row_state_idx.shape[0]
+    qp, q0, q1, T = _token_rows(plan, q, plan.q_heads, "q")
+    if out is None:
+        out = _new(stream, (T, plan.q_heads, plan.head_dim), plan.dtype, q.device)
+    op, o0, o1, n = _token_rows(plan, out, plan.q_heads, "out")
+    if n != T:
+        raise ValueError("out must have q's tokens")
+    if lse is True:
+        lse = _new(stream, (T, plan.q_heads), torch.float32, q.device)
+    code = lib().markov_paged_attention_e4m3(
+        plan.handle, qp, q0, q1, *_e4m3_views(plan, k_cache, v_cache, k_scales, v_scales),
+        *_page_table(page_table), _flat(row_state_idx, torch.int64, rows, "row_state_idx"),
+        _flat(query_start, torch.int32, rows + 1, "query_start"),
+        _flat(seq_lens, torch.int32, rows, "seq_lens"), rows, T,
+        float(plan.head_dim ** -0.5 if scale is None else scale), int(window), int(sinks), op, o0, o1,
+        None if lse is None else _flat(lse, torch.float32, T * plan.q_heads, "lse"), _stream(stream))
+    _check(code, "markov_paged_attention_e4m3")
+    return out, lse
+
+
+class Logprobs(NamedTuple):
+    """What markov_logprobs returns; None for what was not asked for."""
+    logprobs: torch.Tensor | None
+    ranks: torch.Tensor | None
+    entropy: torch.Tensor
+    top_ids: torch.Tensor | None
+    top_logprobs: torch.Tensor | None
+
+
+def markov_logprobs(logits, tokens=None, temperature=None, top: int = 0, logprobs=None, ranks=None,
+                    entropy=None, top_ids=None, top_logprobs=None, stream=None) -> Logprobs:
+    """Log probabilities of tokens [rows] int64 under softmax(logits / T), their
+    ranks, the entropy, and the `top` most probable ids with theirs, from logits
+    [rows, vocab] (bfloat16 or float32, rows contiguous).  temperature [rows]
+    fp32; without one, and where it is not above 0, T is 1.  Rows whose token is
+    outside the vocabulary (-1) are not written; without tokens every row is
+    taken, for entropy and alternatives only."""
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGITS:
+        raise TypeError("logits must be bfloat16 or float32")
+    p = _dev(logits, logits.dtype, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [rows, vocab], got {tuple(logits.shape)}")
+    rows, V = logits.shape
+    s0, s1 = logits.stride()
+    if s1 != 1 and V > 1:
+        raise ValueError("the rows of logits must be contiguous")
+    top = int(top)
+    f32, i32, dev = torch.float32, torch.int32, logits.device
+    if tokens is None and (logprobs is not None or ranks is not None):
+        raise ValueError("logprobs and ranks need tokens")
+    if stream is None:
+        # of the logits' device, whichever is current
+        stream = torch.cuda.current_stream(dev)
+        new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    else:
+        new = lambda shape, dtype: _new(stream, shape, dtype, dev)  # noqa: E731
+    if tokens is not None:
+        logprobs = new((rows,), f32) if logprobs is None else logprobs
+        ranks = new((rows,), i32) if ranks is None else ranks
+    entropy = new((rows,), f32) if entropy is None else entropy
+    if top > 0:
+        top_ids = new((rows, top), i32) if top_ids is None else top_ids
+        top_logprobs = new((rows, top), f32) if top_logprobs is None else top_logprobs
+    else:
+        top_ids = top_logprobs = None
+
+    def at(t, dtype, n, name):
+        return None if t is None else _flat(t, dtype, n, name)
+
+    code = lib().markov_logprobs(
+        p, _LOGITS[logits.dtype], s0 if rows > 1 else V, rows, V, at(tokens, torch.int64, rows, "tokens"),
+        at(temperature, f32, rows, "temperature"), top, at(logprobs, f32, rows, "logprobs"),
+        at(ranks, i32, rows, "ranks"), at(entropy, f32, rows, "entropy"), at(top_ids, i32, rows * top, "top_ids"),
+        at(top_logprobs, f32, rows * top, "top_logprobs"), _stream(stream))
+    _check(code, "markov_logprobs")
+    return Logprobs(logprobs, ranks, entropy, top_ids, top_logprobs)

@@ -48,6 +48,51 @@ struct WriteArgs {
     const uint32_t *status;
 };
 
+// One side of an e4m3 cache; data strides in bytes, scale strides in floats.
+struct E4m3Side {
+    uint8_t *data;
+    int64_t s_page, s_slot, s_head;
+    float *scales;
+    int64_t ss_page, ss_block, ss_head;
+    int block_shift;           // log2 of the tokens of a scale
+};
+
+// One side of a store into an e4m3 cache: [T, heads, D] of 16-bit elements.
+struct StoreSide {
+    const uint4 *src;
+    int64_t src_s0, src_s1;    // in 16-byte units
+    E4m3Side cache;
+};
+
+struct StoreArgs {
+    StoreSide side[2];         // keys, values
+    const int64_t *slots;
+    int64_t num_slots;
+    int T, heads, page_shift;
+    int chunk;                 // tokens whose blocks a thread block looks after
+    const uint32_t *status;
+};
+
+// The rows of a call over a paged cache.
+struct PagedRows {
+    const int32_t *table;
+    int64_t table_s0;
+    int num_states, room, page_shift;
+    int64_t num_pages;
+    const int64_t *idx;
+    const int32_t *query_start, *seq_lens;
+    int rows, T;
+};
+
+struct FetchArgs {
+    PagedRows r;
+    E4m3Side side[2];
+    uint4 *dst[2];
+    int64_t dst_s0[2], dst_s1[2];          // in 16-byte units
+    int heads, tile;           // tile: tokens of a block
+    const uint32_t *status;
+};
+
 struct AttnArgs {
     int negate;                // the scale is negative
     const int32_t *table;
@@ -68,6 +113,30 @@ struct AttnArgs {
     uint32_t *status;
     uint64_t timeout_ns;
     uint64_t walk_ns;          // the same with the time that the walk to the first item may take
+};
+
+// The scales of one side of an e4m3 cache, as attention reads them.
+struct E4m3Scales {
+    const float *p;
+    int64_t s_page, s_block, s_head;
+    int block_shift;
+};
+
+struct AttnE4m3Args {
+    PagedRows r;
+    E4m3Scales ks, vs;
+    int q_heads, kv_heads, group;
+    float scale2;              // scale log2(e)
+    int window, sinks;
+    const uint16_t *q;
+    int64_t q_s0, q_s1;
+    uint16_t *out;
+    int64_t out_s0, out_s1;
+    float *lse;
+    float *parts;              // split items' parts
+    void *joins;               // the item that begins in a worker's range and goes on
+    uint32_t *status;
+    uint64_t timeout_ns;
 };
 
 struct VerifyArgs {
@@ -99,6 +168,14 @@ constexpr int kVerifyMaxSegs = 32;         // a lane each
 
 cudaError_t launch_paged_layout(const LayoutArgs &a, cudaStream_t s);
 cudaError_t launch_paged_write(const WriteArgs &a, cudaStream_t s);
+cudaError_t launch_store_e4m3(const StoreArgs &a, int head_dim, bool f16, bool keep, cudaStream_t s);
+cudaError_t launch_fetch_e4m3(const FetchArgs &a, int head_dim, bool f16, cudaStream_t s);
+cudaError_t attention_e4m3_prepare();
+size_t attention_e4m3_parts(int head_dim, int blocks);
+size_t attention_e4m3_joins(int blocks);
+// Calls of few query rows a request: k and v are maps of 16 slots by head_dim.
+cudaError_t launch_attention_e4m3_few(const AttnE4m3Args &a, const CUtensorMap &k, const CUtensorMap &v, int head_dim,
+                                      bool f16, bool half, int blocks, cudaStream_t s);
 cudaError_t paged_attention_prepare();
 size_t paged_attention_parts(int head_dim, int blocks);
 size_t paged_attention_joins(int blocks);

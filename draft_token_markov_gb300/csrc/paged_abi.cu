@@ -1,6 +1,7 @@
 // paged_abi.cu -- host side of the paged calls declared in include/markov.h:
 // plan creation (all scratch allocated once), argument checks, launches and
 // the sticky device status.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -79,9 +80,71 @@ bool encode_query_map(CUtensorMap *m, const void *q, int64_t s0, int64_t s1, int
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// An e4m3 cache view of the plan's pages; scales that are written must be the
+// blocks' own.
+bool valid_view(const markov_e4m3_view *v, const markov_paged_desc &d, bool scales_written) {
+    if (!v || !v->data || !aligned16(v->data) || !v->scales || (reinterpret_cast<uintptr_t>(v->scales) & 3u)) return false;
+    if (v->num_pages < 1 || v->num_pages > INT32_MAX) return false;
+    if (v->s_page < 0 || v->s_slot < d.head_dim || v->s_head < d.head_dim) return false;
+    if (v->s_page % 16 || v->s_slot % 16 || v->s_head % 16) return false;
+    if (v->block < 16 || v->block > d.page_size || (v->block & (v->block - 1)) != 0) return false;
+    if (v->ss_page < 0 || v->ss_block < 0 || v->ss_head < 0) return false;
+    if (scales_written)
+        return (v->num_pages == 1 || v->ss_page > 0) && (v->block == d.page_size || v->ss_block > 0) &&
+               (d.kv_heads == 1 || v->ss_head > 0);
+    return true;
+}
+
+int log2_of(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+
+E4m3Side side_of(const markov_e4m3_view &v) {
+    return E4m3Side{static_cast<uint8_t *>(v.data), v.s_page, v.s_slot, v.s_head, v.scales, v.ss_page, v.ss_block, v.ss_head,
+                    log2_of(v.block)};
+}
+
+E4m3Scales scales_of(const markov_e4m3_view &v) {
+    return E4m3Scales{v.scales, v.ss_page, v.ss_block, v.ss_head, log2_of(v.block)};
+}
+
+// An e4m3 cache as [pages, heads, slots, head_dim] tiles of `slots` slots; the
+// swizzle spans a slot's bytes of a head.
+bool encode_e4m3_map(CUtensorMap *m, const markov_e4m3_view &v, const markov_paged_plan &p, int slots) {
+    const EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn) return false;
+    const int page = p.d.page_size;
+    const cuuint64_t dims[4] = {(cuuint64_t)p.d.head_dim, (cuuint64_t)page, (cuuint64_t)p.d.kv_heads,
+                                (cuuint64_t)v.num_pages};
+    // a lone page's stride is never used, but has to be one
+    const int64_t s_page = v.num_pages > 1 ? v.s_page : v.s_slot * page;
+    const cuuint64_t strides[3] = {(cuuint64_t)v.s_slot, (cuuint64_t)v.s_head, (cuuint64_t)s_page};
+    const cuuint32_t box[4] = {(cuuint32_t)p.d.head_dim, (cuuint32_t)(page < slots ? page : slots), 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, v.data, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              p.d.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What a call over a paged cache says of its rows.
+bool valid_table(const void *page_table, int64_t table_s0, int32_t num_states, int32_t table_width, const void *idx,
+                 const void *query_start, const void *seq_lens, const markov_paged_plan &p) {
+    return page_table && idx && query_start && seq_lens && num_states >= 1 && table_width >= 1 &&
+           table_s0 >= table_width && ((int64_t)table_width << p.page_shift) <= kMaxRoom;
+}
+
 // Token rows [T, heads, head_dim].
 bool valid_rows(const void *p, int64_t s0, int64_t s1, const markov_paged_desc &d) {
     return p && aligned16(p) && s0 >= 0 && s1 >= d.head_dim && s0 % 8 == 0 && s1 % 8 == 0;
+}
+
+PagedRows rows_of(const markov_paged_plan &p, const int32_t *page_table, int64_t table_s0, int32_t num_states,
+                  int32_t table_width, int64_t num_pages, const int64_t *idx, const int32_t *query_start,
+                  const int32_t *seq_lens, int32_t rows, int32_t num_tokens) {
+    return PagedRows{page_table, table_s0, num_states, (int)((int64_t)table_width << p.page_shift), p.page_shift, num_pages, idx,
+                     query_start, seq_lens, rows, num_tokens};
 }
 
 }  // namespace
@@ -120,10 +183,13 @@ markov_status markov_paged_plan_create(const markov_paged_desc *desc, markov_pag
     p->sm_count = prop.multiProcessorCount;
     while ((1 << p->page_shift) < d.page_size) ++p->page_shift;
     p->blocks = p->sm_count;
-    if (paged_attention_prepare() != cudaSuccess ||
+    // the scratch serves the calls over either kind of cache
+    const size_t parts = std::max(paged_attention_parts(d.head_dim, p->blocks), attention_e4m3_parts(d.head_dim, p->blocks));
+    const size_t joins = std::max(paged_attention_joins(p->blocks), attention_e4m3_joins(p->blocks));
+    if (paged_attention_prepare() != cudaSuccess || attention_e4m3_prepare() != cudaSuccess ||
         cudaMalloc(&p->ctrl, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
-        cudaMalloc(&p->parts, paged_attention_parts(d.head_dim, p->blocks) * sizeof(float)) != cudaSuccess ||
-        cudaMalloc(&p->joins, paged_attention_joins(p->blocks)) != cudaSuccess ||
+        cudaMalloc(&p->parts, parts * sizeof(float)) != cudaSuccess ||
+        cudaMalloc(&p->joins, joins) != cudaSuccess ||
         cudaMemset(p->ctrl, 0, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
         cudaDeviceSynchronize() != cudaSuccess) {
         cudaGetLastError();
@@ -321,6 +387,132 @@ markov_status markov_paged_attention(markov_paged_plan *p, const void *q, int64_
     a.walk_ns = a.timeout_ns + (uint64_t)((int64_t)num_tokens * a.group / 256 + rows + 1) * 1000ull;
     if (launch_paged_attention(a, qmap, kmap, vmap, p->d.head_dim, p->d.dtype == MARKOV_F16, p->blocks,
                                (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return MARKOV_ECUDA;
+    }
+    return MARKOV_OK;
+}
+
+markov_status markov_paged_write_e4m3(markov_paged_plan *p, const void *key, int64_t key_s0,
+                                      int64_t key_s1, const void *value, int64_t value_s0,
+                                      int64_t value_s1, const markov_e4m3_view *k_cache,
+                                      const markov_e4m3_view *v_cache, const int64_t *slots,
+                                      int32_t num_tokens, int32_t keep_scales, void *stream) {
+    if (!p || num_tokens < 0 || (int64_t)num_tokens * p->d.kv_heads > INT32_MAX) return MARKOV_EINVAL;
+    if (keep_scales != 0 && keep_scales != 1) return MARKOV_EINVAL;
+    if (num_tokens == 0) return MARKOV_OK;
+    if (!valid_rows(key, key_s0, key_s1, p->d) || !valid_rows(value, value_s0, value_s1, p->d) ||
+        !valid_view(k_cache, p->d, !keep_scales) || !valid_view(v_cache, p->d, !keep_scales) || !slots ||
+        k_cache->num_pages != v_cache->num_pages)
+        return MARKOV_EINVAL;
+    DeviceGuard guard(p->d.device);
+    if (!guard.ok) return MARKOV_EDEVICE;
+    StoreArgs a{};
+    a.side[0] = StoreSide{static_cast<const uint4 *>(key), key_s0 / 8, key_s1 / 8, side_of(*k_cache)};
+    a.side[1] = StoreSide{static_cast<const uint4 *>(value), value_s0 / 8, value_s1 / 8, side_of(*v_cache)};
+    a.slots = slots;
+    a.num_slots = k_cache->num_pages << p->page_shift;
+    a.T = num_tokens;
+    a.heads = p->d.kv_heads;
+    a.page_shift = p->page_shift;
+    // a token a block while all of them are resident, else a cache block's worth
+    a.chunk = (int64_t)num_tokens * p->d.kv_heads <= 2048 ? 1 : k_cache->block;
+    a.status = p->ctrl;
+    if (launch_store_e4m3(a, p->d.head_dim, p->d.dtype == MARKOV_F16, keep_scales != 0, (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return MARKOV_ECUDA;
+    }
+    return MARKOV_OK;
+}
+
+markov_status markov_paged_read_e4m3(markov_paged_plan *p, const markov_e4m3_view *k_cache,
+                                     const markov_e4m3_view *v_cache, const int32_t *page_table,
+                                     int64_t table_s0, int32_t num_states, int32_t table_width,
+                                     const int64_t *row_state_idx, const int32_t *query_start,
+                                     const int32_t *seq_lens, int32_t rows, int32_t num_tokens,
+                                     void *key, int64_t key_s0, int64_t key_s1, void *value,
+                                     int64_t value_s0, int64_t value_s1, void *stream) {
+    if (!p || num_tokens < 0 || rows < 1 || rows > p->d.max_rows) return MARKOV_EINVAL;
+    if (!valid_table(page_table, table_s0, num_states, table_width, row_state_idx, query_start, seq_lens, *p) ||
+        !valid_view(k_cache, p->d, false) || !valid_view(v_cache, p->d, false) ||
+        k_cache->num_pages != v_cache->num_pages)
+        return MARKOV_EINVAL;
+    if (num_tokens == 0) return MARKOV_OK;
+    if (!valid_rows(key, key_s0, key_s1, p->d) || !valid_rows(value, value_s0, value_s1, p->d) || key == value)
+        return MARKOV_EINVAL;
+    DeviceGuard guard(p->d.device);
+    if (!guard.ok) return MARKOV_EDEVICE;
+    FetchArgs a{};
+    a.r = rows_of(*p, page_table, table_s0, num_states, table_width, k_cache->num_pages, row_state_idx, query_start, seq_lens,
+                  rows, num_tokens);
+    a.side[0] = side_of(*k_cache);
+    a.side[1] = side_of(*v_cache);
+    a.dst[0] = static_cast<uint4 *>(key);
+    a.dst[1] = static_cast<uint4 *>(value);
+    a.dst_s0[0] = key_s0 / 8;
+    a.dst_s1[0] = key_s1 / 8;
+    a.dst_s0[1] = value_s0 / 8;
+    a.dst_s1[1] = value_s1 / 8;
+    a.heads = p->d.kv_heads;
+    // two blocks a multiprocessor before a block takes more tokens
+    a.tile = 1;
+    while (a.tile < 32 && num_tokens / (2 * a.tile) >= 2 * p->sm_count) a.tile *= 2;
+    a.status = p->ctrl;
+    if (launch_fetch_e4m3(a, p->d.head_dim, p->d.dtype == MARKOV_F16, (cudaStream_t)stream) != cudaSuccess) {
+        cudaGetLastError();
+        return MARKOV_ECUDA;
+    }
+    return MARKOV_OK;
+}
+
+markov_status markov_paged_attention_e4m3(
+    markov_paged_plan *p, const void *q, int64_t q_s0, int64_t q_s1,
+    const markov_e4m3_view *k_cache, const markov_e4m3_view *v_cache, const int32_t *page_table,
+    int64_t table_s0, int32_t num_states, int32_t table_width, const int64_t *row_state_idx,
+    const int32_t *query_start, const int32_t *seq_lens, int32_t rows, int32_t num_tokens,
+    float scale, int32_t window, int32_t sinks, void *out, int64_t out_s0, int64_t out_s1,
+    float *lse, void *stream) {
+    if (!p || num_tokens < 0 || rows < 1 || rows > p->d.max_rows) return MARKOV_EINVAL;
+    if (!std::isfinite(scale) || window < 0 || sinks < 0) return MARKOV_EINVAL;
+    if (!valid_table(page_table, table_s0, num_states, table_width, row_state_idx, query_start, seq_lens, *p) ||
+        !valid_view(k_cache, p->d, false) || !valid_view(v_cache, p->d, false) ||
+        k_cache->num_pages != v_cache->num_pages)
+        return MARKOV_EINVAL;
+    const int group = p->d.q_heads / p->d.kv_heads;
+    if ((int64_t)num_tokens * group > INT32_MAX / 2) return MARKOV_EINVAL;
+    if (num_tokens == 0) return MARKOV_OK;
+    if (!valid_rows(q, q_s0, q_s1, p->d) || !valid_rows(out, out_s0, out_s1, p->d) || q == out)
+        return MARKOV_EINVAL;
+    DeviceGuard guard(p->d.device);
+    if (!guard.ok) return MARKOV_EDEVICE;
+    AttnE4m3Args a{};
+    a.r = rows_of(*p, page_table, table_s0, num_states, table_width, k_cache->num_pages, row_state_idx, query_start, seq_lens,
+                  rows, num_tokens);
+    a.ks = scales_of(*k_cache);
+    a.vs = scales_of(*v_cache);
+    a.q_heads = p->d.q_heads;
+    a.kv_heads = p->d.kv_heads;
+    a.group = group;
+    a.scale2 = scale * 1.4426950408889634f;
+    a.window = window;
+    // a row has no more keys than kMaxRoom
+    a.sinks = sinks < kMaxRoom ? sinks : (int)kMaxRoom;
+    a.q = static_cast<const uint16_t *>(q);
+    a.q_s0 = q_s0;
+    a.q_s1 = q_s1;
+    a.out = static_cast<uint16_t *>(out);
+    a.out_s0 = out_s0;
+    a.out_s1 = out_s1;
+    a.lse = lse;
+    a.parts = p->parts;
+    a.joins = p->joins;
+    a.status = p->ctrl;
+    a.timeout_ns = (uint64_t)p->d.timeout_ms * 1000000ull;
+    CUtensorMap kmap, vmap;
+    if (!encode_e4m3_map(&kmap, *k_cache, *p, 16) || !encode_e4m3_map(&vmap, *v_cache, *p, 16)) return MARKOV_EINVAL;
+    const bool half = (int64_t)num_tokens * group <= 8 * (int64_t)rows;
+    if (launch_attention_e4m3_few(a, kmap, vmap, p->d.head_dim, p->d.dtype == MARKOV_F16, half, p->blocks,
+                                  (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();
         return MARKOV_ECUDA;
     }

@@ -1,0 +1,286 @@
+// paged_e4m3.cu -- the store of keys and values into a paged cache of e4m3 with a
+// scale for each block of tokens and head, and reading it back.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "e4m3.cuh"
+#include "paged.h"
+
+namespace dtm {
+
+// 8 elements of the plan's type as fp32.
+template <bool F16>
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (F16) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        } else {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- store
+//
+// A block's scale needs the largest of the call's values for it before the first
+// of them is rounded, and a block that was begun by earlier calls may have to be
+// rescaled: a thread block (chunk of tokens, head, side) takes the cache blocks
+// whose first token of the call lies in its chunk, one after the other, with all
+// of their tokens, also those past the chunk.  Up to kHeld * 128 vectors of them
+// stay in registers between the maximum and the rounding, the rest is read
+// again.  Rescaling comes before the new values, so that it need not know which
+// entries they replace.  Bound by memory: the elements are read once and written
+// as bytes.
+constexpr int kStoreThreads = 128;
+constexpr int kHeld = 8;
+
+// x / s, rounded: by its reciprocal where that is exact (s a power of two).
+__device__ __forceinline__ uint2 round8(const float (&x)[8], float s, float inv) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = inv != 0.0f ? x[i] * inv : __fdiv_rn(x[i], s);
+    return make_uint2(e4m3_of_f32(y[0], y[1], y[2], y[3]), e4m3_of_f32(y[4], y[5], y[6], y[7]));
+}
+
+// 1 / s where it is exact and normal, else 0.
+__device__ __forceinline__ float exact_inverse(float s) {
+    const uint32_t b = __float_as_uint(s), e = b >> 23;
+    return (b & 0x7fffffu) == 0u && e >= 1u && e <= 252u ? __uint_as_float((254u - e) << 23) : 0.0f;
+}
+
+template <int D, bool F16, bool KEEP>
+__global__ void __launch_bounds__(kStoreThreads) store_e4m3_kernel(const __grid_constant__ StoreArgs a) {
+    if (__ldcg(a.status) != 0u) return;
+    constexpr int kLanes = D / 8, kTokens = kStoreThreads / kLanes;     // threads of a token, tokens of a turn
+    __shared__ uint32_t top_s[kStoreThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, sub = tid / kLanes, vec = tid % kLanes;
+    const StoreSide &side = a.side[blockIdx.z];
+    const E4m3Side &c = side.cache;
+    const int head = blockIdx.y, t_first = blockIdx.x * a.chunk, t_last = min(t_first + a.chunk, a.T);
+    const int64_t in_page = (1 << a.page_shift) - 1;
+    const auto slot_at = [&](int t) {
+        const int64_t s = t >= 0 && t < a.T ? __ldg(a.slots + t) : -1;
+        return s >= 0 && s < a.num_slots ? s : (int64_t)-1;
+    };
+    const auto load = [&](int t) { return __ldcs(side.src + t * side.src_s0 + head * side.src_s1 + vec); };
+    const auto store = [&](int64_t slot, const uint4 &v, float s, float inv) {
+        float x[8];
+        unpack8<F16>(v, x);
+        uint8_t *to = c.data + (slot >> a.page_shift) * c.s_page + (slot & in_page) * c.s_slot + head * c.s_head + 8 * vec;
+        *reinterpret_cast<uint2 *>(to) = round8(x, s, inv);
+    };
+    const auto scale_at = [&](int64_t slot) {
+        return c.scales + (slot >> a.page_shift) * c.ss_page + ((slot & in_page) >> c.block_shift) * c.ss_block +
+               head * c.ss_head;
+    };
+    if (KEEP) {
+        for (int t = t_first + sub; t < t_last; t += kTokens) {
+            const int64_t slot = slot_at(t);
+            if (slot < 0) continue;
+            const float s = __ldg(scale_at(slot));
+            store(slot, load(t), s, exact_inverse(s));
+        }
+        return;
+    }
+    int64_t before = slot_at(t_first - 1);
+    for (int t0 = t_first; t0 < t_last;) {
+        // the tokens [t0, t1) of one cache block, which no earlier one began
+        const int64_t slot0 = slot_at(t0), block = slot0 >> c.block_shift;
+        int t1 = t0 + 1;
+        bool anew = false;
+        if (slot0 >= 0) {
+            for (int base = t0;; base += kStoreThreads) {
+                const int64_t s = slot_at(base + tid);
+                const bool same = s >= 0 && s >> c.block_shift == block;
+                // the first that is not of the block ends the run
+                const int n = __syncthreads_count(same);
+                if (n == kStoreThreads) {
+                    if (__syncthreads_or((s & ((1 << c.block_shift) - 1)) == 0)) anew = true;
+                    continue;
+                }
+                __shared__ int end_s;
+                if (tid == 0) end_s = kStoreThreads;
+                __syncthreads();
+                if (!same) atomicMin(&end_s, tid);
+                __syncthreads();
+                const int end = end_s;
+                t1 = base + end;
+                if (__syncthreads_or(tid < end && (s & ((1 << c.block_shift) - 1)) == 0)) anew = true;
+                break;
+            }
+        }
+        const bool mine = slot0 >= 0 && (before < 0 || before >> c.block_shift != block);
+        if (!mine) {
+            before = slot_at(t1 - 1);
+            t0 = t1;
+            continue;
+        }
+        float *scale = scale_at(slot0);
+        const float old = __ldcg(scale);
+        uint4 held[kHeld];
+        float top = 0.0f;
+        const auto look = [&](const uint4 &v) {
+            float x[8];
+            unpack8<F16>(v, x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = fabsf(x[i]);
+                top = y < INFINITY ? fmaxf(top, y) : top;
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int t = t0 + k * kTokens + sub;
+            held[k] = t < t1 ? load(t) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) look(held[k]);
+        for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) look(load(t));
+        uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        if (lane == 0) top_s[tid >> 5] = bits;
+        __syncthreads();                              // every thread has read the old scale
+        bits = top_s[0];
+#pragma unroll
+        for (int w = 1; w < kStoreThreads / 32; ++w) bits = max(bits, top_s[w]);
+        float s = scale_of(__uint_as_float(bits));
+        if (!anew && usable_scale(old)) {
+            if (s > old) {
+                // the block's entries so far, 16 bytes a thread
+                const float ratio = __fdiv_rn(old, s);
+                constexpr int kVec = D / 16;
+                uint8_t *at = c.data + (slot0 >> a.page_shift) * c.s_page + head * c.s_head +
+                              ((slot0 & in_page) >> c.block_shift << c.block_shift) * c.s_slot;
+                for (int i = tid; i < kVec << c.block_shift; i += kStoreThreads) {
+                    uint4 *p = reinterpret_cast<uint4 *>(at + (i / kVec) * c.s_slot + i % kVec * 16);
+                    uint4 v = *p;
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 lo = f32x2_of_e4m3(w[j]), hi = f32x2_of_e4m3(w[j] >> 16);
+                        w[j] = e4m3_of_f32(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
+                    }
+                    *p = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                __syncthreads();
+            } else {
+                s = old;
+            }
+        }
+        const float inv = exact_inverse(s);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            const int t = t0 + k * kTokens + sub;
+            if (t < t1) store(slot_at(t), held[k], s, inv);
+        }
+        for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) store(slot_at(t), load(t), s, inv);
+        if (tid == 0) *scale = s;
+        __syncthreads();                              // top_s is free
+        before = slot_at(t1 - 1);
+        t0 = t1;
+    }
+}
+
+template <int D, bool F16>
+static cudaError_t launch_store_typed(const StoreArgs &a, bool keep, cudaStream_t s) {
+    const dim3 grid((a.T + a.chunk - 1) / a.chunk, a.heads, 2);
+    if (keep)
+        store_e4m3_kernel<D, F16, true><<<grid, kStoreThreads, 0, s>>>(a);
+    else
+        store_e4m3_kernel<D, F16, false><<<grid, kStoreThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_store_e4m3(const StoreArgs &a, int head_dim, bool f16, bool keep, cudaStream_t s) {
+    if (head_dim == 64)
+        return f16 ? launch_store_typed<64, true>(a, keep, s) : launch_store_typed<64, false>(a, keep, s);
+    return f16 ? launch_store_typed<128, true>(a, keep, s) : launch_store_typed<128, false>(a, keep, s);
+}
+
+// ------------------------------------------------------------------- fetch
+//
+// A thread block finds the slots of its tokens (a binary search over the rows, a
+// thread a token), then copies their vectors of 16 bytes, each to 32.  Bound by
+// memory.
+constexpr int kFetchThreads = 256;
+constexpr int kFetchTokens = 32;
+
+template <int D, bool F16>
+__global__ void __launch_bounds__(kFetchThreads) fetch_e4m3_kernel(const __grid_constant__ FetchArgs a) {
+    if (__ldcg(a.status) != 0u) return;
+    // page * 2^32 + slot in it; kNone: zeros, kSkip: not a row's
+    constexpr int64_t kNone = -1, kSkip = -2;
+    __shared__ int64_t where[kFetchTokens];
+    const int tid = threadIdx.x, t0 = blockIdx.x * a.tile, tokens = min(a.tile, a.r.T - t0);
+    if (tid < tokens) {
+        const int t = t0 + tid;
+        // the last row that begins at or before t, then back over empty ones
+        int lo = 0, hi = a.r.rows;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(a.r.query_start + mid) <= t) lo = mid; else hi = mid;
+        }
+        const int qs = __ldg(a.r.query_start + lo), qe = __ldg(a.r.query_start + lo + 1);
+        const int64_t state = __ldg(a.r.idx + lo);
+        int64_t at = kSkip;
+        if (t >= qs && t < qe && state >= 0) {
+            const int64_t pos = (int64_t)max(__ldg(a.r.seq_lens + lo), 0) - (qe - qs) + (t - qs);
+            at = kNone;
+            if (pos >= 0 && pos < a.r.room && state < a.r.num_states) {
+                const int page = __ldg(a.r.table + state * a.r.table_s0 + (pos >> a.r.page_shift));
+                if (page >= 0 && page < a.r.num_pages) at = (int64_t)page << 32 | (pos & ((1 << a.r.page_shift) - 1));
+            }
+        }
+        where[tid] = at;
+    }
+    __syncthreads();
+    constexpr int kVec = D / 16;
+    const int n = tokens * a.heads * kVec;
+#pragma unroll 2
+    for (int i = tid; i < n; i += kFetchThreads) {
+        const int th = i / kVec, v = i % kVec, t = th / a.heads, h = th - t * a.heads;
+        const int64_t at = where[t];
+        if (at == kSkip) continue;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const E4m3Side &c = a.side[k];
+            uint4 x = make_uint4(0, 0, 0, 0);
+            float s = 0.0f;
+            if (at != kNone) {
+                const int64_t page = at >> 32, slot = at & 0xffffffff;
+                x = __ldcs(reinterpret_cast<const uint4 *>(c.data + page * c.s_page + slot * c.s_slot + h * c.s_head + 16 * v));
+                s = __ldg(c.scales + page * c.ss_page + (slot >> c.block_shift) * c.ss_block + h * c.ss_head);
+            }
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = f32x2_of_e4m3(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]);
+                if (F16)
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y[j]) : "f"(f.y * s), "f"(f.x * s));
+                else
+                    y[j] = bf16x2_rn(f.x * s, f.y * s);
+            }
+            uint4 *to = a.dst[k] + (int64_t)(t0 + t) * a.dst_s0[k] + h * a.dst_s1[k] + 2 * v;
+            to[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            to[1] = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+    }
+}
+
+template <int D, bool F16>
+static cudaError_t launch_fetch_typed(const FetchArgs &a, cudaStream_t s) {
+    fetch_e4m3_kernel<D, F16><<<(a.r.T + a.tile - 1) / a.tile, kFetchThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fetch_e4m3(const FetchArgs &a, int head_dim, bool f16, cudaStream_t s) {
+    if (head_dim == 64) return f16 ? launch_fetch_typed<64, true>(a, s) : launch_fetch_typed<64, false>(a, s);
+    return f16 ? launch_fetch_typed<128, true>(a, s) : launch_fetch_typed<128, false>(a, s);
+}
+
+}  // namespace dtm

@@ -585,6 +585,185 @@ markov_status markov_verify(markov_plan *plan, const void *target_logits,
                             int64_t tok_s0, int32_t *num_accepted, float *target_probs,
                             float *draft_probs, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Around the verify step: rotary positions, a paged cache of 8 bits, and log
+ * probabilities.  Additions of this library, as the verify step is. */
+
+/* How the angles of a rotary plan are scaled for contexts longer than the
+ * model was trained on.  With f_i = theta^(-2 i / rot_dim) the angle per
+ * position of pair i, s = factor and L = original_len:
+ *   NONE        f_i
+ *   LINEAR      f_i / s
+ *   BASE        theta' = theta s^(rot_dim / (rot_dim - 2)) in theta's place
+ *   PARTS       f_i (1 - t) + f_i / s t, t = clamp((i - a) / (b - a), 0, 1), where
+ *               a = max(floor(d(high)), 0), b = min(ceil(d(low)), rot_dim - 1) and
+ *               d(r) = rot_dim ln(L / (2 pi r)) / (2 ln theta) is the pair that
+ *               turns r times in L positions (b - a is at least 0.001)
+ *   WAVELENGTH  f_i t + f_i / s (1 - t), t = clamp((L f_i / (2 pi) - low) / (high -
+ *               low), 0, 1)
+ *   GIVEN       the caller's frequencies */
+typedef enum markov_rotary_scaling {
+    MARKOV_ROTARY_NONE = 0,
+    MARKOV_ROTARY_LINEAR = 1,
+    MARKOV_ROTARY_BASE = 2,
+    MARKOV_ROTARY_PARTS = 3,
+    MARKOV_ROTARY_WAVELENGTH = 4,
+    MARKOV_ROTARY_GIVEN = 5
+} markov_rotary_scaling;
+
+typedef struct markov_rotary_desc {
+    int32_t head_dim;     /* a multiple of 16, 16 .. 512 */
+    int32_t rot_dim;      /* the leading dims that turn: a multiple of 16, 16 .. head_dim */
+    int32_t interleaved;  /* 0: pairs (i, i + rot_dim / 2); 1: pairs (2 i, 2 i + 1) */
+    int32_t scaling;      /* markov_rotary_scaling */
+    int32_t device;
+    double theta;         /* > 1 */
+    double factor;        /* > 0 */
+    double original_len;  /* > 0 where PARTS or WAVELENGTH needs it */
+    double low, high;     /* 0 < low < high, likewise */
+    double amplitude;     /* sines and cosines are multiplied by it; 0: 0.1 ln(factor) + 1
+                             with PARTS and a factor above 1, else 1 */
+    const double *frequencies;  /* host, [rot_dim / 2], radians a position, each of magnitude
+                                   2 pi or less: GIVEN only */
+} markov_rotary_desc;
+
+typedef struct markov_rotary_plan markov_rotary_plan;
+
+/* Validate `desc` and compute the plan's frequencies (on the host, in 64
+ * bits).  EINVAL for a bad desc, EDEVICE for a bad device; *out is NULL then.
+ * Calls on one plan may overlap. */
+markov_status markov_rotary_plan_create(const markov_rotary_desc *desc, markov_rotary_plan **out);
+
+/* Synchronize the plan's device and free it.  NULL is a no-op. */
+void markov_rotary_plan_destroy(markov_rotary_plan *plan);
+
+/* Turn the queries and keys of num_tokens tokens by their positions:
+ *   (x_a, x_b) -> amplitude (x_a cos t - x_b sin t, x_b cos t + x_a sin t),
+ * t = position * f_i, for every pair of every head; dims from rot_dim on are
+ * copied.  Sines and cosines are fp32 of an angle that is kept to 2^-64 of a
+ * turn per position, so far positions lose nothing; products are fp32 and the
+ * result is rounded once.  One launch.
+ *   q, k          [num_tokens, q_heads, head_dim] and [num_tokens, k_heads,
+ *                 head_dim] of dtype (MARKOV_BF16, MARKOV_F16 or MARKOV_F32),
+ *                 strides s0 (token) and s1 (head) in elements, multiples of
+ *                 16 bytes, 16-byte aligned; k may be NULL with k_heads 0, and
+ *                 q with q_heads 0.
+ *   q_out, k_out  the same shapes; may be q and k (with the same strides), else
+ *                 they must not overlap them.
+ *   positions     int32 [num_tokens] (as markov_paged_layout gives them;
+ *                 negative ones turn the other way).
+ * EINVAL for a bad shape, stride, alignment or dtype, or 2^31 and more tokens
+ * times heads. */
+markov_status markov_rotary(markov_rotary_plan *plan, const void *q, int64_t q_s0, int64_t q_s1,
+                            int32_t q_heads, const void *k, int64_t k_s0, int64_t k_s1,
+                            int32_t k_heads, markov_dtype dtype, const int32_t *positions,
+                            int32_t num_tokens, void *q_out, int64_t qo_s0, int64_t qo_s1,
+                            void *k_out, int64_t ko_s0, int64_t ko_s1, void *stream);
+
+/* A paged cache of e4m3 (sign, 4 exponent and 3 mantissa bits; no infinities,
+ * largest 448) with an fp32 scale for each `block` tokens of a page and each
+ * head: the element (page, slot, head, d) stands for its value times the scale
+ * (page, slot / block, head).  Elements lie at page * s_page + slot * s_slot +
+ * head * s_head + d bytes, all three multiples of 16, base 16-byte aligned; scales
+ * at page * ss_page + (slot / block) * ss_block + head * ss_head floats, any
+ * strides of at least 0 (0 shares a scale, where it is only read).  block is a
+ * power of two, 16 .. page_size, so pages have 16 slots at least. */
+typedef struct markov_e4m3_view {
+    void *data;
+    int64_t num_pages;
+    int64_t s_page, s_slot, s_head;
+    float *scales;
+    int64_t ss_page, ss_block, ss_head;
+    int32_t block;
+} markov_e4m3_view;
+
+/* markov_paged_write into an e4m3 cache: each value is divided by its block's
+ * scale and rounded to nearest, ties to even; beyond +-448 (infinities too) it
+ * becomes +-448, NaN stays NaN.  With keep_scales = 0 the scales follow the
+ * values: with need = the least power of two that max |x| / 448 over the
+ * block's finite new values is not above (2^-40 at least), a block whose first
+ * slot is written takes need as its scale; another takes max(its scale, need),
+ * its entries so far being divided by the growth and rounded again (a growth
+ * that is a power of two loses nothing but what falls below the least
+ * subnormal); a scale that is not positive and finite counts as none.  The
+ * tokens that go to one block must then be neighbours in the call (as
+ * markov_paged_layout gives them): where others, skipped ones too, lie between
+ * them, the block's contents are unspecified.  With keep_scales = 1 the scales
+ * are read and left as they are (positive and finite; strides may be 0).
+ * Both caches have the same num_pages; the blocks may differ.  Tokens whose
+ * slot is negative or not below num_pages * page_size are skipped; slots are
+ * distinct.  One launch.  EINVAL as markov_paged_write. */
+markov_status markov_paged_write_e4m3(markov_paged_plan *plan, const void *key, int64_t key_s0,
+                                      int64_t key_s1, const void *value, int64_t value_s0,
+                                      int64_t value_s1, const markov_e4m3_view *k_cache,
+                                      const markov_e4m3_view *v_cache, const int64_t *slots,
+                                      int32_t num_tokens, int32_t keep_scales, void *stream);
+
+/* Read keys and values back in the plan's dtype: row b's last n =
+ * query_start[b + 1] - query_start[b] of its seq_lens[b] cached tokens go to
+ * tokens [query_start[b], query_start[b + 1]) of key and value [num_tokens,
+ * kv_heads, head_dim] (strides s0, s1 multiples of 8, 16-byte aligned), each
+ * value times its scale, rounded once; the arguments are
+ * markov_paged_attention's.  Tokens of negative positions, keys past the
+ * table's and keys of pages outside [0, num_pages) come as zeros.  Padding rows,
+ * and tokens outside every row, are not written.  One launch.  EINVAL for a
+ * bad shape, stride or alignment. */
+markov_status markov_paged_read_e4m3(markov_paged_plan *plan, const markov_e4m3_view *k_cache,
+                                     const markov_e4m3_view *v_cache, const int32_t *page_table,
+                                     int64_t table_s0, int32_t num_states, int32_t table_width,
+                                     const int64_t *row_state_idx, const int32_t *query_start,
+                                     const int32_t *seq_lens, int32_t rows, int32_t num_tokens,
+                                     void *key, int64_t key_s0, int64_t key_s1, void *value,
+                                     int64_t value_s0, int64_t value_s1, void *stream);
+
+/* markov_paged_attention over an e4m3 cache: the same tokens, masks, outputs
+ * and refusals, with keys and values that stand for their value times their
+ * scale.  The 8-bit values enter the tensor cores exactly, as fp16; queries
+ * exactly too (BF16 ones times a power of two for each row, which leaves what is
+ * below 2^-29 of a row's largest element without some bits); scores, scales,
+ * softmax sums and outputs are fp32, the weights are rounded to fp16.  Scales of
+ * values below 2^-60 count as 2^-60.  Two launches. */
+markov_status markov_paged_attention_e4m3(
+    markov_paged_plan *plan, const void *q, int64_t q_s0, int64_t q_s1,
+    const markov_e4m3_view *k_cache, const markov_e4m3_view *v_cache, const int32_t *page_table,
+    int64_t table_s0, int32_t num_states, int32_t table_width, const int64_t *row_state_idx,
+    const int32_t *query_start, const int32_t *seq_lens, int32_t rows, int32_t num_tokens,
+    float scale, int32_t window, int32_t sinks, void *out, int64_t out_s0, int64_t out_s1,
+    float *lse, void *stream);
+
+/* Log probabilities of given tokens, with rank, entropy and the most probable
+ * alternatives, from `rows` rows of logits.  For row i with T = temperature[i]
+ * (T <= 0, NaN and a NULL array count as 1: a greedy request reports its model's
+ * own probabilities) and p = softmax(logits[i] / T):
+ *   logprobs[i]   ln p(tokens[i])
+ *   ranks[i]      ids before tokens[i] in the order of the alternatives (0: it
+ *                 is the argmax)
+ *   entropy[i]    - sum p ln p
+ *   top_ids[i], top_logprobs[i]   the `top` first ids by falling logit, the
+ *                 lowest id first among equals (NaN above all, as the argmax of
+ *                 the sampling calls), and their ln p
+ * fp32, the sums too; ln p of a masked id (a logit of -inf) is -inf.  T = +inf:
+ * uniform over the ids whose logit is not -inf.  A row whose largest logit is NaN
+ * or infinite is one-hot at the argmax, as in markov_verify: ln p is 0 there and
+ * -inf elsewhere, the entropy 0.
+ *   logits        [rows, vocab] of dtype (MARKOV_BF16 or MARKOV_F32), row stride
+ *                 s0 >= vocab elements, aligned to its elements; vocab 1 .. 262144
+ *   tokens        int64 [rows]; a row whose token is outside [0, vocab) (-1 past
+ *                 a request's accepted ones) is neither read nor written.  NULL:
+ *                 every row is taken, without logprobs and ranks.
+ *   top           0 .. 32 and not above vocab; top_ids int32 and top_logprobs fp32
+ *                 [rows, top] contiguous
+ *   logprobs, ranks (int32), entropy, and the pair top_ids and top_logprobs may
+ *                 each be NULL.
+ * All device memory of one device, whichever is current.  No plan: calls may
+ * overlap.  One launch.  EINVAL for a bad shape, stride, alignment or dtype,
+ * EDEVICE where logits is not device memory. */
+markov_status markov_logprobs(const void *logits, markov_dtype dtype, int64_t logits_s0,
+                              int32_t rows, int32_t vocab, const int64_t *tokens,
+                              const float *temperature, int32_t top, float *logprobs,
+                              int32_t *ranks, float *entropy, int32_t *top_ids,
+                              float *top_logprobs, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
