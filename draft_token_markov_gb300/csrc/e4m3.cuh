@@ -46,6 +46,29 @@ __device__ __forceinline__ float scale_of(float max) {
     return fmaxf(__uint_as_float((uint32_t)::max(e, 1) << 23), kLeastScale);
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+
+// ------------------------------------------------- of the attention kernels
+
+// A weight is 2^(y - m + kShiftE4), m lagging behind the maximum by kLazyE4 at most:
+// up to 2^15 in fp16, so that small ones stay normal.
+constexpr float kLazyE4 = 8.0f, kShiftE4 = 7.0f;
+
+// log2 of a value's scale, which enters the exponent of its weight.
+__device__ __forceinline__ float scale_log2(float s) { return __log2f(fmaxf(s, 8.673617379884035e-19f /* 2^-60 */)); }
+
+// The exponent of the power of two that brings a row's largest element just below
+// 2^14: BF16 queries times that become fp16 ones without a loss.
+__device__ __forceinline__ int row_exponent(float max) {
+    const int e = max > 0.0f ? min((int)(__float_as_uint(max) >> 23), 254) : 127;
+    return min(127 + 13 - e, 100);
+}
+__device__ __forceinline__ float power_of_two(int k) { return __uint_as_float((uint32_t)(127 + k) << 23); }
+
 __device__ __forceinline__ bool usable_scale(float s) { return s > 0.0f && s < INFINITY; }
 
 }  // namespace dtm

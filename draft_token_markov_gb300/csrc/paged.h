@@ -126,6 +126,7 @@ struct AttnE4m3Args {
     PagedRows r;
     E4m3Scales ks, vs;
     int q_heads, kv_heads, group;
+    int tile_tokens, group_inv;            // as in AttnArgs
     float scale2;              // scale log2(e)
     int window, sinks;
     const uint16_t *q;
@@ -137,6 +138,7 @@ struct AttnE4m3Args {
     void *joins;               // the item that begins in a worker's range and goes on
     uint32_t *status;
     uint64_t timeout_ns;
+    uint64_t walk_ns;          // as in AttnArgs
 };
 
 struct VerifyArgs {
@@ -170,12 +172,18 @@ cudaError_t launch_paged_layout(const LayoutArgs &a, cudaStream_t s);
 cudaError_t launch_paged_write(const WriteArgs &a, cudaStream_t s);
 cudaError_t launch_store_e4m3(const StoreArgs &a, int head_dim, bool f16, bool keep, cudaStream_t s);
 cudaError_t launch_fetch_e4m3(const FetchArgs &a, int head_dim, bool f16, cudaStream_t s);
-cudaError_t attention_e4m3_prepare();
-size_t attention_e4m3_parts(int head_dim, int blocks);
-size_t attention_e4m3_joins(int blocks);
+cudaError_t attention_e4m3_few_prepare();
+size_t attention_e4m3_few_parts(int head_dim, int blocks);
+size_t attention_e4m3_few_joins(int blocks);
 // Calls of few query rows a request: k and v are maps of 16 slots by head_dim.
 cudaError_t launch_attention_e4m3_few(const AttnE4m3Args &a, const CUtensorMap &k, const CUtensorMap &v, int head_dim,
                                       bool f16, bool half, int blocks, cudaStream_t s);
+cudaError_t attention_e4m3_many_prepare();
+size_t attention_e4m3_many_parts(int head_dim, int blocks);
+size_t attention_e4m3_many_joins(int blocks);
+// Other calls: k and v are maps of up to 128 slots, q one of 64 elements by a row tile's tokens.
+cudaError_t launch_attention_e4m3_many(const AttnE4m3Args &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                                       int head_dim, bool f16, int blocks, cudaStream_t s);
 cudaError_t paged_attention_prepare();
 size_t paged_attention_parts(int head_dim, int blocks);
 size_t paged_attention_joins(int blocks);

@@ -184,9 +184,12 @@ markov_status markov_paged_plan_create(const markov_paged_desc *desc, markov_pag
     while ((1 << p->page_shift) < d.page_size) ++p->page_shift;
     p->blocks = p->sm_count;
     // the scratch serves the calls over either kind of cache
-    const size_t parts = std::max(paged_attention_parts(d.head_dim, p->blocks), attention_e4m3_parts(d.head_dim, p->blocks));
-    const size_t joins = std::max(paged_attention_joins(p->blocks), attention_e4m3_joins(p->blocks));
-    if (paged_attention_prepare() != cudaSuccess || attention_e4m3_prepare() != cudaSuccess ||
+    const size_t parts = std::max({paged_attention_parts(d.head_dim, p->blocks), attention_e4m3_few_parts(d.head_dim, p->blocks),
+                                   attention_e4m3_many_parts(d.head_dim, p->blocks)});
+    const size_t joins = std::max({paged_attention_joins(p->blocks), attention_e4m3_few_joins(p->blocks),
+                                   attention_e4m3_many_joins(p->blocks)});
+    if (paged_attention_prepare() != cudaSuccess || attention_e4m3_few_prepare() != cudaSuccess ||
+        attention_e4m3_many_prepare() != cudaSuccess ||
         cudaMalloc(&p->ctrl, kCtrlWords * sizeof(uint32_t)) != cudaSuccess ||
         cudaMalloc(&p->parts, parts * sizeof(float)) != cudaSuccess ||
         cudaMalloc(&p->joins, joins) != cudaSuccess ||
@@ -493,6 +496,8 @@ markov_status markov_paged_attention_e4m3(
     a.q_heads = p->d.q_heads;
     a.kv_heads = p->d.kv_heads;
     a.group = group;
+    a.tile_tokens = 128 / group;
+    a.group_inv = (65536 + group - 1) / group;
     a.scale2 = scale * 1.4426950408889634f;
     a.window = window;
     // a row has no more keys than kMaxRoom
@@ -508,11 +513,21 @@ markov_status markov_paged_attention_e4m3(
     a.joins = p->joins;
     a.status = p->ctrl;
     a.timeout_ns = (uint64_t)p->d.timeout_ms * 1000000ull;
-    CUtensorMap kmap, vmap;
-    if (!encode_e4m3_map(&kmap, *k_cache, *p, 16) || !encode_e4m3_map(&vmap, *v_cache, *p, 16)) return MARKOV_EINVAL;
-    const bool half = (int64_t)num_tokens * group <= 8 * (int64_t)rows;
-    if (launch_attention_e4m3_few(a, kmap, vmap, p->d.head_dim, p->d.dtype == MARKOV_F16, half, p->blocks,
-                                  (cudaStream_t)stream) != cudaSuccess) {
+    a.walk_ns = a.timeout_ns + (uint64_t)((int64_t)num_tokens * group / 256 + rows + 1) * 1000ull;
+    const bool f16 = p->d.dtype == MARKOV_F16;
+    const cudaStream_t s = (cudaStream_t)stream;
+    // up to 16 rows of query heads a request on average: bound by the cache's bytes
+    const int64_t query_rows = (int64_t)num_tokens * group;
+    const bool few = query_rows <= 16 * (int64_t)rows;
+    CUtensorMap qmap, kmap, vmap;
+    const int slots = few ? 16 : 128;
+    if (!encode_e4m3_map(&kmap, *k_cache, *p, slots) || !encode_e4m3_map(&vmap, *v_cache, *p, slots) ||
+        (!few && !encode_query_map(&qmap, q, q_s0, q_s1, num_tokens, *p)))
+        return MARKOV_EINVAL;
+    const cudaError_t e =
+        few ? launch_attention_e4m3_few(a, kmap, vmap, p->d.head_dim, f16, query_rows <= 8 * (int64_t)rows, p->blocks, s)
+            : launch_attention_e4m3_many(a, qmap, kmap, vmap, p->d.head_dim, f16, p->blocks, s);
+    if (e != cudaSuccess) {
         cudaGetLastError();
         return MARKOV_ECUDA;
     }

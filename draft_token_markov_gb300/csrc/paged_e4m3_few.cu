@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "attention_tc.cuh"
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "f32x2.cuh"
@@ -42,7 +43,6 @@ constexpr int kStep = 16;                    // keys of a step
 constexpr int kStepShift = 4;
 constexpr int kEnds = 6;                     // an item's start and end, in steps
 constexpr int kLeast = 10;                   // units of a range
-constexpr float kLazyE4 = 8.0f, kShiftE4 = 7.0f;
 
 template <int D>
 struct FewShape {
@@ -80,21 +80,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t f16x2_rn(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
-    return F16 ? f16x2_rn(lo, hi) : bf16x2_rn(lo, hi);
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t at) {
     uint2 v;
     asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
@@ -107,18 +92,6 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int 
         "[%6];" ::"r"(dst),
         "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
         : "memory");
-}
-
-// log2 of a value's scale, which enters the exponent of its weight.
-__device__ __forceinline__ float scale_log2(float s) { return __log2f(fmaxf(s, 8.673617379884035e-19f /* 2^-60 */)); }
-
-// The power of two that brings a row's largest element just below 2^14, and its
-// inverse: BF16 queries become fp16 ones without a loss.
-__device__ __forceinline__ float row_power(float max, float &inverse) {
-    const int e = max > 0.0f ? min((int)(__float_as_uint(max) >> 23), 254) : 127;
-    const int k = min(127 + 13 - e, 100);     // 2^k
-    inverse = __uint_as_float((uint32_t)(127 - k) << 23);
-    return __uint_as_float((uint32_t)(127 + k) << 23);
 }
 
 // The scores of dim steps: Q's fragments of rows g and g + 8, and each row's
@@ -153,12 +126,12 @@ struct FewQueries {
                 top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            float inverse;
-            const float power = row_power(top, inverse);
+            const int k = row_exponent(top);
+            const float power = power_of_two(k);
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
-                to[i / 2][i % 2] = f16x2_rn(__uint_as_float(w[i] << 16) * power, __uint_as_float(w[i] & 0xffff0000u) * power);
-            c = a.scale2 * inverse;
+                to[i / 2][i % 2] = pack2<true>(__uint_as_float(w[i] << 16) * power, __uint_as_float(w[i] & 0xffff0000u) * power);
+            c = a.scale2 * power_of_two(-k);
         }
     }
     __device__ __forceinline__ void load(const AttnE4m3Args &a, const FewItem &it) {
@@ -465,8 +438,8 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
                     const float b = M[x] == -INFINITY ? 0.0f : kShiftE4 - M[x];
                     const float p0 = ex2(y[x][0] + b), p1 = ex2(y[x][1] + b), p2 = ex2(y[x][2] + b), p3 = ex2(y[x][3] + b);
                     l[x] = fmaf((p0 + p1) + (p2 + p3), iv, l[x]);
-                    p[x] = f16x2_rn(p0, p1);
-                    p[2 + x] = f16x2_rn(p2, p3);
+                    p[x] = pack2<true>(p0, p1);
+                    p[2 + x] = pack2<true>(p2, p3);
                 }
                 // ------------------------------------------------ O += P V
 #pragma unroll
@@ -516,7 +489,7 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int col = 8 * i + 2 * k, t = col % kTiles, e = 2 * x + col / kTiles;
-                        w[k] = sum == 0.0f ? 0u : pack_out<F16>(o[t][e] * inv, o[t + 1][e] * inv);
+                        w[k] = sum == 0.0f ? 0u : pack2<F16>(o[t][e] * inv, o[t + 1][e] * inv);
                     }
                     to[i] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -593,7 +566,7 @@ __global__ void __launch_bounds__(kFewJoinThreads) few_join_kernel(const __grid_
         const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
         const int sr = j.row0 + r, tok = sr / a.group, head = j.head0 + sr - tok * a.group;
         const int64_t token = j.qs + tok;
-        uint2 v = make_uint2(pack_out<F16>(o.x * inv, o.y * inv), pack_out<F16>(o.z * inv, o.w * inv));
+        uint2 v = make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
         if (L == 0.0f) v = make_uint2(0u, 0u);
         *reinterpret_cast<uint2 *>(a.out + token * a.out_s0 + head * a.out_s1 + 4 * k) = v;
         if (k == 0 && a.lse)
@@ -641,13 +614,13 @@ static cudaError_t prepare_few() {
     return cudaSuccess;
 }
 
-cudaError_t attention_e4m3_prepare() {
+cudaError_t attention_e4m3_few_prepare() {
     const cudaError_t e = prepare_few<64>();
     return e == cudaSuccess ? prepare_few<128>() : e;
 }
 
 // Floats of the parts that `blocks` blocks may leave, bytes of their joins.
-size_t attention_e4m3_parts(int head_dim, int blocks) { return (size_t)blocks * kFewWarps * 2 * 16 * (head_dim + 2); }
-size_t attention_e4m3_joins(int blocks) { return (size_t)blocks * kFewWarps * sizeof(FewJoin); }
+size_t attention_e4m3_few_parts(int head_dim, int blocks) { return (size_t)blocks * kFewWarps * 2 * 16 * (head_dim + 2); }
+size_t attention_e4m3_few_joins(int blocks) { return (size_t)blocks * kFewWarps * sizeof(FewJoin); }
 
 }  // namespace dtm
