@@ -2,25 +2,25 @@
 // probable alternatives: one launch, a cluster of thread blocks a row of logits,
 // and its C ABI.
 //
-// Each block of the cluster takes a slice of the row to shared memory (at most
-// 32 KB where 8 blocks do, so that several slices are in flight on a
-// multiprocessor) and reads it there three times: for the largest logit, for the
-// sums
-//   Z = sum 2^d,  S = sum 2^d d,  d = (l - m) log2(e) / T
-// against the slice's own maximum m, and for the few logits that may be among
-// the `top` largest.  For these, the slice is cut into 64 groups (four
-// neighbouring lanes each): the top-th largest group maximum is a bound that at
-// least `top` logits reach and that fewer than `top` groups exceed; what exceeds
-// it is collected, what equals it too (lowest ids first), and put in order by
-// counting.  The first block joins the cluster's sums and sorted lists, which the
-// others write to its shared memory.
+// Each block of the cluster has a slice of the row in its threads' registers, read
+// once from memory: the maximum m, the sums
+//   Z = sum 2^d,  S = sum 2^d d,  d = x c - M,  c = log2(e) / T,  M = m c rounded
+// against the slice's own maximum (one fused operation a logit; what the rounding of
+// M is worth is put right once, in the sums), the ids before the token, and the few
+// logits that may be among the `top` largest.  For these, the slice is cut into 64
+// groups (four neighbouring lanes each): the top-th largest group maximum is a bound
+// that at least `top` logits reach and that fewer than `top` groups exceed.  What
+// reaches it goes to a list, which is put in order by counting.  Where the list is
+// too short for that (a slice with many equal logits, a few lanes with all the large
+// ones), the block takes its maximum `top` times instead.  The first block joins the
+// cluster's sums and sorted lists, which the others write to its shared memory.
 //
-// ln p = (l - m) / T - ln Z, entropy = (log2 Z - S / Z) ln 2.  Every logit is read
-// once from memory.
-#include <atomic>
+// ln p = (d - log2 Z) ln 2, entropy = (log2 Z - S / Z) ln 2.
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+
+#include <cuda_bf16.h>
 
 #include "../../include/markov.h"
 #include "common.cuh"
@@ -36,9 +36,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kGroups = kThreads / 4;
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
-constexpr int kSliceBytes = 32768;        // of a block, unless eight of them are not enough
-constexpr int kTies = 256;
-constexpr int kMostShared = 200 << 10;    // 262144 fp32 logits need 164 KB
+constexpr int kList = 512;                // logits that may be among the largest
 
 struct LogprobArgs {
     const uint8_t *logits;
@@ -48,8 +46,7 @@ struct LogprobArgs {
     const float *temperature;
     float *logprobs, *entropy, *top_logprobs;
     int32_t *ranks, *top_ids;
-    int slice;                            // bytes of a block, a multiple of 16
-    int list;                             // entries of the list of candidates
+    int slice;                            // vectors of 16 bytes of a block
 };
 
 // What a block knows of its slice, in the first block's shared memory.
@@ -89,13 +86,6 @@ struct Logits {
     }
 };
 
-template <bool F32>
-__device__ __forceinline__ float vector_max(const uint4 &v) {
-    const uint32_t w = word_max<F32>(word_max<F32>(v.x, v.y), word_max<F32>(v.z, v.w));
-    if (F32) return __uint_as_float(w);
-    return __uint_as_float(word_max<true>(w << 16, w & 0xffff0000u));
-}
-
 __device__ __forceinline__ float nan_max(float a, float b) {
     return __uint_as_float(word_max<true>(__float_as_uint(a), __float_as_uint(b)));
 }
@@ -128,19 +118,50 @@ __device__ __forceinline__ void st_cluster(uint32_t to, uint64_t x) {
 
 constexpr float kLn2 = 0.69314718055994531f;
 
+// Counts logits above a bound, two at a time where they are BF16 (a count of up to
+// 256 in each half is exact).
 template <bool F32>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+struct Above;
+template <>
+struct Above<false> {
+    __nv_bfloat162 n = __float2bfloat162_rn(0.0f);
+    __device__ __forceinline__ void take(const uint4 &v, uint32_t bound) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w}, b2 = bound >> 16 | (bound & 0xffff0000u);
+        const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(&b2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), b));
+    }
+    __device__ __forceinline__ int count() const { return (int)(__low2float(n) + __high2float(n)); }
+};
+template <>
+struct Above<true> {
+    int n = 0;
+    __device__ __forceinline__ void take(const uint4 &v, uint32_t bound) {
+        const float b = __uint_as_float(bound);
+        n += (__uint_as_float(v.x) > b) + (__uint_as_float(v.y) > b) + (__uint_as_float(v.z) > b) + (__uint_as_float(v.w) > b);
+    }
+    __device__ __forceinline__ int count() const { return n; }
+};
+
+// The bits of the next lower logit of a finite one (fp32 bits; a BF16 one's are the
+// upper half).
+template <bool F32>
+__device__ __forceinline__ uint32_t next_below(float x) {
+    const uint32_t one = F32 ? 1u : 0x10000u, b = __float_as_uint(x);
+    if ((b & 0x7fffffffu) == 0u) return 0x80000000u | one;
+    return b >> 31 ? b + one : b - one;
+}
+
+template <bool F32, int N>
+__global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     constexpr int kSize = F32 ? 4 : 2, kN = 16 / kSize;
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint4 *slice = reinterpret_cast<uint4 *>(smem);
-    uint16_t *list = reinterpret_cast<uint16_t *>(smem + a.slice);     // elements of the slice
     __shared__ Part parts[kMaxCluster];
     __shared__ float warp_f[3][kWarps];
     __shared__ int warp_i[kWarps];
-    __shared__ uint64_t warp_k[kWarps];
+    __shared__ uint64_t warp_k[kWarps], round_k[kWarps];
     __shared__ float group_max[kGroups];
-    __shared__ uint16_t ties[kTies];
-    __shared__ int listed_s, ties_s;
+    __shared__ uint64_t list[kList];
+    __shared__ int listed_s;
     __shared__ float bound_s;
     __shared__ uint64_t sorted[kMaxTop];
 
@@ -151,57 +172,63 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
     if (a.tokens && (token < 0 || token >= a.vocab)) return;           // the whole cluster
     if (blocks > 1) cluster_arrive();                                  // every block runs
 
-    // the slice: whole vectors from the row's first on, whose first `lead` elements
-    // lie before the row
+    // the slice: whole vectors from the row's first on, whose first elements may lie
+    // before the row; -inf where the row does not reach
     const uint8_t *from = a.logits + row * a.s0;
-    const int lead_bytes = (int)(reinterpret_cast<uintptr_t>(from) & 15u);
-    const int64_t bytes = (int64_t)a.vocab * kSize + lead_bytes;       // from the first vector's start
-    const int64_t begin = (int64_t)rank * a.slice;
-    const int vectors = (int)(min(max(bytes - begin, (int64_t)0), (int64_t)a.slice) + 15) / 16;
-    const uint8_t *first = from - lead_bytes + begin;
-    const int id0 = (int)((begin - lead_bytes) / kSize);               // of the slice's first element
-    for (int v = tid; v < vectors; v += kThreads) {
-        const int id = id0 + v * kN;
-        if (id >= 0 && id + kN <= a.vocab) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(slice + v)),
-                         "l"(first + 16 * (int64_t)v)
-                         : "memory");
-        } else {
-            // -inf where the row does not reach
-            uint32_t w[4];
+    const int lead = (int)(reinterpret_cast<uintptr_t>(from) & 15u) / kSize;
+    const int id0 = (int)(rank * (uint32_t)a.slice + tid) * kN - lead;  // of the thread's first vector
+    const int vectors = min(a.slice, (a.vocab + lead + kN - 1) / kN - (int)rank * a.slice);
+    constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;
+    uint4 x[N];
 #pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                const bool there = id + e >= 0 && id + e < a.vocab;
-                if (F32) {
-                    w[e % 4] = there ? __ldg(reinterpret_cast<const uint32_t *>(from) + id + e) : 0xff800000u;
-                } else {
-                    const uint32_t x = there ? __ldg(reinterpret_cast<const uint16_t *>(from) + id + e) : 0xff80u;
-                    w[e / 2 % 4] = e & 1 ? w[e / 2 % 4] | x << 16 : x;
-                }
-            }
-            slice[v] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+    for (int i = 0; i < N; ++i) {
+        const int id = id0 + i * kThreads * kN;
+        x[i] = make_uint4(kNone, kNone, kNone, kNone);
+        if (tid + i * kThreads < vectors && id >= 0 && id + kN <= a.vocab)
+            x[i] = __ldcs(reinterpret_cast<const uint4 *>(from + (int64_t)id * kSize));
     }
     float T = a.temperature ? __ldg(a.temperature + row) : 1.0f;
     if (!samples(T)) T = 1.0f;
-    // finite, and not 0: with T = inf the difference of finite logits vanishes, -inf stays
-    const float c = fmaxf(fminf(__fdiv_rn(1.4426950408889634f, T), 3.0e38f), 1.401298464e-45f);
     float own = 0.0f;
     if (a.tokens)
         own = F32 ? __ldg(reinterpret_cast<const float *>(from) + token)
                   : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + token) << 16);
-    if (tid == 0) listed_s = ties_s = 0;
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int id = id0 + i * kThreads * kN;
+        if (tid + i * kThreads >= vectors || (id >= 0 && id + kN <= a.vocab)) continue;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            const bool there = id + e >= 0 && id + e < a.vocab;
+            if (F32) {
+                w[e % 4] = there ? __ldg(reinterpret_cast<const uint32_t *>(from) + id + e) : 0xff800000u;
+            } else {
+                const uint32_t y = there ? __ldg(reinterpret_cast<const uint16_t *>(from) + id + e) : 0xff80u;
+                w[e / 2 % 4] = e & 1 ? w[e / 2 % 4] | y << 16 : y;
+            }
+        }
+        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // finite, and not 0: with T = inf the difference of finite logits vanishes, -inf stays
+    const float c = fmaxf(fminf(__fdiv_rn(1.4426950408889634f, T), 3.0e38f), 1.401298464e-45f);
+    if (tid == 0) listed_s = 0;
+    // f(logit, id) of the slice's logits, read again: for what is rare
+    const auto each = [&](const auto &f) {
+        const int id1 = min(((int)rank * a.slice + vectors) * kN - lead, a.vocab);
+#pragma unroll 1
+        for (int id = max((int)rank * a.slice * kN - lead, 0) + tid; id < id1; id += kThreads)
+            f(F32 ? __ldg(reinterpret_cast<const float *>(from) + id)
+                  : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + id) << 16),
+              id);
+    };
 
     // ------------------------------------------------------------- maximum
-    const auto element = [&](int e) {
-        return F32 ? reinterpret_cast<const float *>(smem)[e]
-                   : __uint_as_float((uint32_t)reinterpret_cast<const uint16_t *>(smem)[e] << 16);
-    };
-    const auto inside = [&](int e) { return id0 + e >= 0 && id0 + e < a.vocab; };
-    float top = -INFINITY;
-    for (int v = tid; v < vectors; v += kThreads) top = nan_max(top, vector_max<F32>(slice[v]));
+    uint32_t word = kNone;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        word = word_max<F32>(word, word_max<F32>(word_max<F32>(x[i].x, x[i].y), word_max<F32>(x[i].z, x[i].w)));
+    const float top = F32 ? __uint_as_float(word) : __uint_as_float(word_max<true>(word << 16, word & 0xffff0000u));
     float group = nan_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     group = nan_max(group, __shfl_xor_sync(0xffffffffu, group, 2));
     if ((lane & 3) == 0) group_max[tid >> 2] = group;
@@ -219,33 +246,26 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
     float z = 0.0f, s = 0.0f;
     int before = 0;
     uint64_t best = 0;
+    const float M = m * c;
+    const bool fused = fabsf(M) < 1e30f && c > 1e-20f && c < 1e7f;     // else differences come first
     const bool by_key = a.tokens && (odd || !(own > -INFINITY));       // NaN or -inf in the comparison
-    if (!odd) {
-        const uint64_t neg = f32x2(-m, -m), c2 = f32x2(c, c);
+    if (!odd && fused) {
+        const uint64_t neg = f32x2(-M, -M), c2 = f32x2(c, c);
         uint64_t z2[2] = {0, 0}, s2[2] = {0, 0};
-        for (int v = tid; v < vectors; v += kThreads) {
-            const Logits<F32> l(slice[v]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            // a masked logit's 0 times -inf would be NaN: -1e30 times c weighs 0 too
+            constexpr uint32_t kLow = F32 ? 0xf149f2cau : 0xf149f149u;
+            const Logits<F32> l(make_uint4(word_max<F32>(x[i].x, kLow), word_max<F32>(x[i].y, kLow), word_max<F32>(x[i].z, kLow),
+                                           word_max<F32>(x[i].w, kLow)));
 #pragma unroll
             for (int e = 0; e < kN; e += 2) {
+                const uint64_t d = fma2(f32x2(l.x[e], l.x[e + 1]), c2, neg);
                 float d0, d1;
-                split2(mul2(add2(f32x2(l.x[e], l.x[e + 1]), neg), c2), d0, d1);
+                split2(d, d0, d1);
                 const uint64_t p = f32x2(ex2(d0), ex2(d1));
                 z2[e / 2 & 1] = add2(z2[e / 2 & 1], p);
-                // a masked logit's 0 times -inf is 0
-                s2[e / 2 & 1] = fma2(p, f32x2(fmaxf(d0, -1024.0f), fmaxf(d1, -1024.0f)), s2[e / 2 & 1]);
-            }
-            if (a.tokens && !by_key) {
-                const int64_t id = id0 + (int64_t)v * kN;
-                if (id + kN <= token) {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) before += l.x[e] >= own;
-                } else if (id > token) {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) before += l.x[e] > own;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) before += id + e < token ? l.x[e] >= own : l.x[e] > own;
-                }
+                s2[e / 2 & 1] = fma2(p, d, s2[e / 2 & 1]);
             }
         }
         float x0, x1, y0, y1;
@@ -253,15 +273,41 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
         split2(add2(s2[0], s2[1]), y0, y1);
         z = x0 + x1;
         s = y0 + y1;
+        // relative to m c instead of M
+        const float off = fmaf(m, c, -M), f = ex2(-off);
+        s = f * fmaf(-off, z, s);
+        z *= f;
+    } else if (!odd) {
+        each([&](float l, int) {
+            const float d = (l - m) * c, p = ex2(d);
+            z += p;
+            s += d > -1024.0f ? p * d : 0.0f;
+        });
+    }
+    if (a.tokens && !by_key) {
+        const uint32_t equal = __float_as_uint(own), below = next_below<F32>(own);
+        Above<F32> above;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int id = id0 + i * kThreads * kN;
+            // equal logits count where their ids are lower
+            if (id <= token && token < id + kN) {
+                const Logits<F32> l(x[i]);
+#pragma unroll
+                for (int e = 0; e < kN; ++e) before += id + e < token ? l.x[e] >= own : l.x[e] > own;
+            } else {
+                above.take(x[i], id > token ? equal : below);
+            }
+        }
+        before += above.count();
     }
     if (odd || by_key) {
         const uint64_t own_key = a.tokens ? pack_key(own, (uint32_t)token) : 0;
-        for (int e = tid; e < vectors * kN; e += kThreads) {
-            if (!inside(e)) continue;
-            const uint64_t k = pack_key(element(e), (uint32_t)(id0 + e));
+        each([&](float l, int id) {
+            const uint64_t k = pack_key(l, (uint32_t)id);
             if (by_key) before += k > own_key;
             if (odd) best = k > best ? k : best;
-        }
+        });
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -269,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
         s += __shfl_xor_sync(0xffffffffu, s, o);
     }
     before = __reduce_add_sync(0xffffffffu, before);
-    best = warp_max_key(best);
+    if (odd) best = warp_max_key(best);
     if (lane == 0) {
         warp_f[1][warp] = z;
         warp_f[2][warp] = s;
@@ -290,60 +336,83 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
                     if (g0 == g) g0 = 0; else g1 = 0;
                 }
             }
-            if (lane == 0) bound_s = key_from_ordered(g);              // NaN for NaN: 0x7fffffff
+            if (lane == 0) bound_s = key_from_ordered(g);
+        } else if (warp == 1) {
+            sorted[lane] = 0;
         }
         __syncthreads();
         const float bound = bound_s;
-        const uint32_t bound_key = ordered_key(bound);
-        if (ordered_key(group) >= bound_key) {
-            for (int v = tid; v < vectors; v += kThreads) {
-                const uint4 w = slice[v];
-                if (ordered_key(vector_max<F32>(w)) < bound_key) continue;
-                const Logits<F32> l(w);
+        const bool nothing = bound == -INFINITY;                       // groups without a logit: -inf is not listed
+        if (top >= bound && top > -INFINITY) {
 #pragma unroll
-                for (int e = 0; e < kN; ++e) {
-                    const uint32_t k = ordered_key(l.x[e]);
-                    const int at = v * kN + e;
-                    if (k > bound_key) {
-                        list[atomicAdd(&listed_s, 1)] = (uint16_t)at;
-                    } else if (k == bound_key && inside(at)) {
-                        const int n = atomicAdd(&ties_s, 1);
-                        if (n < kTies) ties[n] = (uint16_t)at;
+            for (int i = 0; i < N; ++i) {
+                const uint32_t w = word_max<F32>(word_max<F32>(x[i].x, x[i].y), word_max<F32>(x[i].z, x[i].w));
+                const float most = F32 ? __uint_as_float(w) : __uint_as_float(word_max<true>(w << 16, w & 0xffff0000u));
+                if (!(most >= bound) || most == -INFINITY) continue;
+                const Logits<F32> l(x[i]);
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    if (l.x[e] >= bound && l.x[e] > -INFINITY) {
+                        const int at = atomicAdd(&listed_s, 1);
+                        if (at < kList) list[at] = pack_key(l.x[e], (uint32_t)(id0 + i * kThreads * kN + e));
                     }
-                }
             }
         }
         __syncthreads();
-        const int listed = listed_s;
-        int tied = ties_s;
-        if (tied > kTies) {
-            // many: the lowest ids of them, in order
+        int listed = listed_s;
+        // masked ids follow by their number: those of the first 32 vectors are enough, or the slow way
+        bool slow = listed > kList || m != m || m == INFINITY;
+        if (nothing && listed < a.top && !slow) {
+            uint32_t masked = 0;
             if (warp == 0) {
-                int n = 0;
-                for (int e0 = 0; n < a.top && e0 < vectors * kN; e0 += 32) {
-                    const int e = e0 + lane;
-                    const bool is = e < vectors * kN && inside(e) && ordered_key(element(e)) == bound_key;
-                    const uint32_t who = __ballot_sync(0xffffffffu, is);
-                    const int at = n + __popc(who & ((1u << lane) - 1u));
-                    if (is && at < a.top) ties[at] = (uint16_t)e;
-                    n += __popc(who);
+                const Logits<F32> l(x[0]);
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    if (lane < vectors && l.x[e] == -INFINITY && id0 + e >= 0 && id0 + e < a.vocab) masked |= 1u << e;
+                int at = __popc(masked);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, at, o);
+                    if (lane >= o) at += y;
                 }
+                const int all = __shfl_sync(0xffffffffu, at, 31);
+                at -= __popc(masked);
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    if (masked >> e & 1) {
+                        if (at < a.top) list[listed + at] = pack_key(-INFINITY, (uint32_t)(id0 + e));
+                        ++at;
+                    }
+                if (lane == 0) listed_s = all >= a.top || vectors <= 32 ? listed + min(all, a.top) : kList + 1;
             }
-            tied = a.top;
             __syncthreads();
+            listed = listed_s;
+            slow = listed > kList;
         }
-        if (tid < kMaxTop) sorted[tid] = 0;
-        __syncthreads();
-        // in order, by counting
-        const auto key = [&](int i) {
-            const int e = i < listed ? list[i] : ties[i - listed];
-            return pack_key(element(e), (uint32_t)(id0 + e));
-        };
-        for (int i = tid; i < listed + tied; i += kThreads) {
-            const uint64_t k = key(i);
-            int n = 0;
-            for (int j = 0; j < listed + tied && n < a.top; ++j) n += key(j) > k;
-            if (n < a.top) sorted[n] = k;
+        if (!slow) {
+            for (int i = tid; i < listed; i += kThreads) {
+                const uint64_t k = list[i];
+                int n = 0;
+                for (int j = 0; j < listed; ++j) n += list[j] > k;
+                if (n < a.top) sorted[n] = k;
+            }
+        } else {
+            uint64_t last = 1;
+            for (int n = 0; n < a.top && last != 0; ++n) {
+                uint64_t most = 0;
+                each([&](float l, int id) {
+                    const uint64_t k = pack_key(l, (uint32_t)id);
+                    if (n == 0 || k < last) most = k > most ? k : most;
+                });
+                most = warp_max_key(most);
+                if (lane == 0) round_k[warp] = most;
+                __syncthreads();
+                last = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) last = round_k[w] > last ? round_k[w] : last;
+                if (tid == 0) sorted[n] = last;
+                __syncthreads();
+            }
         }
     }
     __syncthreads();
@@ -399,8 +468,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
     const float log_z = one_hot ? 0.0f : log2f(z);
     const auto log_p = [&](float l, int id) {
         if (one_hot) return id == (int)packed_id(best) ? 0.0f : -INFINITY;
-        // in nats: a logit of the type's lowest value would leave the range of d
-        return l == -INFINITY ? l : __fdiv_rn(l - all, T) - log_z * kLn2;
+        if (l == -INFINITY) return l;
+        const float d = (l - all) * c;
+        // a logit of the type's lowest value leaves the range of d
+        return d > -INFINITY ? (d - log_z) * kLn2 : __fdiv_rn(l - all, T);
     };
     if (tid == 0) {
         if (a.logprobs && a.tokens) a.logprobs[row] = log_p(own, (int)token);
@@ -432,25 +503,15 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const __grid_constan
     }
 }
 
-// The blocks of a row's cluster and the bytes of a slice.
-void cut_row(int64_t bytes, int &blocks, int &slice) {
-    blocks = 1;
-    while (blocks < kMaxCluster && (bytes + blocks - 1) / blocks > kSliceBytes) blocks *= 2;
-    slice = (int)((bytes + blocks - 1) / blocks + 15) / 16 * 16;
-}
+// The vectors of a thread: up to 8 while the cluster can grow.
+constexpr int kFewVectors = 8;
 
-// Lets the kernels take what a call may need, once a device.
-bool allow_shared_memory(int device) {
-    static std::atomic<uint64_t> done{0};
-    const uint64_t bit = device < 64 ? 1ull << device : 0ull;
-    if (done.load(std::memory_order_relaxed) & bit) return true;
-    for (const void *fn : {(const void *)logprobs_kernel<false>, (const void *)logprobs_kernel<true>})
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared) != cudaSuccess) {
-            cudaGetLastError();
-            return false;
-        }
-    done.fetch_or(bit, std::memory_order_relaxed);
-    return true;
+template <bool F32>
+const void *kernel_for(int vectors) {
+    if (vectors <= 2) return (const void *)logprobs_kernel<F32, 2>;
+    if (vectors <= 8) return (const void *)logprobs_kernel<F32, 8>;
+    if (vectors <= 17) return (const void *)logprobs_kernel<F32, 17>;
+    return (const void *)logprobs_kernel<F32, 33>;                     // fp32 alone has as many
 }
 
 }  // namespace
@@ -491,13 +552,13 @@ extern "C" markov_status markov_logprobs(const void *logits, markov_dtype dtype,
     a.top_logprobs = top_logprobs;
     a.ranks = ranks;
     a.top_ids = top_ids;
-    int blocks;
-    cut_row((int64_t)vocab * size + 16, blocks, a.slice);
-    // fewer than `top` groups have logits above the bound
-    const int in_group = 4 * ((a.slice / 16 + kThreads - 1) / kThreads) * (16 / size);
-    a.list = (top > 0 ? top - 1 : 0) * in_group;
-    const int smem = a.slice + (a.list * 2 + 15) / 16 * 16;
-    if (!allow_shared_memory(at.device)) return MARKOV_ECUDA;
+    // whole vectors, the first of which may begin before the row
+    const int vectors = (int)(((int64_t)vocab * size + 15) / 16) + 1;
+    int blocks = 1;
+    while (blocks < kMaxCluster && vectors > blocks * kFewVectors * kThreads) blocks *= 2;
+    a.slice = (vectors + blocks - 1) / blocks;
+    const int each = (a.slice + kThreads - 1) / kThreads;
+    const void *fn = f32 ? kernel_for<true>(each) : kernel_for<false>(each);
     for (int32_t r0 = 0; r0 < rows; r0 += 65535) {
         LogprobArgs b = a;
         b.logits += r0 * a.s0;
@@ -514,13 +575,11 @@ extern "C" markov_status markov_logprobs(const void *logits, markov_dtype dtype,
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(blocks, rows - r0 < 65535 ? rows - r0 : 65535);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
         cfg.stream = (cudaStream_t)stream;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        const cudaError_t e = f32 ? cudaLaunchKernelEx(&cfg, logprobs_kernel<true>, b)
-                                  : cudaLaunchKernelEx(&cfg, logprobs_kernel<false>, b);
-        if (e != cudaSuccess) {
+        void *params[1] = {&b};
+        if (cudaLaunchKernelExC(&cfg, fn, params) != cudaSuccess) {
             cudaGetLastError();
             return MARKOV_ECUDA;
         }

@@ -31,13 +31,16 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
 // of them is rounded, and a block that was begun by earlier calls may have to be
 // rescaled: a thread block (chunk of tokens, head, side) takes the cache blocks
 // whose first token of the call lies in its chunk, one after the other, with all
-// of their tokens, also those past the chunk.  Up to kHeld * 128 vectors of them
-// stay in registers between the maximum and the rounding, the rest is read
-// again.  Rescaling comes before the new values, so that it need not know which
-// entries they replace.  Bound by memory: the elements are read once and written
-// as bytes.
+// of their tokens, also those past the chunk.  Where the runs of a cache block's
+// tokens begin and end is found once, from the slots: a bit a token.
+// Up to kHeld * 128 vectors of a run stay in registers between the maximum and the
+// rounding, the rest is read again.  Rescaling comes before the new values, so that
+// it need not know which entries they replace.  Bound by latency (slots, values,
+// maximum one after the other) where a call is small, then by memory: the elements
+// are read once and written as bytes.
 constexpr int kStoreThreads = 128;
 constexpr int kHeld = 8;
+constexpr int kMostChunk = 256;              // tokens of a chunk: a cache block at most
 
 // x / s, rounded: by its reciprocal where that is exact (s a power of two).
 __device__ __forceinline__ uint2 round8(const float (&x)[8], float s, float inv) {
@@ -54,7 +57,7 @@ __device__ __forceinline__ float exact_inverse(float s) {
 }
 
 template <int D, bool F16, bool KEEP>
-__global__ void __launch_bounds__(kStoreThreads) store_e4m3_kernel(const __grid_constant__ StoreArgs a) {
+__global__ void __launch_bounds__(kStoreThreads, 5) store_e4m3_kernel(const __grid_constant__ StoreArgs a) {
     if (__ldcg(a.status) != 0u) return;
     constexpr int kLanes = D / 8, kTokens = kStoreThreads / kLanes;     // threads of a token, tokens of a turn
     __shared__ uint32_t top_s[kStoreThreads / 32];
@@ -87,43 +90,53 @@ __global__ void __launch_bounds__(kStoreThreads) store_e4m3_kernel(const __grid_
         }
         return;
     }
-    int64_t before = slot_at(t_first - 1);
-    for (int t0 = t_first; t0 < t_last;) {
-        // the tokens [t0, t1) of one cache block, which no earlier one began
-        const int64_t slot0 = slot_at(t0), block = slot0 >> c.block_shift;
-        int t1 = t0 + 1;
-        bool anew = false;
-        if (slot0 >= 0) {
-            for (int base = t0;; base += kStoreThreads) {
-                const int64_t s = slot_at(base + tid);
-                const bool same = s >= 0 && s >> c.block_shift == block;
-                // the first that is not of the block ends the run
-                const int n = __syncthreads_count(same);
-                if (n == kStoreThreads) {
-                    if (__syncthreads_or((s & ((1 << c.block_shift) - 1)) == 0)) anew = true;
-                    continue;
-                }
-                __shared__ int end_s;
-                if (tid == 0) end_s = kStoreThreads;
-                __syncthreads();
-                if (!same) atomicMin(&end_s, tid);
-                __syncthreads();
-                const int end = end_s;
-                t1 = base + end;
-                if (__syncthreads_or(tid < end && (s & ((1 << c.block_shift) - 1)) == 0)) anew = true;
+    // bit i: token t_first + i is of another cache block than the one before it, and
+    // (first_s) is one of the cache's
+    __shared__ uint32_t breaks_s[kMostChunk / 16], first_s[kMostChunk / 32];
+    // a run is a cache block's tokens at most, as a rule
+    const int window = (a.chunk + (1 << c.block_shift) + 31) & ~31;
+    for (int i = tid; i < window; i += kStoreThreads) {
+        const int64_t s = slot_at(t_first + i), before = slot_at(t_first + i - 1);
+        const bool breaks = s < 0 || before < 0 || s >> c.block_shift != before >> c.block_shift;
+        const uint32_t b = __ballot_sync(0xffffffffu, breaks), f = __ballot_sync(0xffffffffu, breaks && s >= 0);
+        if (lane == 0) {
+            breaks_s[i >> 5] = b;
+            if (i < a.chunk) first_s[i >> 5] = f;
+        }
+    }
+    __syncthreads();
+    // the first break from token i of the window on; past the window the slots are looked at
+    const auto run_end = [&](int i) {
+        for (; i < window; i = (i | 31) + 1) {
+            const uint32_t b = breaks_s[i >> 5] >> (i & 31);
+            if (b) {
+                i += __ffs(b) - 1;
                 break;
             }
         }
-        const bool mine = slot0 >= 0 && (before < 0 || before >> c.block_shift != block);
-        if (!mine) {
-            before = slot_at(t1 - 1);
-            t0 = t1;
+        int t = t_first + min(i, window);
+        if (i >= window) {
+            const int64_t block = slot_at(t - 1) >> c.block_shift;
+            for (int64_t s; t < a.T && (s = slot_at(t)) >= 0 && s >> c.block_shift == block; ++t) {}
+        }
+        return t;
+    };
+    for (int i0 = 0; i0 < t_last - t_first; ++i0) {
+        // the tokens [t0, t1) of one cache block
+        const uint32_t f = first_s[i0 >> 5] >> (i0 & 31);
+        if (f == 0) {
+            i0 |= 31;
             continue;
         }
+        i0 += __ffs(f) - 1;
+        if (i0 >= t_last - t_first) break;
+        const int t0 = t_first + i0, t1 = run_end(i0 + 1);
+        const int64_t slot0 = slot_at(t0);
         float *scale = scale_at(slot0);
         const float old = __ldcg(scale);
         uint4 held[kHeld];
         float top = 0.0f;
+        bool first = false;                           // the block's first slot is one of the run's
         const auto look = [&](const uint4 &v) {
             float x[8];
             unpack8<F16>(v, x);
@@ -138,12 +151,13 @@ __global__ void __launch_bounds__(kStoreThreads) store_e4m3_kernel(const __grid_
             const int t = t0 + k * kTokens + sub;
             held[k] = t < t1 ? load(t) : make_uint4(0, 0, 0, 0);
         }
+        for (int t = t0 + tid; t < t1; t += kStoreThreads) first |= (slot_at(t) & ((1 << c.block_shift) - 1)) == 0;
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) look(held[k]);
         for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) look(load(t));
         uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
         if (lane == 0) top_s[tid >> 5] = bits;
-        __syncthreads();                              // every thread has read the old scale
+        const bool anew = __syncthreads_or(first);    // every thread has read the old scale
         bits = top_s[0];
 #pragma unroll
         for (int w = 1; w < kStoreThreads / 32; ++w) bits = max(bits, top_s[w]);
@@ -180,8 +194,7 @@ __global__ void __launch_bounds__(kStoreThreads) store_e4m3_kernel(const __grid_
         for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) store(slot_at(t), load(t), s, inv);
         if (tid == 0) *scale = s;
         __syncthreads();                              // top_s is free
-        before = slot_at(t1 - 1);
-        t0 = t1;
+        i0 = t1 - t_first - 1;
     }
 }
 
