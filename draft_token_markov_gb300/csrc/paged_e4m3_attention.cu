@@ -273,7 +273,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
     };
 
     // 256 x 184 + 256 x 72 registers of the 512 x 128 at launch
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 15) {
         // ------------------------------------------- the walk, query loads
         Item it;
@@ -669,7 +669,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
         }
     } else {
         // -------------------------------------------- softmax and output
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         const int slot = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // TMEM lane of the warp
         const uint32_t t_s = tmem + slot * kTileRows + lanes, t_o = tmem + 2 * kTileRows + slot * D + lanes;
