@@ -7,13 +7,16 @@
 //   Z = sum 2^d,  S = sum 2^d d,  d = x c - M,  c = log2(e) / T,  M = m c rounded
 // against the slice's own maximum (one fused operation a logit; what the rounding of
 // M is worth is put right once, in the sums), the ids before the token, and the few
-// logits that may be among the `top` largest.  For these, the slice is cut into 64
-// groups (four neighbouring lanes each): the top-th largest group maximum is a bound
-// that at least `top` logits reach and that fewer than `top` groups exceed.  What
-// reaches it goes to a list, which is put in order by counting.  Where the list is
-// too short for that (a slice with many equal logits, a few lanes with all the large
-// ones), the block takes its maximum `top` times instead.  The first block joins the
-// cluster's sums and sorted lists, which the others write to its shared memory.
+// logits that may be among the `top` largest.  For these, a slice is cut into 64
+// groups (four neighbouring lanes each) and its j-th largest group maximum goes to
+// every block while the sums are taken: q of the cluster's blocks have j logits each
+// that reach the q-th largest of those, so that with q j >= top it bounds the row's
+// alternatives from below (about twice `top` logits reach it).  What reaches it goes
+// to a list, which is put in order by counting.  Where the list is too short (many
+// equal logits, all large ones in one slice), the slice's own top-th largest group
+// maximum is the bound, and where that is not enough either, the block takes its
+// maximum `top` times.  The first block joins the sums and the sorted lists, which
+// the others write to its shared memory.
 //
 // ln p = (d - log2 Z) ln 2, entropy = (log2 Z - S / Z) ln 2.
 #include <cmath>
@@ -101,12 +104,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// The address of the same variable in the cluster's first block.
-__device__ __forceinline__ uint32_t first_block(const void *p) {
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of the same variable in a block of the cluster.
+__device__ __forceinline__ uint32_t of_block(const void *p, uint32_t block) {
     uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)));
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(block));
     return r;
 }
 __device__ __forceinline__ void st_cluster(uint32_t to, uint32_t x) {
@@ -152,18 +161,33 @@ __device__ __forceinline__ uint32_t next_below(float x) {
     return b >> 31 ? b + one : b - one;
 }
 
+// The k-th largest of the 64 group maxima, as an ordered key; by a warp.
+__device__ __forceinline__ uint32_t group_bound(const uint32_t *group_key, int k) {
+    const int lane = threadIdx.x & 31;
+    uint32_t g0 = group_key[lane], g1 = group_key[32 + lane], g = 0;
+    for (int i = 0; i < k; ++i) {
+        const uint32_t mine = max(g0, g1);
+        g = __reduce_max_sync(0xffffffffu, mine);
+        const uint32_t who = __ballot_sync(0xffffffffu, mine == g);
+        if (lane == __ffs(who) - 1) {
+            if (g0 == g) g0 = 0; else g1 = 0;
+        }
+    }
+    return g;
+}
+
 template <bool F32, int N>
 __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     constexpr int kSize = F32 ? 4 : 2, kN = 16 / kSize;
     __shared__ Part parts[kMaxCluster];
+    __shared__ uint32_t bounds[kMaxCluster];
     __shared__ float warp_f[3][kWarps];
     __shared__ int warp_i[kWarps];
-    __shared__ uint64_t warp_k[kWarps], round_k[kWarps];
-    __shared__ float group_max[kGroups];
+    __shared__ uint64_t warp_k[kWarps];
+    __shared__ uint32_t group_key[kGroups];
     __shared__ uint64_t list[kList];
-    __shared__ int listed_s;
-    __shared__ float bound_s;
-    __shared__ uint64_t sorted[kMaxTop];
+    __shared__ int listed_s[2];
+    __shared__ uint32_t bound_s;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank(), blocks = gridDim.x;
@@ -176,16 +200,18 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
     // before the row; -inf where the row does not reach
     const uint8_t *from = a.logits + row * a.s0;
     const int lead = (int)(reinterpret_cast<uintptr_t>(from) & 15u) / kSize;
-    const int id0 = (int)(rank * (uint32_t)a.slice + tid) * kN - lead;  // of the thread's first vector
-    const int vectors = min(a.slice, (a.vocab + lead + kN - 1) / kN - (int)rank * a.slice);
+    const int slice0 = (int)rank * a.slice;                            // its first vector
+    const int vectors = min(a.slice, (a.vocab + lead + kN - 1) / kN - slice0);
+    const int whole0 = slice0 == 0 && lead > 0 ? 1 : 0;                // vectors that lie in the row, whole
+    const int whole = min(vectors, (a.vocab + lead) / kN - slice0) - whole0;
+    const int id0 = (slice0 + tid) * kN - lead;                        // of the thread's first vector
     constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;
     uint4 x[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int id = id0 + i * kThreads * kN;
         x[i] = make_uint4(kNone, kNone, kNone, kNone);
-        if (tid + i * kThreads < vectors && id >= 0 && id + kN <= a.vocab)
-            x[i] = __ldcs(reinterpret_cast<const uint4 *>(from + (int64_t)id * kSize));
+        const int v = tid + i * kThreads - whole0;
+        if (v >= 0 && v < whole) x[i] = __ldcs(reinterpret_cast<const uint4 *>(from + (int64_t)id0 * kSize) + i * kThreads);
     }
     float T = a.temperature ? __ldg(a.temperature + row) : 1.0f;
     if (!samples(T)) T = 1.0f;
@@ -193,31 +219,34 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
     if (a.tokens)
         own = F32 ? __ldg(reinterpret_cast<const float *>(from) + token)
                   : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + token) << 16);
+    if (whole < vectors) {
+        // the vectors at the row's ends, which are not its own in part
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int id = id0 + i * kThreads * kN;
-        if (tid + i * kThreads >= vectors || (id >= 0 && id + kN <= a.vocab)) continue;
-        uint32_t w[4];
+        for (int i = 0; i < N; ++i) {
+            const int v = tid + i * kThreads, id = id0 + i * kThreads * kN;
+            if (v >= vectors || (v >= whole0 && v < whole0 + whole)) continue;
+            uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            const bool there = id + e >= 0 && id + e < a.vocab;
-            if (F32) {
-                w[e % 4] = there ? __ldg(reinterpret_cast<const uint32_t *>(from) + id + e) : 0xff800000u;
-            } else {
-                const uint32_t y = there ? __ldg(reinterpret_cast<const uint16_t *>(from) + id + e) : 0xff80u;
-                w[e / 2 % 4] = e & 1 ? w[e / 2 % 4] | y << 16 : y;
+            for (int e = 0; e < kN; ++e) {
+                const bool there = id + e >= 0 && id + e < a.vocab;
+                if (F32) {
+                    w[e % 4] = there ? __ldg(reinterpret_cast<const uint32_t *>(from) + id + e) : 0xff800000u;
+                } else {
+                    const uint32_t y = there ? __ldg(reinterpret_cast<const uint16_t *>(from) + id + e) : 0xff80u;
+                    w[e / 2 % 4] = e & 1 ? w[e / 2 % 4] | y << 16 : y;
+                }
             }
+            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        x[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
     // finite, and not 0: with T = inf the difference of finite logits vanishes, -inf stays
     const float c = fmaxf(fminf(__fdiv_rn(1.4426950408889634f, T), 3.0e38f), 1.401298464e-45f);
-    if (tid == 0) listed_s = 0;
+    if (tid < 2) listed_s[tid] = 0;
     // f(logit, id) of the slice's logits, read again: for what is rare
     const auto each = [&](const auto &f) {
-        const int id1 = min(((int)rank * a.slice + vectors) * kN - lead, a.vocab);
+        const int id1 = min((slice0 + vectors) * kN - lead, a.vocab);
 #pragma unroll 1
-        for (int id = max((int)rank * a.slice * kN - lead, 0) + tid; id < id1; id += kThreads)
+        for (int id = max(slice0 * kN - lead, 0) + tid; id < id1; id += kThreads)
             f(F32 ? __ldg(reinterpret_cast<const float *>(from) + id)
                   : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + id) << 16),
               id);
@@ -231,12 +260,19 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
     const float top = F32 ? __uint_as_float(word) : __uint_as_float(word_max<true>(word << 16, word & 0xffff0000u));
     float group = nan_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     group = nan_max(group, __shfl_xor_sync(0xffffffffu, group, 2));
-    if ((lane & 3) == 0) group_max[tid >> 2] = group;
+    if ((lane & 3) == 0) group_key[tid >> 2] = ordered_key(group);
     float m = group;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) warp_f[0][warp] = m;
     __syncthreads();
+    const int q = max((int)blocks / 2, 1);
+    if (blocks > 1) cluster_wait();                                    // of the first arrival
+    if (a.top > 0 && warp == 0) {
+        const uint32_t g = group_bound(group_key, (a.top + q - 1) / q);
+        if (lane < blocks) st_cluster(of_block(bounds + rank, lane), g);
+    }
+    if (blocks > 1) cluster_arrive();
     m = warp_f[0][0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) m = nan_max(m, warp_f[0][w]);
@@ -285,18 +321,25 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
         });
     }
     if (a.tokens && !by_key) {
+        // equal logits count where their ids are lower
         const uint32_t equal = __float_as_uint(own), below = next_below<F32>(own);
+        const int first_id = slice0 * kN - lead, end_id = first_id + vectors * kN;
         Above<F32> above;
+        if (token < first_id || token >= end_id) {
+            const uint32_t bound = token < first_id ? equal : below;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int id = id0 + i * kThreads * kN;
-            // equal logits count where their ids are lower
-            if (id <= token && token < id + kN) {
-                const Logits<F32> l(x[i]);
+            for (int i = 0; i < N; ++i) above.take(x[i], bound);
+        } else {
 #pragma unroll
-                for (int e = 0; e < kN; ++e) before += id + e < token ? l.x[e] >= own : l.x[e] > own;
-            } else {
-                above.take(x[i], id > token ? equal : below);
+            for (int i = 0; i < N; ++i) {
+                const int id = id0 + i * kThreads * kN;
+                if (id <= token && token < id + kN) {
+                    const Logits<F32> l(x[i]);
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) before += id + e < token ? l.x[e] >= own : l.x[e] > own;
+                } else {
+                    above.take(x[i], id > token ? equal : below);
+                }
             }
         }
         before += above.count();
@@ -322,28 +365,27 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
         warp_i[warp] = before;
         warp_k[warp] = best;
     }
+    if (blocks > 1) cluster_wait(); else __syncthreads();              // the bounds, the warps' sums
 
     // --------------------------------------------------------- alternatives
+    const uint32_t part_at = of_block(parts + rank, 0);
+    const auto put = [&](int n, uint64_t k) { st_cluster(part_at + (uint32_t)offsetof(Part, top) + 8 * n, k); };
     if (a.top > 0) {
-        if (warp == 0) {
-            // the top-th largest group maximum
-            uint32_t g0 = ordered_key(group_max[lane]), g1 = ordered_key(group_max[32 + lane]), g = 0;
-            for (int k = 0; k < a.top; ++k) {
-                const uint32_t mine = max(g0, g1);
-                g = __reduce_max_sync(0xffffffffu, mine);
-                const uint32_t who = __ballot_sync(0xffffffffu, mine == g);
-                if (lane == __ffs(who) - 1) {
-                    if (g0 == g) g0 = 0; else g1 = 0;
-                }
-            }
-            if (lane == 0) bound_s = key_from_ordered(g);
-        } else if (warp == 1) {
-            sorted[lane] = 0;
+        // the q-th largest of the blocks' bounds
+        const uint32_t mine = lane < blocks ? bounds[lane] : 0;
+        int larger = 0;
+        for (int b = 0; b < (int)blocks; ++b) {
+            const uint32_t y = bounds[b];
+            larger += y > mine || (y == mine && b < lane);
         }
-        __syncthreads();
-        const float bound = bound_s;
-        const bool nothing = bound == -INFINITY;                       // groups without a logit: -inf is not listed
-        if (top >= bound && top > -INFINITY) {
+        const uint32_t at_q = __ballot_sync(0xffffffffu, lane < blocks && larger == q - 1);
+        uint32_t bound_key = __shfl_sync(0xffffffffu, mine, __ffs(at_q) - 1);
+        const bool whole_way = m != m || m == INFINITY;                // NaN and infinities: by their keys
+        int listed = 0;
+        bool slow = whole_way;
+        const auto collect = [&](int *count) {
+            const float bound = key_from_ordered(bound_key);
+            if (!(top >= bound) || top == -INFINITY) return;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const uint32_t w = word_max<F32>(word_max<F32>(x[i].x, x[i].y), word_max<F32>(x[i].z, x[i].w));
@@ -353,18 +395,33 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
 #pragma unroll
                 for (int e = 0; e < kN; ++e)
                     if (l.x[e] >= bound && l.x[e] > -INFINITY) {
-                        const int at = atomicAdd(&listed_s, 1);
+                        const int at = atomicAdd(count, 1);
                         if (at < kList) list[at] = pack_key(l.x[e], (uint32_t)(id0 + i * kThreads * kN + e));
                     }
             }
+        };
+        if (!slow) {
+            collect(listed_s);
+            __syncthreads();
+            listed = listed_s[0];
+            if (listed > kList) {
+                if (warp == 0) {
+                    const uint32_t g = group_bound(group_key, a.top);
+                    if (lane == 0) bound_s = max(bound_key, g);
+                }
+                __syncthreads();
+                bound_key = bound_s;
+                collect(listed_s + 1);
+                __syncthreads();
+                listed = listed_s[1];
+                slow = listed > kList;
+            }
         }
-        __syncthreads();
-        int listed = listed_s;
-        // masked ids follow by their number: those of the first 32 vectors are enough, or the slow way
-        bool slow = listed > kList || m != m || m == INFINITY;
-        if (nothing && listed < a.top && !slow) {
-            uint32_t masked = 0;
+        if (!slow && listed < a.top && key_from_ordered(bound_key) == -INFINITY) {
+            // masked ids follow by their number: those of the first 32 vectors are enough, or the slow way
+            __syncthreads();                                           // listed_s is read
             if (warp == 0) {
+                uint32_t masked = 0;
                 const Logits<F32> l(x[0]);
 #pragma unroll
                 for (int e = 0; e < kN; ++e)
@@ -383,71 +440,71 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
                         if (at < a.top) list[listed + at] = pack_key(-INFINITY, (uint32_t)(id0 + e));
                         ++at;
                     }
-                if (lane == 0) listed_s = all >= a.top || vectors <= 32 ? listed + min(all, a.top) : kList + 1;
+                if (lane == 0) listed_s[0] = all >= a.top || vectors <= 32 ? listed + min(all, a.top) : kList + 1;
             }
             __syncthreads();
-            listed = listed_s;
+            listed = listed_s[0];
             slow = listed > kList;
         }
         if (!slow) {
-            for (int i = tid; i < listed; i += kThreads) {
+            // in order, by counting; by one warp where the others would not help
+            const int step = listed > 64 ? kThreads : 32;
+            for (int i = tid; i < listed && tid < step; i += step) {
                 const uint64_t k = list[i];
                 int n = 0;
                 for (int j = 0; j < listed; ++j) n += list[j] > k;
-                if (n < a.top) sorted[n] = k;
+                if (n < a.top) put(n, k);
             }
+            if (tid < a.top && tid >= listed) put(tid, 0);
         } else {
             uint64_t last = 1;
-            for (int n = 0; n < a.top && last != 0; ++n) {
+            for (int n = 0; n < a.top; ++n) {
                 uint64_t most = 0;
-                each([&](float l, int id) {
-                    const uint64_t k = pack_key(l, (uint32_t)id);
-                    if (n == 0 || k < last) most = k > most ? k : most;
-                });
+                if (last != 0)
+                    each([&](float l, int id) {
+                        const uint64_t k = pack_key(l, (uint32_t)id);
+                        if (n == 0 || k < last) most = k > most ? k : most;
+                    });
                 most = warp_max_key(most);
-                if (lane == 0) round_k[warp] = most;
+                if (lane == 0) list[warp] = most;
                 __syncthreads();
                 last = 0;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) last = round_k[w] > last ? round_k[w] : last;
-                if (tid == 0) sorted[n] = last;
+                for (int w = 0; w < kWarps; ++w) last = list[w] > last ? list[w] : last;
+                if (tid == 0) put(n, last);
                 __syncthreads();
             }
         }
     }
-    __syncthreads();
 
     // ------------------------------------------------------------ the parts
-    Part &mine = parts[rank];
-    if (blocks > 1) cluster_wait();                                    // the first block runs
-    if (warp == 0) {
-        z = s = 0.0f;
-        before = 0;
-        best = 0;
+    if (warp == kWarps - 1) {
+        z = lane < kWarps ? warp_f[1][lane] : 0.0f;
+        s = lane < kWarps ? warp_f[2][lane] : 0.0f;
+        before = lane < kWarps ? warp_i[lane] : 0;
+        best = lane < kWarps ? warp_k[lane] : 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            z += warp_f[1][w];
-            s += warp_f[2][w];
-            before += warp_i[w];
-            best = warp_k[w] > best ? warp_k[w] : best;
+        for (int o = kWarps / 2; o > 0; o >>= 1) {
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+            s += __shfl_xor_sync(0xffffffffu, s, o);
         }
-        const uint32_t to = first_block(&mine);
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (odd) best = warp_max_key(best);
         if (lane == 0) {
-            st_cluster(to + offsetof(Part, m), __float_as_uint(m));
-            st_cluster(to + offsetof(Part, z), __float_as_uint(z));
-            st_cluster(to + offsetof(Part, s), __float_as_uint(s));
-            st_cluster(to + offsetof(Part, before), (uint32_t)before);
-            st_cluster(to + offsetof(Part, best), best);
+            st_cluster(part_at + offsetof(Part, m), __float_as_uint(m));
+            st_cluster(part_at + offsetof(Part, z), __float_as_uint(z));
+            st_cluster(part_at + offsetof(Part, s), __float_as_uint(s));
+            st_cluster(part_at + offsetof(Part, before), (uint32_t)before);
+            st_cluster(part_at + offsetof(Part, best), best);
         }
-        if (lane < a.top) st_cluster(to + offsetof(Part, top) + 8 * lane, sorted[lane]);
     }
     if (blocks > 1) {
         cluster_arrive();
+        if (rank != 0) return;
         cluster_wait();
     } else {
         __syncthreads();
     }
-    if (rank != 0) return;
 
     // ------------------------------------------------------------- the join
     float all = parts[0].m;
