@@ -1,24 +1,22 @@
 // logprobs.cu -- log probabilities of given tokens, rank, entropy and the most
-// probable alternatives: one launch, a cluster of thread blocks a row of logits,
-// and its C ABI.
+// probable alternatives: one launch and its C ABI.
 //
-// Each block of the cluster has a slice of the row in its threads' registers, read
-// once from memory: the maximum m, the sums
+// A block has a row of logits, or a cluster of blocks a slice each where there are
+// few rows.  Its threads stream the slice once, four vectors of 16 bytes a turn and
+// the next four on their way, without a stop for the block: a thread keeps its own
+// maximum m and
 //   Z = sum 2^d,  S = sum 2^d d,  d = x c - M,  c = log2(e) / T,  M = m c rounded
-// against the slice's own maximum (one fused operation a logit; what the rounding of
-// M is worth is put right once, in the sums), the ids before the token, and the few
-// logits that may be among the `top` largest.  For these, a slice is cut into 64
-// groups (four neighbouring lanes each) and its j-th largest group maximum goes to
-// every block while the sums are taken: q of the cluster's blocks have j logits each
-// that reach the q-th largest of those, so that with q j >= top it bounds the row's
-// alternatives from below (about twice `top` logits reach it).  What reaches it goes
-// to a list, which is put in order by counting.  Where the list is too short (many
-// equal logits, all large ones in one slice), the slice's own top-th largest group
-// maximum is the bound, and where that is not enough either, the block takes its
-// maximum `top` times.  The first block joins the sums and the sorted lists, which
-// the others write to its shared memory.
+// (one fused operation a logit; what the rounding of M is worth is put right at the
+// end), the ids before the token, and each turn's maximum in shared memory.  The
+// top-th largest of the threads' maxima bounds the alternatives from below; turns
+// that reach it are read again (from L2; some 20 of 4000 for 20 alternatives of a row
+// of 129280), and what reaches it in them goes to a list, which is put in order by
+// counting.  Where the list is too short (many equal logits), the block takes its
+// maximum `top` times instead.  The cluster's first block joins sums and sorted
+// lists, which the others write to its shared memory.
 //
 // ln p = (d - log2 Z) ln 2, entropy = (log2 Z - S / Z) ln 2.
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
@@ -36,7 +34,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kGroups = kThreads / 4;
+constexpr int kTurn = 4;                  // vectors of a thread's turn
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 constexpr int kList = 512;                // logits that may be among the largest
@@ -134,9 +132,11 @@ struct Above;
 template <>
 struct Above<false> {
     __nv_bfloat162 n = __float2bfloat162_rn(0.0f);
+    // the bound in both halves
+    static __device__ __forceinline__ uint32_t spread(uint32_t bound) { return bound >> 16 | (bound & 0xffff0000u); }
     __device__ __forceinline__ void take(const uint4 &v, uint32_t bound) {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w}, b2 = bound >> 16 | (bound & 0xffff0000u);
-        const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(&b2);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162 *>(&bound);
 #pragma unroll
         for (int i = 0; i < 4; ++i) n = __hadd2(n, __hgt2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), b));
     }
@@ -145,6 +145,7 @@ struct Above<false> {
 template <>
 struct Above<true> {
     int n = 0;
+    static __device__ __forceinline__ uint32_t spread(uint32_t bound) { return bound; }
     __device__ __forceinline__ void take(const uint4 &v, uint32_t bound) {
         const float b = __uint_as_float(bound);
         n += (__uint_as_float(v.x) > b) + (__uint_as_float(v.y) > b) + (__uint_as_float(v.z) > b) + (__uint_as_float(v.w) > b);
@@ -161,139 +162,56 @@ __device__ __forceinline__ uint32_t next_below(float x) {
     return b >> 31 ? b + one : b - one;
 }
 
-// The k-th largest of the 64 group maxima, as an ordered key; by a warp.
-__device__ __forceinline__ uint32_t group_bound(const uint32_t *group_key, int k) {
-    const int lane = threadIdx.x & 31;
-    uint32_t g0 = group_key[lane], g1 = group_key[32 + lane], g = 0;
-    for (int i = 0; i < k; ++i) {
-        const uint32_t mine = max(g0, g1);
-        g = __reduce_max_sync(0xffffffffu, mine);
-        const uint32_t who = __ballot_sync(0xffffffffu, mine == g);
-        if (lane == __ffs(who) - 1) {
-            if (g0 == g) g0 = 0; else g1 = 0;
+// A vector at a row's end, -inf where the row does not reach; id: of its first logit.
+template <bool F32>
+__device__ __noinline__ uint4 edge_vector(const uint8_t *from, int id, int vocab) {
+    constexpr int kN = F32 ? 4 : 8;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+        const bool there = id + e >= 0 && id + e < vocab;
+        if (F32) {
+            w[e % 4] = there ? __ldg(reinterpret_cast<const uint32_t *>(from) + id + e) : 0xff800000u;
+        } else {
+            const uint32_t y = there ? __ldg(reinterpret_cast<const uint16_t *>(from) + id + e) : 0xff80u;
+            w[e / 2 % 4] = e & 1 ? w[e / 2 % 4] | y << 16 : y;
         }
     }
-    return g;
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <bool F32, int N>
-__global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
-    constexpr int kSize = F32 ? 4 : 2, kN = 16 / kSize;
-    __shared__ Part parts[kMaxCluster];
-    __shared__ uint32_t bounds[kMaxCluster];
-    __shared__ float warp_f[3][kWarps];
-    __shared__ int warp_i[kWarps];
-    __shared__ uint64_t warp_k[kWarps];
-    __shared__ uint32_t group_key[kGroups];
-    __shared__ uint64_t list[kList];
-    __shared__ int listed_s[2];
-    __shared__ uint32_t bound_s;
+// A thread's logits so far.
+template <bool F32>
+struct Running {
+    float m = -INFINITY, M = 0.0f, z = 0.0f, s = 0.0f;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank(), blocks = gridDim.x;
-    const int64_t row = blockIdx.y;
-    const int64_t token = a.tokens ? __ldg(a.tokens + row) : -1;
-    if (a.tokens && (token < 0 || token >= a.vocab)) return;           // the whole cluster
-    if (blocks > 1) cluster_arrive();                                  // every block runs
-
-    // the slice: whole vectors from the row's first on, whose first elements may lie
-    // before the row; -inf where the row does not reach
-    const uint8_t *from = a.logits + row * a.s0;
-    const int lead = (int)(reinterpret_cast<uintptr_t>(from) & 15u) / kSize;
-    const int slice0 = (int)rank * a.slice;                            // its first vector
-    const int vectors = min(a.slice, (a.vocab + lead + kN - 1) / kN - slice0);
-    const int whole0 = slice0 == 0 && lead > 0 ? 1 : 0;                // vectors that lie in the row, whole
-    const int whole = min(vectors, (a.vocab + lead) / kN - slice0) - whole0;
-    const int id0 = (slice0 + tid) * kN - lead;                        // of the thread's first vector
-    constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;
-    uint4 x[N];
+    // One turn; returns its maximum.
+    __device__ __forceinline__ float take(const uint4 (&x)[kTurn], float c) {
+        constexpr int kN = F32 ? 4 : 8;
+        uint32_t w = word_max<F32>(word_max<F32>(x[0].x, x[0].y), word_max<F32>(x[0].z, x[0].w));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        x[i] = make_uint4(kNone, kNone, kNone, kNone);
-        const int v = tid + i * kThreads - whole0;
-        if (v >= 0 && v < whole) x[i] = __ldcs(reinterpret_cast<const uint4 *>(from + (int64_t)id0 * kSize) + i * kThreads);
-    }
-    float T = a.temperature ? __ldg(a.temperature + row) : 1.0f;
-    if (!samples(T)) T = 1.0f;
-    float own = 0.0f;
-    if (a.tokens)
-        own = F32 ? __ldg(reinterpret_cast<const float *>(from) + token)
-                  : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + token) << 16);
-    if (whole < vectors) {
-        // the vectors at the row's ends, which are not its own in part
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int v = tid + i * kThreads, id = id0 + i * kThreads * kN;
-            if (v >= vectors || (v >= whole0 && v < whole0 + whole)) continue;
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                const bool there = id + e >= 0 && id + e < a.vocab;
-                if (F32) {
-                    w[e % 4] = there ? __ldg(reinterpret_cast<const uint32_t *>(from) + id + e) : 0xff800000u;
-                } else {
-                    const uint32_t y = there ? __ldg(reinterpret_cast<const uint16_t *>(from) + id + e) : 0xff80u;
-                    w[e / 2 % 4] = e & 1 ? w[e / 2 % 4] | y << 16 : y;
-                }
+        for (int k = 1; k < kTurn; ++k)
+            w = word_max<F32>(w, word_max<F32>(word_max<F32>(x[k].x, x[k].y), word_max<F32>(x[k].z, x[k].w)));
+        const float top = F32 ? __uint_as_float(w) : __uint_as_float(word_max<true>(w << 16, w & 0xffff0000u));
+        if (!(top <= m) && m == m) {                  // larger, or NaN, which stays
+            const float next = top * c, back = M - next;
+            if (m != -INFINITY) {
+                const float f = ex2(back);
+                s = f * fmaf(back, z, s);
+                z *= f;
             }
-            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            m = top;
+            M = next;
         }
-    }
-    // finite, and not 0: with T = inf the difference of finite logits vanishes, -inf stays
-    const float c = fmaxf(fminf(__fdiv_rn(1.4426950408889634f, T), 3.0e38f), 1.401298464e-45f);
-    if (tid < 2) listed_s[tid] = 0;
-    // f(logit, id) of the slice's logits, read again: for what is rare
-    const auto each = [&](const auto &f) {
-        const int id1 = min((slice0 + vectors) * kN - lead, a.vocab);
-#pragma unroll 1
-        for (int id = max(slice0 * kN - lead, 0) + tid; id < id1; id += kThreads)
-            f(F32 ? __ldg(reinterpret_cast<const float *>(from) + id)
-                  : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + id) << 16),
-              id);
-    };
-
-    // ------------------------------------------------------------- maximum
-    uint32_t word = kNone;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        word = word_max<F32>(word, word_max<F32>(word_max<F32>(x[i].x, x[i].y), word_max<F32>(x[i].z, x[i].w)));
-    const float top = F32 ? __uint_as_float(word) : __uint_as_float(word_max<true>(word << 16, word & 0xffff0000u));
-    float group = nan_max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    group = nan_max(group, __shfl_xor_sync(0xffffffffu, group, 2));
-    if ((lane & 3) == 0) group_key[tid >> 2] = ordered_key(group);
-    float m = group;
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) warp_f[0][warp] = m;
-    __syncthreads();
-    const int q = max((int)blocks / 2, 1);
-    if (blocks > 1) cluster_wait();                                    // of the first arrival
-    if (a.top > 0 && warp == 0) {
-        const uint32_t g = group_bound(group_key, (a.top + q - 1) / q);
-        if (lane < blocks) st_cluster(of_block(bounds + rank, lane), g);
-    }
-    if (blocks > 1) cluster_arrive();
-    m = warp_f[0][0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) m = nan_max(m, warp_f[0][w]);
-    const bool odd = !(fabsf(m) < INFINITY);                           // NaN, an infinity, nothing
-
-    // ------------------------------------------- sums, ids before the token
-    float z = 0.0f, s = 0.0f;
-    int before = 0;
-    uint64_t best = 0;
-    const float M = m * c;
-    const bool fused = fabsf(M) < 1e30f && c > 1e-20f && c < 1e7f;     // else differences come first
-    const bool by_key = a.tokens && (odd || !(own > -INFINITY));       // NaN or -inf in the comparison
-    if (!odd && fused) {
+        if (m == -INFINITY) return top;
         const uint64_t neg = f32x2(-M, -M), c2 = f32x2(c, c);
         uint64_t z2[2] = {0, 0}, s2[2] = {0, 0};
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int k = 0; k < kTurn; ++k) {
             // a masked logit's 0 times -inf would be NaN: -1e30 times c weighs 0 too
             constexpr uint32_t kLow = F32 ? 0xf149f2cau : 0xf149f149u;
-            const Logits<F32> l(make_uint4(word_max<F32>(x[i].x, kLow), word_max<F32>(x[i].y, kLow), word_max<F32>(x[i].z, kLow),
-                                           word_max<F32>(x[i].w, kLow)));
+            const Logits<F32> l(make_uint4(word_max<F32>(x[k].x, kLow), word_max<F32>(x[k].y, kLow), word_max<F32>(x[k].z, kLow),
+                                           word_max<F32>(x[k].w, kLow)));
 #pragma unroll
             for (int e = 0; e < kN; e += 2) {
                 const uint64_t d = fma2(f32x2(l.x[e], l.x[e + 1]), c2, neg);
@@ -307,12 +225,143 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
         float x0, x1, y0, y1;
         split2(add2(z2[0], z2[1]), x0, x1);
         split2(add2(s2[0], s2[1]), y0, y1);
-        z = x0 + x1;
-        s = y0 + y1;
-        // relative to m c instead of M
-        const float off = fmaf(m, c, -M), f = ex2(-off);
-        s = f * fmaf(-off, z, s);
-        z *= f;
+        z += x0 + x1;
+        s += y0 + y1;
+        return top;
+    }
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_constant__ LogprobArgs a) {
+    constexpr int kSize = F32 ? 4 : 2, kN = 16 / kSize, kTurnVectors = kTurn * kThreads;
+    extern __shared__ float turn_max[];                                // [turns][kThreads]
+    __shared__ Part parts[kMaxCluster];
+    __shared__ float warp_f[3][kWarps];
+    __shared__ int warp_i[kWarps];
+    __shared__ uint64_t warp_k[kWarps];
+    __shared__ uint32_t thread_key[kThreads];
+    __shared__ uint64_t list[kList];
+    __shared__ int listed_s;
+    __shared__ uint32_t bound_s;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank(), blocks = gridDim.x;
+    const int64_t row = blockIdx.y;
+    const int64_t token64 = a.tokens ? __ldg(a.tokens + row) : 0;
+
+    // the slice: whole vectors from the row's first on, whose first elements may lie
+    // before the row
+    const uint8_t *from = a.logits + row * a.s0;
+    const int lead = (int)(reinterpret_cast<uintptr_t>(from) & 15u) / kSize;
+    const int slice0 = (int)rank * a.slice;                            // its first vector
+    const int vectors = max(min(a.slice, (a.vocab + lead + kN - 1) / kN - slice0), 0);
+    const int whole0 = slice0 == 0 && lead > 0 ? 1 : 0;                // vectors that lie in the row, whole
+    const int whole = min(vectors, (a.vocab + lead) / kN - slice0) - whole0;
+    const int first_id = slice0 * kN - lead;                           // of the slice's first vector
+    const uint8_t *at0 = from + (int64_t)first_id * kSize;
+    constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80ff80u;
+    const auto load1 = [&](int v) {
+        if ((uint32_t)(v - whole0) < (uint32_t)whole && whole > 0) return __ldg(reinterpret_cast<const uint4 *>(at0) + v);
+        if (v < vectors) return edge_vector<F32>(from, first_id + v * kN, a.vocab);
+        return make_uint4(kNone, kNone, kNone, kNone);
+    };
+    const uint4 *mine = reinterpret_cast<const uint4 *>(at0) + tid;
+    const auto load = [&](uint4 (&x)[kTurn], int turn) {
+        const int v0 = turn * kTurnVectors;
+        if (v0 >= whole0 && v0 + kTurnVectors <= whole0 + whole) {
+#pragma unroll
+            for (int k = 0; k < kTurn; ++k) x[k] = __ldg(mine + v0 + k * kThreads);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTurn; ++k) x[k] = load1(v0 + k * kThreads + tid);
+        }
+    };
+    // f(logit, id) of the slice's logits, read again: for what is rare
+    const auto each = [&](const auto &f) {
+        const int id1 = min(first_id + vectors * kN, a.vocab);
+#pragma unroll 1
+        for (int id = max(first_id, 0) + tid; id < id1; id += kThreads)
+            f(F32 ? __ldg(reinterpret_cast<const float *>(from) + id)
+                  : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + id) << 16),
+              id);
+    };
+    uint4 x[kTurn], y[kTurn];
+    const int turns = (vectors + kTurnVectors - 1) / kTurnVectors;
+    if (turns > 0) load(x, 0);                                         // on its way while the token comes
+    if (token64 < 0 || token64 >= a.vocab) return;                     // the whole cluster
+    if (blocks > 1) cluster_arrive();                                  // every block runs
+    const int token = (int)token64;
+    float T = a.temperature ? __ldg(a.temperature + row) : 1.0f;
+    if (!samples(T)) T = 1.0f;
+    float own = 0.0f;
+    if (a.tokens)
+        own = F32 ? __ldg(reinterpret_cast<const float *>(from) + token)
+                  : __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(from) + token) << 16);
+    // finite, and not 0: with T = inf the difference of finite logits vanishes, -inf stays
+    const float c = fmaxf(fminf(__fdiv_rn(1.4426950408889634f, T), 3.0e38f), 1.401298464e-45f);
+    if (tid == 0) listed_s = 0;
+
+    // ------------------------------------------------------------- the stream
+    // equal logits come before the token where their ids are lower
+    const bool ranked = a.tokens && fabsf(own) < INFINITY;
+    const uint32_t equal = Above<F32>::spread(__float_as_uint(own)), below = Above<F32>::spread(next_below<F32>(own));
+    Running<F32> r;
+    Above<F32> above;
+    int before = 0;
+    const auto take = [&](const uint4 (&x)[kTurn], int turn) {
+        turn_max[turn * kThreads + tid] = r.take(x, c);
+        if (!ranked) return;
+        // the turn lies before the token, behind it or around it
+        const int id = first_id + turn * kTurnVectors * kN;
+        if (token < id || token >= id + kTurnVectors * kN) {
+            const uint32_t bound = token < id ? equal : below;
+#pragma unroll
+            for (int k = 0; k < kTurn; ++k) above.take(x[k], bound);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kTurn; ++k) {
+                const int at = id + (k * kThreads + tid) * kN;
+                const Logits<F32> l(x[k]);
+#pragma unroll
+                for (int e = 0; e < kN; ++e) before += at + e < token ? l.x[e] >= own : l.x[e] > own;
+            }
+        }
+        // BF16 counts are exact up to 256 in each half
+        if ((turn & 7) == 7) {
+            before += above.count();
+            above = Above<F32>();
+        }
+    };
+#pragma unroll 1
+    for (int turn = 0; turn < turns; turn += 2) {
+        if (turn + 1 < turns) load(y, turn + 1);
+        take(x, turn);
+        if (turn + 1 == turns) break;
+        if (turn + 2 < turns) load(x, turn + 2);
+        take(y, turn + 1);
+    }
+    before += above.count();
+    thread_key[tid] = ordered_key(r.m);
+    float m = r.m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) warp_f[0][warp] = m;
+    // what the fused form cannot do: scales and logits that leave its range
+    const bool wild = r.m != -INFINITY && !(fabsf(r.M) < 1e30f);
+    const bool plain = __syncthreads_or(wild) || c < 1e-20f || c > 1e7f;
+    m = warp_f[0][0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) m = nan_max(m, warp_f[0][w]);
+    const bool odd = !(fabsf(m) < INFINITY);                           // NaN, an infinity, nothing
+    float z = 0.0f, s = 0.0f;
+    uint64_t best = 0;
+    if (!odd && !plain) {
+        if (r.m != -INFINITY) {
+            // relative to the slice's maximum, and to m c instead of M
+            const float off = fmaf(r.m, c, -r.M), d = fmaf(r.m - m, c, -off), f = ex2(d);
+            s = f > 0.0f ? f * fmaf(d, r.z, r.s) : 0.0f;
+            z = f * r.z;
+        }
     } else if (!odd) {
         each([&](float l, int) {
             const float d = (l - m) * c, p = ex2(d);
@@ -320,31 +369,9 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
             s += d > -1024.0f ? p * d : 0.0f;
         });
     }
-    if (a.tokens && !by_key) {
-        // equal logits count where their ids are lower
-        const uint32_t equal = __float_as_uint(own), below = next_below<F32>(own);
-        const int first_id = slice0 * kN - lead, end_id = first_id + vectors * kN;
-        Above<F32> above;
-        if (token < first_id || token >= end_id) {
-            const uint32_t bound = token < first_id ? equal : below;
-#pragma unroll
-            for (int i = 0; i < N; ++i) above.take(x[i], bound);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int id = id0 + i * kThreads * kN;
-                if (id <= token && token < id + kN) {
-                    const Logits<F32> l(x[i]);
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) before += id + e < token ? l.x[e] >= own : l.x[e] > own;
-                } else {
-                    above.take(x[i], id > token ? equal : below);
-                }
-            }
-        }
-        before += above.count();
-    }
+    const bool by_key = a.tokens && (odd || !ranked);                  // NaN or an infinity in the comparison
     if (odd || by_key) {
+        if (by_key) before = 0;
         const uint64_t own_key = a.tokens ? pack_key(own, (uint32_t)token) : 0;
         each([&](float l, int id) {
             const uint64_t k = pack_key(l, (uint32_t)id);
@@ -365,85 +392,91 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
         warp_i[warp] = before;
         warp_k[warp] = best;
     }
-    if (blocks > 1) cluster_wait(); else __syncthreads();              // the bounds, the warps' sums
+    if (a.top > 0 && warp == 0) {
+        // the top-th largest of the threads' maxima, eight a lane
+        uint32_t g[kWarps], key = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) g[w] = thread_key[w * 32 + lane];
+        for (int i = 0; i < a.top; ++i) {
+            uint32_t mine = g[0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) mine = max(mine, g[w]);
+            key = __reduce_max_sync(0xffffffffu, mine);
+            const uint32_t who = __ballot_sync(0xffffffffu, mine == key);
+            if (lane == __ffs(who) - 1) {
+                bool gone = false;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    if (!gone && g[w] == key) {
+                        g[w] = 0;
+                        gone = true;
+                    }
+            }
+        }
+        if (lane == 0) bound_s = key;
+    }
+    if (blocks > 1) cluster_wait();                                    // the first block runs
+    __syncthreads();
 
     // --------------------------------------------------------- alternatives
     const uint32_t part_at = of_block(parts + rank, 0);
     const auto put = [&](int n, uint64_t k) { st_cluster(part_at + (uint32_t)offsetof(Part, top) + 8 * n, k); };
     if (a.top > 0) {
-        // the q-th largest of the blocks' bounds
-        const uint32_t mine = lane < blocks ? bounds[lane] : 0;
-        int larger = 0;
-        for (int b = 0; b < (int)blocks; ++b) {
-            const uint32_t y = bounds[b];
-            larger += y > mine || (y == mine && b < lane);
-        }
-        const uint32_t at_q = __ballot_sync(0xffffffffu, lane < blocks && larger == q - 1);
-        uint32_t bound_key = __shfl_sync(0xffffffffu, mine, __ffs(at_q) - 1);
-        const bool whole_way = m != m || m == INFINITY;                // NaN and infinities: by their keys
+        const float bound = key_from_ordered(bound_s);
+        bool slow = m != m || m == INFINITY;                           // NaN and infinities: by their keys
         int listed = 0;
-        bool slow = whole_way;
-        const auto collect = [&](int *count) {
-            const float bound = key_from_ordered(bound_key);
-            if (!(top >= bound) || top == -INFINITY) return;
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint32_t w = word_max<F32>(word_max<F32>(x[i].x, x[i].y), word_max<F32>(x[i].z, x[i].w));
-                const float most = F32 ? __uint_as_float(w) : __uint_as_float(word_max<true>(w << 16, w & 0xffff0000u));
-                if (!(most >= bound) || most == -INFINITY) continue;
-                const Logits<F32> l(x[i]);
-#pragma unroll
-                for (int e = 0; e < kN; ++e)
-                    if (l.x[e] >= bound && l.x[e] > -INFINITY) {
-                        const int at = atomicAdd(count, 1);
-                        if (at < kList) list[at] = pack_key(l.x[e], (uint32_t)(id0 + i * kThreads * kN + e));
-                    }
-            }
-        };
         if (!slow) {
-            collect(listed_s);
-            __syncthreads();
-            listed = listed_s[0];
-            if (listed > kList) {
-                if (warp == 0) {
-                    const uint32_t g = group_bound(group_key, a.top);
-                    if (lane == 0) bound_s = max(bound_key, g);
+            if (r.m >= bound && r.m > -INFINITY) {
+#pragma unroll 1
+                for (int turn = 0; turn < turns; ++turn) {
+                    const float most = turn_max[turn * kThreads + tid];
+                    if (!(most >= bound) || most == -INFINITY) continue;
+                    load(x, turn);
+#pragma unroll
+                    for (int k = 0; k < kTurn; ++k) {
+                        const Logits<F32> l(x[k]);
+#pragma unroll
+                        for (int e = 0; e < kN; ++e)
+                            if (l.x[e] >= bound && l.x[e] > -INFINITY) {
+                                const int at = atomicAdd(&listed_s, 1);
+                                if (at < kList)
+                                    list[at] = pack_key(l.x[e], (uint32_t)(first_id + (turn * kTurnVectors + k * kThreads + tid) * kN + e));
+                            }
+                    }
                 }
-                __syncthreads();
-                bound_key = bound_s;
-                collect(listed_s + 1);
-                __syncthreads();
-                listed = listed_s[1];
-                slow = listed > kList;
             }
+            __syncthreads();
+            listed = listed_s;
+            slow = listed > kList;
         }
-        if (!slow && listed < a.top && key_from_ordered(bound_key) == -INFINITY) {
+        if (!slow && listed < a.top && bound == -INFINITY) {
             // masked ids follow by their number: those of the first 32 vectors are enough, or the slow way
             __syncthreads();                                           // listed_s is read
             if (warp == 0) {
                 uint32_t masked = 0;
-                const Logits<F32> l(x[0]);
+                const Logits<F32> l(load1(lane));
+                const int id = first_id + lane * kN;
 #pragma unroll
                 for (int e = 0; e < kN; ++e)
-                    if (lane < vectors && l.x[e] == -INFINITY && id0 + e >= 0 && id0 + e < a.vocab) masked |= 1u << e;
+                    if (lane < vectors && l.x[e] == -INFINITY && id + e >= 0 && id + e < a.vocab) masked |= 1u << e;
                 int at = __popc(masked);
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, at, o);
-                    if (lane >= o) at += y;
+                    const int n = __shfl_up_sync(0xffffffffu, at, o);
+                    if (lane >= o) at += n;
                 }
                 const int all = __shfl_sync(0xffffffffu, at, 31);
                 at -= __popc(masked);
 #pragma unroll
                 for (int e = 0; e < kN; ++e)
                     if (masked >> e & 1) {
-                        if (at < a.top) list[listed + at] = pack_key(-INFINITY, (uint32_t)(id0 + e));
+                        if (at < a.top) list[listed + at] = pack_key(-INFINITY, (uint32_t)(id + e));
                         ++at;
                     }
-                if (lane == 0) listed_s[0] = all >= a.top || vectors <= 32 ? listed + min(all, a.top) : kList + 1;
+                if (lane == 0) listed_s = all >= a.top || vectors <= 32 ? listed + min(all, a.top) : kList + 1;
             }
             __syncthreads();
-            listed = listed_s[0];
+            listed = listed_s;
             slow = listed > kList;
         }
         if (!slow) {
@@ -457,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
             }
             if (tid < a.top && tid >= listed) put(tid, 0);
         } else {
+            __syncthreads();                                           // the list is read
             uint64_t last = 1;
             for (int n = 0; n < a.top; ++n) {
                 uint64_t most = 0;
@@ -560,15 +594,18 @@ __global__ void __launch_bounds__(kThreads, N <= 8 ? 4 : N <= 17 ? 2 : 1) logpro
     }
 }
 
-// The vectors of a thread: up to 8 while the cluster can grow.
-constexpr int kFewVectors = 8;
+// Lets the kernels take what a call may need, once a device.
+constexpr int kMostShared = 80 << 10;     // 262144 fp32 logits: 65 turns of 1 KB
 
-template <bool F32>
-const void *kernel_for(int vectors) {
-    if (vectors <= 2) return (const void *)logprobs_kernel<F32, 2>;
-    if (vectors <= 8) return (const void *)logprobs_kernel<F32, 8>;
-    if (vectors <= 17) return (const void *)logprobs_kernel<F32, 17>;
-    return (const void *)logprobs_kernel<F32, 33>;                     // fp32 alone has as many
+bool allow_shared_memory(int device, int &multiprocessors) {
+    static std::atomic<int> known[64];
+    const bool kept = device < 64;
+    if (kept && (multiprocessors = known[device].load(std::memory_order_relaxed)) > 0) return true;
+    for (const void *fn : {(const void *)logprobs_kernel<false>, (const void *)logprobs_kernel<true>})
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared) != cudaSuccess) return false;
+    if (cudaDeviceGetAttribute(&multiprocessors, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) return false;
+    if (kept) known[device].store(multiprocessors, std::memory_order_relaxed);
+    return true;
 }
 
 }  // namespace
@@ -609,13 +646,20 @@ extern "C" markov_status markov_logprobs(const void *logits, markov_dtype dtype,
     a.top_logprobs = top_logprobs;
     a.ranks = ranks;
     a.top_ids = top_ids;
-    // whole vectors, the first of which may begin before the row
+    int multiprocessors = 0;
+    if (!allow_shared_memory(at.device, multiprocessors)) {
+        cudaGetLastError();
+        return MARKOV_ECUDA;
+    }
+    // whole vectors, the first of which may begin before the row; a cluster a row while
+    // its blocks find a place, four to a multiprocessor, and have a turn to do
     const int vectors = (int)(((int64_t)vocab * size + 15) / 16) + 1;
     int blocks = 1;
-    while (blocks < kMaxCluster && vectors > blocks * kFewVectors * kThreads) blocks *= 2;
+    while (blocks < kMaxCluster && (int64_t)rows * blocks * 2 <= 4 * multiprocessors && vectors > 2 * blocks * kTurn * kThreads)
+        blocks *= 2;
     a.slice = (vectors + blocks - 1) / blocks;
-    const int each = (a.slice + kThreads - 1) / kThreads;
-    const void *fn = f32 ? kernel_for<true>(each) : kernel_for<false>(each);
+    const int turns = (a.slice + kTurn * kThreads - 1) / (kTurn * kThreads);
+    const void *fn = f32 ? (const void *)logprobs_kernel<true> : (const void *)logprobs_kernel<false>;
     for (int32_t r0 = 0; r0 < rows; r0 += 65535) {
         LogprobArgs b = a;
         b.logits += r0 * a.s0;
@@ -632,6 +676,7 @@ extern "C" markov_status markov_logprobs(const void *logits, markov_dtype dtype,
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(blocks, rows - r0 < 65535 ? rows - r0 : 65535);
         cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = turns * kThreads * sizeof(float);
         cfg.stream = (cudaStream_t)stream;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
