@@ -175,7 +175,7 @@ cudaError_t launch_fetch_e4m3(const FetchArgs &a, int head_dim, bool f16, cudaSt
 cudaError_t attention_e4m3_few_prepare();
 size_t attention_e4m3_few_parts(int head_dim, int blocks);
 size_t attention_e4m3_few_joins(int blocks);
-// Calls of few query rows a request: k and v are maps of 16 slots by head_dim.
+// Calls of few query rows a request: k and v are maps of up to 32 slots by head_dim.
 cudaError_t launch_attention_e4m3_few(const AttnE4m3Args &a, const CUtensorMap &k, const CUtensorMap &v, int head_dim,
                                       bool f16, bool half, int blocks, cudaStream_t s);
 cudaError_t attention_e4m3_many_prepare();

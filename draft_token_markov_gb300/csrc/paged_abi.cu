@@ -525,7 +525,7 @@ markov_status markov_paged_attention_e4m3(
     const int64_t query_rows = (int64_t)num_tokens * group;
     const bool few = query_rows <= 16 * (int64_t)rows;
     CUtensorMap qmap, kmap, vmap;
-    const int slots = few ? 16 : 128;
+    const int slots = few ? 32 : 128;
     if (!encode_e4m3_map(&kmap, *k_cache, *p, slots) || !encode_e4m3_map(&vmap, *v_cache, *p, slots) ||
         (!few && !encode_query_map(&qmap, q, q_s0, q_s1, num_tokens, *p)))
         return MARKOV_EINVAL;

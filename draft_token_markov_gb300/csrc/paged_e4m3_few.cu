@@ -2,15 +2,15 @@
 // batch, short drafts) over a paged e4m3 cache: bound by the cache's bytes.
 //
 // A warp is a worker of its own: it has a range of the call's work, a ring of
-// shared memory that TMA fills with 16 keys and values at a time, and the running
+// shared memory that TMA fills with 32 keys and values at a time, and the running
 // softmax of the item it is at.  An item is (request, key head, 16 stacked query
 // rows: row = token * group + head, or 8 where a request has no more).
-//   S = Q K^T    m16n8k16 on fp16: two tiles of 8 keys, dims in any order as Q's
+//   S = Q K^T    m16n8k16 on fp16: four tiles of 8 keys, dims in any order as Q's
 //   m, p = 2^(y - m), y = S ks c + log2 vs, l += 2^(-log2 vs) sum p
 //   O += P V     the scores' registers are P's fragment
 // The scale of a value enters its weight, as an addition in the exponent, and is
 // taken out of the sum again; m is the maximum of y, which is what bounds p.  So a
-// block's scales cost a few instructions for 16 keys.  Keys and values go from
+// block's scales cost a few instructions for 16 keys, a scale's half step.  Keys and values go from
 // shared memory to registers once and become fp16 there (exact: e4m3 is a subset);
 // values in pairs of keys by byte permutes.  (Through tcgen05 they would be written
 // to shared memory as fp16 and read from there: 7 bytes of its traffic for each of
@@ -20,7 +20,7 @@
 // (kLazy), so that most steps need no exchange between lanes; weights are at most
 // 2^(kShift + kLazy) = 2^15.
 //
-// Work.  An item weighs one for each of its steps of 16 keys and kEnds for its
+// Work.  An item weighs one for each of its steps of 32 keys and kEnds for its
 // start and end; items lie end to end in order of request, key head and rows, and
 // the whole is cut into one range of equal weight a warp.  A cut item leaves its
 // parts in the plan's scratch, which a second launch joins.
@@ -37,17 +37,17 @@
 
 namespace dtm {
 
-constexpr int kFewWarps = 12;
+constexpr int kFewWarps = 8;
 constexpr int kFewThreads = kFewWarps * 32;
-constexpr int kStep = 16;                    // keys of a step
-constexpr int kStepShift = 4;
-constexpr int kEnds = 6;                     // an item's start and end, in steps
-constexpr int kLeast = 10;                   // units of a range
+constexpr int kStep = 32;                    // keys of a step, in two halves of 16
+constexpr int kStepShift = 5;
+constexpr int kEnds = 3;                     // an item's start and end, in steps
+constexpr int kLeast = 3;                    // units of a range
 
 template <int D>
 struct FewShape {
     static constexpr int kSide = kStep * D;                  // bytes of a step's keys or values
-    static constexpr int kStages = D == 128 ? 4 : 8;
+    static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kRing = 2 * kSide * kStages;        // of a warp
     static constexpr int kBars = kFewWarps * kRing;
     static constexpr int kAborts = kBars + 8 * kFewWarps * kStages;
@@ -183,7 +183,7 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         total += x * a.kv_heads;
     }
-    if (total >> 34) {                                       // 2^31 tiles of 128 keys
+    if (total >> 33) {                                       // 2^31 tiles of 128 keys
         if (tid == 0 && !pending) set_status(a.status, 2u /* MARKOV_EUNSUPPORTED */, 0x700);
         total = 0;
     }
@@ -236,7 +236,8 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
     }
 
     // -------------------------------------------------------------- items
-    uint32_t filled = 0, taken = 0;                          // steps loaded and used; stage and phase follow
+    // the next stages to load and to use, the latter's phase, and how many so far
+    uint32_t fill = 0, use = 0, use_phase = 0, loaded = 0, used = 0;
     bool ok = true;
     // the step of an offset within an item's units
     const auto step_at = [&](uint64_t off, int all) { return off <= kEnds ? 0 : (int)min(off - kEnds, (uint64_t)all); };
@@ -261,37 +262,50 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
                 c0 = split.range_of(u + kEnds);              // the range that has the first step's unit
                 c1 = split.range_of(u + units - 1);
             }
-            // page and scales of 32 steps, a lane each, and of the next 32
+            // page and scales of 16 steps, a lane a half, and of the next 16
             int pid = -1, pid_next = -1;
-            float ks = 1.0f, vs = 1.0f, ks_next = 1.0f, vs_next = 1.0f;
-            const auto look = [&](int j, int &pid, float &ks, float &vs) {
+            float ks = 1.0f, lv = 0.0f, ks_next = 1.0f, lv_next = 0.0f;
+            const bool pairs = a.r.page_shift >= kStepShift;         // a step's keys lie in one page
+            const auto seen = [&](int key, int n) {
+                return key < it.keys.end && (key + n > it.keys.first || key < it.keys.kept);
+            };
+            const auto look = [&](int j, int &pid, float &ks, float &lv) {
                 pid = -1;
-                ks = vs = 1.0f;
+                ks = 1.0f;
+                lv = 0.0f;
+                j += lane >> 1;
                 if (j >= steps) return;
-                const int key = it.keys.key<kStepShift>(j);
-                const int id = __ldg(a.r.table + it.state * a.r.table_s0 + (key >> a.r.page_shift));
+                const int key0 = it.keys.key<kStepShift>(j), key = key0 + 16 * (lane & 1);
+                if (!(pairs || seen(key, 16))) return;
+                const int id = __ldg(a.r.table + it.state * a.r.table_s0 + (key0 + (pairs ? 0 : 16 * (lane & 1)) >> a.r.page_shift));
                 if (id < 0 || id >= a.r.num_pages) return;
                 pid = id;
+                if (!seen(key, 16)) return;
                 const int slot = key & ((1 << a.r.page_shift) - 1);
                 ks = __ldg(a.ks.p + id * a.ks.s_page + (slot >> a.ks.block_shift) * a.ks.s_block + h * a.ks.s_head);
-                vs = __ldg(a.vs.p + id * a.vs.s_page + (slot >> a.vs.block_shift) * a.vs.s_block + h * a.vs.s_head);
+                lv = scale_log2(__ldg(a.vs.p + id * a.vs.s_page + (slot >> a.vs.block_shift) * a.vs.s_block + h * a.vs.s_head));
             };
-            look(j0 + lane, pid, ks, vs);
-            look(j0 + 32 + lane, pid_next, ks_next, vs_next);
+            look(j0, pid, ks, lv);
+            look(j0 + 16, pid_next, ks_next, lv_next);
             int jb = j0;                                     // the step of lane 0
             int issued = j0;
             const auto issue = [&]() {
-                const int off = issued - jb;
-                const int id = __shfl_sync(0xffffffffu, off < 32 ? pid : pid_next, off & 31);
-                const uint32_t stage = filled % S::kStages;
+                const int off = 2 * (issued - jb);
+                const int ids = off < 32 ? pid : pid_next;
+                const int id0 = __shfl_sync(0xffffffffu, ids, off & 31), id1 = __shfl_sync(0xffffffffu, ids, off + 1 & 31);
                 if (lane == 0) {
-                    const uint32_t bar = bars + 8 * stage, dst = ring + stage * 2 * S::kSide;
+                    const uint32_t bar = bars + 8 * fill, dst = ring + fill * 2 * S::kSide;
                     const int slot = it.keys.key<kStepShift>(issued) & ((1 << a.r.page_shift) - 1);
                     tc::mbar_expect_tx(bar, 2 * S::kSide);
-                    tma_load_4d(dst, &kmap, 0, slot, h, id, bar);
-                    tma_load_4d(dst + S::kSide, &vmap, 0, slot, h, id, bar);
+                    tma_load_4d(dst, &kmap, 0, slot, h, id0, bar);
+                    tma_load_4d(dst + S::kSide, &vmap, 0, slot, h, id0, bar);
+                    if (!pairs) {
+                        tma_load_4d(dst + S::kSide / 2, &kmap, 0, slot, h, id1, bar);
+                        tma_load_4d(dst + S::kSide + S::kSide / 2, &vmap, 0, slot, h, id1, bar);
+                    }
                 }
-                ++filled;
+                if (++fill == S::kStages) fill = 0;
+                ++loaded;
                 ++issued;
                 __syncwarp();
             };
@@ -312,117 +326,116 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
             const int whole_first = window_start(a.window, it.pos0 + (it.row0 + it.rows - 1) / a.group);
 #pragma unroll 1
             for (int j = j0; j < steps; ++j) {
-                if (j - jb == 32) {
+                if (j - jb == 16) {
                     jb = j;
                     pid = pid_next;
                     ks = ks_next;
-                    vs = vs_next;
-                    look(j + 32 + lane, pid_next, ks_next, vs_next);
+                    lv = lv_next;
+                    look(j + 16, pid_next, ks_next, lv_next);
                 }
-                const float ks_j = __shfl_sync(0xffffffffu, ks, j - jb), lv = scale_log2(__shfl_sync(0xffffffffu, vs, j - jb));
-                const float iv = ex2(-lv);
-                const uint32_t stage = taken % S::kStages, bar = bars + 8 * stage, parity = taken / S::kStages & 1;
-                if (!__all_sync(0xffffffffu, tc::mbar_test(bar, parity)))
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait_or_abort(bar, parity, 0x710, a.timeout_ns, abort_s + warp));
+                float ks_j[2], lv_j[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    ks_j[f] = __shfl_sync(0xffffffffu, ks, 2 * (j - jb) + f);
+                    lv_j[f] = __shfl_sync(0xffffffffu, lv, 2 * (j - jb) + f);
+                }
+                const uint32_t bar = bars + 8 * use;
+                if (!__all_sync(0xffffffffu, tc::mbar_test(bar, use_phase)))
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait_or_abort(bar, use_phase, 0x710, a.timeout_ns, abort_s + warp));
                 if (!ok) break;
-                ++taken;
-                const uint32_t kst = ring + stage * 2 * S::kSide, vst = kst + S::kSide;
+                const uint32_t kst = ring + use * 2 * S::kSide, vst = kst + S::kSide;
+                if (++use == S::kStages) {
+                    use = 0;
+                    use_phase ^= 1;
+                }
+                ++used;
                 const int key0 = it.keys.key<kStepShift>(j);
                 // ------------------------------------------------ S = Q K^T
-                float sc[2][4];
-                if (D == 128) {
-                    uint4 w[2][2];
+                float sc[4][4];
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 4; ++n) {
+                    sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+                    uint4 w[D / 64];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) w[n][i] = lds128(kst + n * 1024 + g * 128 + (((2 * q + i) ^ g) << 4));
+                    for (int i = 0; i < D / 64; ++i)
+                        w[i] = D == 128 ? lds128(kst + n * 1024 + g * 128 + (((2 * q + i) ^ g) << 4))
+                                        : lds128(kst + n * 512 + g * 64 + ((q ^ (g >> 1)) << 4));
 #pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
-#pragma unroll
-                        for (int s = 0; s < kSteps; ++s) {
-                            const uint4 &x = w[n][s / 4];
-                            uint32_t b0, b1;
-                            f16x4_of_e4m3((s & 3) == 0 ? x.x : (s & 3) == 1 ? x.y : (s & 3) == 2 ? x.z : x.w, b0, b1);
-                            mma_f16(sc[n], qf.lo[s][0], HALF ? 0u : qf.hi[HALF ? 0 : s][0], qf.lo[s][1],
-                                    HALF ? 0u : qf.hi[HALF ? 0 : s][1], b0, b1);
-                        }
-                    }
-                } else {
-                    uint4 w[2];
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) w[n] = lds128(kst + n * 512 + g * 64 + ((q ^ (g >> 1)) << 4));
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
-#pragma unroll
-                        for (int s = 0; s < kSteps; ++s) {
-                            const uint4 &x = w[n];
-                            uint32_t b0, b1;
-                            f16x4_of_e4m3((s & 3) == 0 ? x.x : (s & 3) == 1 ? x.y : (s & 3) == 2 ? x.z : x.w, b0, b1);
-                            mma_f16(sc[n], qf.lo[s][0], HALF ? 0u : qf.hi[HALF ? 0 : s][0], qf.lo[s][1],
-                                    HALF ? 0u : qf.hi[HALF ? 0 : s][1], b0, b1);
-                        }
+                    for (int s = 0; s < kSteps; ++s) {
+                        const uint4 &x = w[s / 4];
+                        uint32_t b0, b1;
+                        f16x4_of_e4m3((s & 3) == 0 ? x.x : (s & 3) == 1 ? x.y : (s & 3) == 2 ? x.z : x.w, b0, b1);
+                        mma_f16(sc[n], qf.lo[s][0], HALF ? 0u : qf.hi[HALF ? 0 : s][0], qf.lo[s][1],
+                                HALF ? 0u : qf.hi[HALF ? 0 : s][1], b0, b1);
                     }
                 }
                 // ---------------------------------------------------- values
-                // word w of the four keys' dims: keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9
-                uint32_t va[kTiles / 4], vb[kTiles / 4], vc[kTiles / 4], vd[kTiles / 4];
-                if (D == 128) {
-                    const uint32_t even = vst + q * 256 + ((g ^ (2 * q)) << 4), odd = vst + q * 256 + 128 + ((g ^ (2 * q + 1)) << 4);
-                    *reinterpret_cast<uint4 *>(va) = lds128(even);
-                    *reinterpret_cast<uint4 *>(vb) = lds128(odd);
-                    *reinterpret_cast<uint4 *>(vc) = lds128(even + 1024);
-                    *reinterpret_cast<uint4 *>(vd) = lds128(odd + 1024);
-                } else {
-                    const uint32_t even = vst + q * 128 + (((g >> 1) ^ q) << 4) + (g & 1) * 8;
-                    *reinterpret_cast<uint2 *>(va) = lds64(even);
-                    *reinterpret_cast<uint2 *>(vb) = lds64(even + 64);
-                    *reinterpret_cast<uint2 *>(vc) = lds64(even + 512);
-                    *reinterpret_cast<uint2 *>(vd) = lds64(even + 576);
+                // of each half, word w of four keys' dims: keys 2 q, 2 q + 1, 2 q + 8, 2 q + 9
+                uint32_t v[2][4][kTiles / 4];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const uint32_t at = vst + f * (S::kSide / 2);
+                    if (D == 128) {
+                        const uint32_t even = at + q * 256 + ((g ^ (2 * q)) << 4), odd = at + q * 256 + 128 + ((g ^ (2 * q + 1)) << 4);
+                        *reinterpret_cast<uint4 *>(v[f][0]) = lds128(even);
+                        *reinterpret_cast<uint4 *>(v[f][1]) = lds128(odd);
+                        *reinterpret_cast<uint4 *>(v[f][2]) = lds128(even + 1024);
+                        *reinterpret_cast<uint4 *>(v[f][3]) = lds128(odd + 1024);
+                    } else {
+                        const uint32_t even = at + q * 128 + (((g >> 1) ^ q) << 4) + (g & 1) * 8;
+                        *reinterpret_cast<uint2 *>(v[f][0]) = lds64(even);
+                        *reinterpret_cast<uint2 *>(v[f][1]) = lds64(even + 64);
+                        *reinterpret_cast<uint2 *>(v[f][2]) = lds64(even + 512);
+                        *reinterpret_cast<uint2 *>(v[f][3]) = lds64(even + 576);
+                    }
                 }
                 __syncwarp();                                // the stage is read
                 if (issued < steps) issue();
-                // values that nobody sees can be anything: zeros
-                const int end = it.keys.end, first = it.keys.first, kept = it.keys.kept;
-                if (key0 + kStep > end || (key0 < first && key0 + kStep > kept)) {
-                    const auto unseen = [&](int k) { return k >= end || (k < first && k >= kept); };
-                    const int k = key0 + 2 * q;
-#pragma unroll
-                    for (int i = 0; i < kTiles / 4; ++i) {
-                        if (unseen(k)) va[i] = 0;
-                        if (unseen(k + 1)) vb[i] = 0;
-                        if (unseen(k + 8)) vc[i] = 0;
-                        if (unseen(k + 9)) vd[i] = 0;
-                    }
-                }
                 // --------------------------------------------------- softmax
-                const bool edge = key0 + kStep > whole_end || (key0 < whole_first && key0 + kStep > a.sinks);
-                float y[kHalves][4];
+                float y[kHalves][8];
+#pragma unroll
+                for (int x = 0; x < kHalves; ++x)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {
+                        const float c = qf.c[x] * ks_j[f];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[x][4 * f + e] = fmaf(sc[2 * f + (e >> 1)][2 * x + (e & 1)], c, lv_j[f]);
+                    }
+                if (key0 + kStep > whole_end || (key0 < whole_first && key0 + kStep > a.sinks)) {
+                    // values that nobody sees can be anything: zeros
+                    const int end = it.keys.end, first = it.keys.first, kept = it.keys.kept;
+#pragma unroll
+                    for (int f = 0; f < 2; ++f)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = key0 + 16 * f + (e >> 1) * 8 + 2 * q + (e & 1);
+                            if (k >= end || (k < first && k >= kept)) {
+#pragma unroll
+                                for (int i = 0; i < kTiles / 4; ++i) v[f][e][i] = 0;
+                            }
+#pragma unroll
+                            for (int x = 0; x < kHalves; ++x) {
+                                const bool sees = k <= pos[x] && k < a.r.room && (k >= window_start(a.window, pos[x]) || k < a.sinks);
+                                if (!sees) y[x][4 * f + e] = -INFINITY;
+                            }
+                        }
+                }
                 bool grow = false;
+                float top[kHalves];
 #pragma unroll
                 for (int x = 0; x < kHalves; ++x) {
-                    const float c = qf.c[x] * ks_j;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[x][e] = fmaf(sc[e >> 1][2 * x + (e & 1)], c, lv);
-                        if (edge) {
-                            const int k = key0 + (e >> 1) * 8 + 2 * q + (e & 1);
-                            const bool seen = k <= pos[x] && k < a.r.room && (k >= window_start(a.window, pos[x]) || k < a.sinks);
-                            if (!seen) y[x][e] = -INFINITY;
-                        }
-                    }
-                    grow |= fmaxf(fmaxf(y[x][0], y[x][1]), fmaxf(y[x][2], y[x][3])) > M[x] + kLazyE4;
+                    top[x] = fmaxf(fmaxf(fmaxf(y[x][0], y[x][1]), fmaxf(y[x][2], y[x][3])),
+                                   fmaxf(fmaxf(y[x][4], y[x][5]), fmaxf(y[x][6], y[x][7])));
+                    grow |= top[x] > M[x] + kLazyE4;
                 }
                 if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                     for (int x = 0; x < kHalves; ++x) {
-                        float top = fmaxf(fmaxf(y[x][0], y[x][1]), fmaxf(y[x][2], y[x][3]));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                        if (top > M[x]) {
-                            const float f = M[x] == -INFINITY ? 0.0f : ex2(M[x] - top);
-                            M[x] = top;
+                        float most = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], 1));
+                        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                        if (most > M[x]) {
+                            const float f = M[x] == -INFINITY ? 0.0f : ex2(M[x] - most);
+                            M[x] = most;
                             l[x] *= f;
 #pragma unroll
                             for (int i = 0; i < kTiles; ++i) {
@@ -432,26 +445,34 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
                         }
                     }
                 }
-                uint32_t p[4] = {0, 0, 0, 0};
+                uint32_t p[2][4];
 #pragma unroll
-                for (int x = 0; x < kHalves; ++x) {
-                    const float b = M[x] == -INFINITY ? 0.0f : kShiftE4 - M[x];
-                    const float p0 = ex2(y[x][0] + b), p1 = ex2(y[x][1] + b), p2 = ex2(y[x][2] + b), p3 = ex2(y[x][3] + b);
-                    l[x] = fmaf((p0 + p1) + (p2 + p3), iv, l[x]);
-                    p[x] = pack2<true>(p0, p1);
-                    p[2 + x] = pack2<true>(p2, p3);
+                for (int f = 0; f < 2; ++f) {
+                    const float iv = ex2(-lv_j[f]);
+                    p[f][1] = p[f][3] = 0;
+#pragma unroll
+                    for (int x = 0; x < kHalves; ++x) {
+                        const float b = M[x] == -INFINITY ? 0.0f : kShiftE4 - M[x];
+                        const float p0 = ex2(y[x][4 * f] + b), p1 = ex2(y[x][4 * f + 1] + b), p2 = ex2(y[x][4 * f + 2] + b),
+                                    p3 = ex2(y[x][4 * f + 3] + b);
+                        l[x] = fmaf((p0 + p1) + (p2 + p3), iv, l[x]);
+                        p[f][x] = pack2<true>(p0, p1);
+                        p[f][2 + x] = pack2<true>(p2, p3);
+                    }
                 }
                 // ------------------------------------------------ O += P V
 #pragma unroll
-                for (int i = 0; i < kTiles / 4; ++i) {
-                    uint32_t b[4], d[4];
-                    f16x4_of_e4m3(__byte_perm(va[i], vb[i], 0x5140), b[0], b[1]);
-                    f16x4_of_e4m3(__byte_perm(va[i], vb[i], 0x7362), b[2], b[3]);
-                    f16x4_of_e4m3(__byte_perm(vc[i], vd[i], 0x5140), d[0], d[1]);
-                    f16x4_of_e4m3(__byte_perm(vc[i], vd[i], 0x7362), d[2], d[3]);
+                for (int f = 0; f < 2; ++f)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) mma_f16(o[4 * i + e], p[0], p[1], p[2], p[3], b[e], d[e]);
-                }
+                    for (int i = 0; i < kTiles / 4; ++i) {
+                        uint32_t b[4], d[4];
+                        f16x4_of_e4m3(__byte_perm(v[f][0][i], v[f][1][i], 0x5140), b[0], b[1]);
+                        f16x4_of_e4m3(__byte_perm(v[f][0][i], v[f][1][i], 0x7362), b[2], b[3]);
+                        f16x4_of_e4m3(__byte_perm(v[f][2][i], v[f][3][i], 0x5140), d[0], d[1]);
+                        f16x4_of_e4m3(__byte_perm(v[f][2][i], v[f][3][i], 0x7362), d[2], d[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) mma_f16(o[4 * i + e], p[f][0], p[f][1], p[f][2], p[f][3], b[e], d[e]);
+                    }
             }
             if (!ok) break;
             // ------------------------------------------------------- the end
@@ -516,8 +537,13 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
         // gave up: no load may be in flight when the block leaves
         set_status(a.status, 4u /* MARKOV_ETIMEOUT */, abort_s[warp]);
         const uint64_t until = tc::now_ns() + a.timeout_ns;
-        for (; taken != filled; ++taken)
-            while (!tc::mbar_test(bars + 8 * (taken % S::kStages), taken / S::kStages & 1) && tc::now_ns() < until) {}
+        for (; used != loaded; ++used) {
+            while (!tc::mbar_test(bars + 8 * use, use_phase) && tc::now_ns() < until) {}
+            if (++use == S::kStages) {
+                use = 0;
+                use_phase ^= 1;
+            }
+        }
     }
 }
 
