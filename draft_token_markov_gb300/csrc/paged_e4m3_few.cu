@@ -21,9 +21,12 @@
 // 2^(kShift + kLazy) = 2^15.
 //
 // Work.  An item weighs one for each of its steps of 32 keys and kEnds for its
-// start and end; items lie end to end in order of request, key head and rows, and
-// the whole is cut into one range of equal weight a warp.  A cut item leaves its
-// parts in the plan's scratch, which a second launch joins.
+// start and end.  Neighbouring warps have neighbouring key heads (as many as the
+// largest power of two up to 8 that divides their number) of the same keys, whose
+// bytes lie side by side in a cache with the heads inside a slot: such a lane of
+// heads has the items of the call end to end, in order of request, group of heads and
+// rows, cut into ranges of equal weight, one a warp.  A cut item leaves its parts in
+// the plan's scratch, which a second launch joins.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -41,8 +44,8 @@ constexpr int kFewWarps = 8;
 constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kStep = 32;                    // keys of a step, in two halves of 16
 constexpr int kStepShift = 5;
-constexpr int kEnds = 3;                     // an item's start and end, in steps
-constexpr int kLeast = 3;                    // units of a range
+constexpr int kEnds = 2;                     // an item's start and end, in steps
+constexpr int kLeast = 2;                    // units of a range
 
 template <int D>
 struct FewShape {
@@ -62,7 +65,8 @@ struct FewItem {
 };
 
 struct FewJoin {
-    int c0, c1;                // workers that share the item (c0 == c1: none)
+    int c0, c1;                // workers that share the item, every `step`-th (c0 == c1: none)
+    int step;
     int qs, head0, row0, rows;
 };
 
@@ -159,7 +163,10 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
     }
     __syncwarp();
     const uint32_t pending = __ldcg(a.status);
-    const int worker = blockIdx.x * kFewWarps + warp, workers = gridDim.x * kFewWarps;
+    const int lanes = min(a.kv_heads & -a.kv_heads, kFewWarps), head_groups = a.kv_heads / lanes;
+    // ranges go round the blocks, so that a small call is spread
+    const int range = warp / lanes * gridDim.x + blockIdx.x, head_lane = warp % lanes;
+    const int worker = range * lanes + head_lane, ranges = gridDim.x * (kFewWarps / lanes);
 
     // ---------------------------------------------------------- the range
     const auto span = [&](const RowOfCall &r, int m) {
@@ -174,26 +181,26 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
         for (int m = 0; m < n; ++m) x += kEnds + max(span(r, m).steps, 1);
         return x;
     };
-    FewJoin join{0, 0, 0, 0, 0, 0};
+    FewJoin join{0, 0, 0, 0, 0, 0, 0};
     uint64_t total = 0;
 #pragma unroll 1
     for (int r0 = 0; r0 < a.r.rows; r0 += 32) {
         uint64_t x = r0 + lane < a.r.rows ? units_of(row_of_call(a.r, r0 + lane)) : 0;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        total += x * a.kv_heads;
+        total += x;
     }
-    if (total >> 33) {                                       // 2^31 tiles of 128 keys
+    if (total * a.kv_heads >> 33) {                          // 2^31 tiles of 128 keys
         if (tid == 0 && !pending) set_status(a.status, 2u /* MARKOV_EUNSUPPORTED */, 0x700);
         total = 0;
     }
     UnitSplit split;
-    split.cut(pending ? 0 : total, workers, kLeast);
-    if (worker >= split.ranges) {
+    split.cut(pending ? 0 : total * head_groups, ranges, kLeast);
+    if (range >= split.ranges) {
         if (lane == 0) reinterpret_cast<FewJoin *>(a.joins)[worker] = join;
         return;
     }
-    const uint64_t u0 = split.first(worker), u_end = split.first(worker + 1);
+    const uint64_t u0 = split.first(range), u_end = split.first(range + 1);
     uint64_t u = 0;                                          // the current item's first unit
     int r = 0;
     RowOfCall row;
@@ -201,7 +208,7 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
     for (int r0 = 0;; r0 += 32) {
         RowOfCall mine{0, 0, 0, -1};
         if (r0 + lane < a.r.rows) mine = row_of_call(a.r, r0 + lane);
-        const uint64_t own = units_of(mine) * a.kv_heads;
+        const uint64_t own = units_of(mine) * head_groups;
         uint64_t incl = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -222,11 +229,11 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
         }
         u = __shfl_sync(0xffffffffu, incl, 31);
     }
-    int tiles = tiles_of(row), m = 0, h;
+    int tiles = tiles_of(row), m = 0, hg;                    // hg: group of key heads
     {
         const uint64_t head = units_of(row);
-        h = (int)((u0 - u) / head);
-        u += h * head;
+        hg = (int)((u0 - u) / head);
+        u += hg * head;
 #pragma unroll 1
         for (;; ++m) {
             const uint32_t units = kEnds + max(span(row, m).steps, 1);
@@ -243,6 +250,7 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
     const auto step_at = [&](uint64_t off, int all) { return off <= kEnds ? 0 : (int)min(off - kEnds, (uint64_t)all); };
 #pragma unroll 1
     while (ok && u < u_end) {
+        const int h = hg * lanes + head_lane;
         FewItem it;
         it.qs = row.qs;
         it.head0 = h * a.group;
@@ -257,7 +265,7 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
         const int j0 = u0 > u ? step_at(u0 - u, all) : 0, j1 = u_end - u < units ? step_at(u_end - u, all) : all;
         if (j0 < j1) {
             const int steps = min(j1, it.keys.steps);        // its share: steps [j0, steps)
-            int c0 = worker, c1 = worker;
+            int c0 = range, c1 = range;
             if (j0 > 0 || j1 < all) {
                 c0 = split.range_of(u + kEnds);              // the range that has the first step's unit
                 c1 = split.range_of(u + units - 1);
@@ -477,7 +485,8 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
             if (!ok) break;
             // ------------------------------------------------------- the end
             const bool split_item = c0 != c1;
-            if (split_item && c0 == worker) join = FewJoin{c0, c1, it.qs, it.head0, it.row0, it.rows};
+            if (split_item && c0 == range)
+                join = FewJoin{worker, c1 * lanes + head_lane, lanes, it.qs, it.head0, it.row0, it.rows};
 #pragma unroll
             for (int x = 0; x < kHalves; ++x) {
                 float sum = l[x];
@@ -487,7 +496,7 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
                 if (rr >= it.rows) continue;
                 // the lane's columns: D / 4 from q D / 4 on, the tiles' even columns first
                 if (split_item) {
-                    float *part = few_part<D>(a, worker, c0 == worker);
+                    float *part = few_part<D>(a, worker, c0 == range);
                     float4 *to = reinterpret_cast<float4 *>(part + rr * D + q * (D / 4));
 #pragma unroll
                     for (int i = 0; i < D / 16; ++i) {
@@ -521,8 +530,8 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
         u += units;
         if (++m == tiles) {
             m = 0;
-            if (++h == a.kv_heads) {
-                h = 0;
+            if (++hg == head_groups) {
+                hg = 0;
                 if (u < u_end) {
                     do {
                         row = row_of_call(a.r, ++r);
@@ -562,15 +571,16 @@ __global__ void __launch_bounds__(kFewJoinThreads) few_join_kernel(const __grid_
         const int r = i / (D / 4), k = i % (D / 4);
         float M = -INFINITY, L = 0.0f;
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int b0 = j.c0; b0 <= j.c1; b0 += 4) {
+        for (int b0 = j.c0; b0 <= j.c1; b0 += 4 * j.step) {
             float pm[4], pl[4], mn = M;
             float4 y[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 pm[e] = -INFINITY;
                 pl[e] = 0.0f;
-                if (b0 + e > j.c1) continue;
-                const float *p = few_part<D>(a, b0 + e, b0 + e == j.c0);
+                const int b = b0 + e * j.step;
+                if (b > j.c1) continue;
+                const float *p = few_part<D>(a, b, b == j.c0);
                 pm[e] = __ldcg(p + 16 * D + r);
                 pl[e] = __ldcg(p + 16 * D + 16 + r);
                 y[e] = __ldcg(reinterpret_cast<const float4 *>(p + r * D) + k);
@@ -583,7 +593,7 @@ __global__ void __launch_bounds__(kFewJoinThreads) few_join_kernel(const __grid_
             o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (b0 + e > j.c1 || pm[e] == -INFINITY) continue;
+                if (b0 + e * j.step > j.c1 || pm[e] == -INFINITY) continue;
                 const float w = ex2(pm[e] - M);
                 L = fmaf(pl[e], w, L);
                 o = make_float4(fmaf(y[e].x, w, o.x), fmaf(y[e].y, w, o.y), fmaf(y[e].z, w, o.z), fmaf(y[e].w, w, o.w));
