@@ -42,12 +42,16 @@ constexpr int kStoreThreads = 128;
 constexpr int kHeld = 8;
 constexpr int kMostChunk = 256;              // tokens of a chunk: a cache block at most
 
-// x / s, rounded: by its reciprocal where that is exact (s a power of two).
+// x / s, rounded.
+__device__ __noinline__ uint2 divide8(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7, float s) {
+    return make_uint2(e4m3_of_f32(__fdiv_rn(x0, s), __fdiv_rn(x1, s), __fdiv_rn(x2, s), __fdiv_rn(x3, s)),
+                      e4m3_of_f32(__fdiv_rn(x4, s), __fdiv_rn(x5, s), __fdiv_rn(x6, s), __fdiv_rn(x7, s)));
+}
+// By its reciprocal where that is exact (s a power of two; inv is 0 elsewhere).
 __device__ __forceinline__ uint2 round8(const float (&x)[8], float s, float inv) {
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = inv != 0.0f ? x[i] * inv : __fdiv_rn(x[i], s);
-    return make_uint2(e4m3_of_f32(y[0], y[1], y[2], y[3]), e4m3_of_f32(y[4], y[5], y[6], y[7]));
+    if (inv == 0.0f) return divide8(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], s);
+    return make_uint2(e4m3_of_f32(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv),
+                      e4m3_of_f32(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv));
 }
 
 // 1 / s where it is exact and normal, else 0.
@@ -56,27 +60,27 @@ __device__ __forceinline__ float exact_inverse(float s) {
     return (b & 0x7fffffu) == 0u && e >= 1u && e <= 252u ? __uint_as_float((254u - e) << 23) : 0.0f;
 }
 
+// The larger magnitudes of two pairs of 16-bit floats, as their bits.
+__device__ __forceinline__ uint32_t larger_magnitudes(uint32_t a, uint32_t b) {
+    return __vmaxu2(a, b & 0x7fff7fffu);
+}
+
 template <int D, bool F16, bool KEEP>
-__global__ void __launch_bounds__(kStoreThreads, 5) store_e4m3_kernel(const __grid_constant__ StoreArgs a) {
-    if (__ldcg(a.status) != 0u) return;
+__global__ void __launch_bounds__(kStoreThreads, 7) store_e4m3_kernel(const __grid_constant__ StoreArgs a) {
     constexpr int kLanes = D / 8, kTokens = kStoreThreads / kLanes;     // threads of a token, tokens of a turn
-    __shared__ uint32_t top_s[kStoreThreads / 32];
+    const uint32_t pending = __ldcg(a.status);                          // nothing is written then
     const int tid = threadIdx.x, lane = tid & 31, sub = tid / kLanes, vec = tid % kLanes;
     const StoreSide &side = a.side[blockIdx.z];
     const E4m3Side &c = side.cache;
     const int head = blockIdx.y, t_first = blockIdx.x * a.chunk, t_last = min(t_first + a.chunk, a.T);
+    const int in_block = (1 << c.block_shift) - 1;
     const int64_t in_page = (1 << a.page_shift) - 1;
     const auto slot_at = [&](int t) {
         const int64_t s = t >= 0 && t < a.T ? __ldg(a.slots + t) : -1;
         return s >= 0 && s < a.num_slots ? s : (int64_t)-1;
     };
-    const auto load = [&](int t) { return __ldcs(side.src + t * side.src_s0 + head * side.src_s1 + vec); };
-    const auto store = [&](int64_t slot, const uint4 &v, float s, float inv) {
-        float x[8];
-        unpack8<F16>(v, x);
-        uint8_t *to = c.data + (slot >> a.page_shift) * c.s_page + (slot & in_page) * c.s_slot + head * c.s_head + 8 * vec;
-        *reinterpret_cast<uint2 *>(to) = round8(x, s, inv);
-    };
+    const uint4 *src = side.src + head * side.src_s1 + vec;
+    const auto load = [&](int t) { return __ldcs(src + t * side.src_s0); };
     const auto scale_at = [&](int64_t slot) {
         return c.scales + (slot >> a.page_shift) * c.ss_page + ((slot & in_page) >> c.block_shift) * c.ss_block +
                head * c.ss_head;
@@ -84,91 +88,122 @@ __global__ void __launch_bounds__(kStoreThreads, 5) store_e4m3_kernel(const __gr
     if (KEEP) {
         for (int t = t_first + sub; t < t_last; t += kTokens) {
             const int64_t slot = slot_at(t);
-            if (slot < 0) continue;
+            if (slot < 0 || pending) continue;
             const float s = __ldg(scale_at(slot));
-            store(slot, load(t), s, exact_inverse(s));
+            float x[8];
+            unpack8<F16>(load(t), x);
+            uint8_t *to = c.data + (slot >> a.page_shift) * c.s_page + (slot & in_page) * c.s_slot + head * c.s_head + 8 * vec;
+            *reinterpret_cast<uint2 *>(to) = round8(x, s, exact_inverse(s));
         }
         return;
     }
-    // bit i: token t_first + i is of another cache block than the one before it, and
-    // (first_s) is one of the cache's
-    __shared__ uint32_t breaks_s[kMostChunk / 16], first_s[kMostChunk / 32];
+    // of token t_first + i: its place in its cache block, and bits: whether its block is
+    // another than the token's before, whether (of the chunk) it is one of the cache's
+    // with that, whether its place is the block's first
+    __shared__ uint8_t place_s[2 * kMostChunk];
+    __shared__ uint32_t breaks_s[kMostChunk / 16], begins_s[kMostChunk / 32], first_s[kMostChunk / 16];
+    __shared__ uint32_t top_s[kStoreThreads / 32];
     // a run is a cache block's tokens at most, as a rule
-    const int window = (a.chunk + (1 << c.block_shift) + 31) & ~31;
+    const int window = (a.chunk + in_block + 1 + 31) & ~31;
     for (int i = tid; i < window; i += kStoreThreads) {
-        const int64_t s = slot_at(t_first + i), before = slot_at(t_first + i - 1);
+        const int64_t s = slot_at(t_first + i);
+        int64_t before = __shfl_up_sync(0xffffffffu, s, 1);
+        if (lane == 0) before = slot_at(t_first + i - 1);
         const bool breaks = s < 0 || before < 0 || s >> c.block_shift != before >> c.block_shift;
-        const uint32_t b = __ballot_sync(0xffffffffu, breaks), f = __ballot_sync(0xffffffffu, breaks && s >= 0);
+        const uint32_t b = __ballot_sync(0xffffffffu, breaks), n = __ballot_sync(0xffffffffu, breaks && s >= 0),
+                       f = __ballot_sync(0xffffffffu, s >= 0 && (s & in_block) == 0);
+        place_s[i] = (uint8_t)(s & in_block);
         if (lane == 0) {
             breaks_s[i >> 5] = b;
-            if (i < a.chunk) first_s[i >> 5] = f;
+            first_s[i >> 5] = f;
+            if (i < a.chunk) begins_s[i >> 5] = n;
         }
     }
     __syncthreads();
+    if (pending) return;
     // the first break from token i of the window on; past the window the slots are looked at
     const auto run_end = [&](int i) {
         for (; i < window; i = (i | 31) + 1) {
             const uint32_t b = breaks_s[i >> 5] >> (i & 31);
-            if (b) {
-                i += __ffs(b) - 1;
-                break;
-            }
+            if (b) return t_first + i + __ffs(b) - 1;
         }
-        int t = t_first + min(i, window);
-        if (i >= window) {
-            const int64_t block = slot_at(t - 1) >> c.block_shift;
-            for (int64_t s; t < a.T && (s = slot_at(t)) >= 0 && s >> c.block_shift == block; ++t) {}
-        }
+        int t = t_first + window;
+        const int64_t block = slot_at(t - 1) >> c.block_shift;
+        for (int64_t s; t < a.T && (s = slot_at(t)) >= 0 && s >> c.block_shift == block; ++t) {}
         return t;
+    };
+    const auto place = [&](int t) {
+        return t - t_first < window ? (int)place_s[t - t_first] : (int)(slot_at(t) & in_block);
     };
     for (int i0 = 0; i0 < t_last - t_first; ++i0) {
         // the tokens [t0, t1) of one cache block
-        const uint32_t f = first_s[i0 >> 5] >> (i0 & 31);
-        if (f == 0) {
+        const uint32_t begins = begins_s[i0 >> 5] >> (i0 & 31);
+        if (begins == 0) {
             i0 |= 31;
             continue;
         }
-        i0 += __ffs(f) - 1;
+        i0 += __ffs(begins) - 1;
         if (i0 >= t_last - t_first) break;
         const int t0 = t_first + i0, t1 = run_end(i0 + 1);
-        const int64_t slot0 = slot_at(t0);
-        float *scale = scale_at(slot0);
-        const float old = __ldcg(scale);
         uint4 held[kHeld];
-        float top = 0.0f;
-        bool first = false;                           // the block's first slot is one of the run's
-        const auto look = [&](const uint4 &v) {
-            float x[8];
-            unpack8<F16>(v, x);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = fabsf(x[i]);
-                top = y < INFINITY ? fmaxf(top, y) : top;
-            }
-        };
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             const int t = t0 + k * kTokens + sub;
             held[k] = t < t1 ? load(t) : make_uint4(0, 0, 0, 0);
         }
-        for (int t = t0 + tid; t < t1; t += kStoreThreads) first |= (slot_at(t) & ((1 << c.block_shift) - 1)) == 0;
+        const int64_t slot0 = slot_at(t0);
+        float *scale = scale_at(slot0);
+        const float old = __ldcg(scale);
+        bool anew = false;
+        for (int i = i0; i < t1 - t_first;) {
+            if (i >= window) {
+                anew |= place(t_first + i++) == 0;
+                continue;
+            }
+            const int next = min((i | 31) + 1, t1 - t_first);
+            uint32_t f = first_s[i >> 5] >> (i & 31);
+            if (next - i < 32) f &= (1u << (next - i)) - 1u;
+            anew |= f != 0;
+            i = next;
+        }
+        // magnitudes as bits; infinities and NaN, which are the largest, do not count
+        constexpr uint32_t kInfinity = F16 ? 0x7c00u : 0x7f80u;
+        uint32_t top2 = 0;
+        const auto look = [&](const uint4 &v) {
+            top2 = larger_magnitudes(larger_magnitudes(larger_magnitudes(larger_magnitudes(top2, v.x), v.y), v.z), v.w);
+        };
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) look(held[k]);
         for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) look(load(t));
-        uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        if (lane == 0) top_s[tid >> 5] = bits;
-        const bool anew = __syncthreads_or(first);    // every thread has read the old scale
-        bits = top_s[0];
+        uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
+        if (top >= kInfinity) {
+            top = 0;
+#pragma unroll 1
+            for (int t = t0 + sub; t < t1; t += kTokens) {
+                const uint4 v = load(t);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int w = 1; w < kStoreThreads / 32; ++w) bits = max(bits, top_s[w]);
-        float s = scale_of(__uint_as_float(bits));
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+                    top = max(top, max(lo < kInfinity ? lo : 0u, hi < kInfinity ? hi : 0u));
+                }
+            }
+            top = __reduce_max_sync(0xffffffffu, top);
+        }
+        if (lane == 0) top_s[tid >> 5] = top;
+        __syncthreads();                              // every thread has read the old scale
+        top = top_s[0];
+#pragma unroll
+        for (int w = 1; w < kStoreThreads / 32; ++w) top = max(top, top_s[w]);
+        float s = scale_of(F16 ? __half2float(__ushort_as_half((unsigned short)top)) : __uint_as_float(top << 16));
+        // the block's first entry of the head
+        uint8_t *at = c.data + (slot0 >> a.page_shift) * c.s_page + head * c.s_head +
+                      ((slot0 & in_page) >> c.block_shift << c.block_shift) * c.s_slot;
         if (!anew && usable_scale(old)) {
             if (s > old) {
                 // the block's entries so far, 16 bytes a thread
                 const float ratio = __fdiv_rn(old, s);
                 constexpr int kVec = D / 16;
-                uint8_t *at = c.data + (slot0 >> a.page_shift) * c.s_page + head * c.s_head +
-                              ((slot0 & in_page) >> c.block_shift << c.block_shift) * c.s_slot;
                 for (int i = tid; i < kVec << c.block_shift; i += kStoreThreads) {
                     uint4 *p = reinterpret_cast<uint4 *>(at + (i / kVec) * c.s_slot + i % kVec * 16);
                     uint4 v = *p;
@@ -186,12 +221,18 @@ __global__ void __launch_bounds__(kStoreThreads, 5) store_e4m3_kernel(const __gr
             }
         }
         const float inv = exact_inverse(s);
+        at += 8 * vec;
+        const auto store = [&](int t, const uint4 &v) {
+            float x[8];
+            unpack8<F16>(v, x);
+            *reinterpret_cast<uint2 *>(at + place(t) * c.s_slot) = round8(x, s, inv);
+        };
 #pragma unroll
         for (int k = 0; k < kHeld; ++k) {
             const int t = t0 + k * kTokens + sub;
-            if (t < t1) store(slot_at(t), held[k], s, inv);
+            if (t < t1) store(t, held[k]);
         }
-        for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) store(slot_at(t), load(t), s, inv);
+        for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) store(t, load(t));
         if (tid == 0) *scale = s;
         __syncthreads();                              // top_s is free
         i0 = t1 - t_first - 1;
@@ -279,8 +320,8 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_e4m3_kernel(const __grid_
                     y[j] = bf16x2_rn(f.x * s, f.y * s);
             }
             uint4 *to = a.dst[k] + (int64_t)(t0 + t) * a.dst_s0[k] + h * a.dst_s1[k] + 2 * v;
-            to[0] = make_uint4(y[0], y[1], y[2], y[3]);
-            to[1] = make_uint4(y[4], y[5], y[6], y[7]);
+            __stcs(to, make_uint4(y[0], y[1], y[2], y[3]));
+            __stcs(to + 1, make_uint4(y[4], y[5], y[6], y[7]));
         }
     }
 }

@@ -32,7 +32,7 @@ struct markov_rotary_plan {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;     // tokens of a block
+constexpr int kMaxTokens = 8;     // tokens of a block
 constexpr int kUnroll = 4;        // vectors that a thread has in flight
 
 // n / d for 32-bit n by a multiplication (d >= 1): exact for n < 2^31.
@@ -69,8 +69,8 @@ struct Vec;                       // 8 elements
 template <>
 struct Vec<__nv_bfloat16> {
     uint4 v;
-    __device__ __forceinline__ void load(const char *p) { v = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void store(char *p) const { *reinterpret_cast<uint4 *>(p) = v; }
+    __device__ __forceinline__ void load(const char *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void store(char *p) const { __stcs(reinterpret_cast<uint4 *>(p), v); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -90,8 +90,8 @@ struct Vec<__nv_bfloat16> {
 template <>
 struct Vec<__half> {
     uint4 v;
-    __device__ __forceinline__ void load(const char *p) { v = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void store(char *p) const { *reinterpret_cast<uint4 *>(p) = v; }
+    __device__ __forceinline__ void load(const char *p) { v = __ldcs(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void store(char *p) const { __stcs(reinterpret_cast<uint4 *>(p), v); }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
