@@ -558,56 +558,58 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
 
 // ----------------------------------------------------------------- joining
 
-constexpr int kFewJoinThreads = 128;
+constexpr int kFewJoinParts = 8;             // loads in flight
 
-// A block a worker whose range ends within an item.  A thread has four columns of
-// a row at a time; four parts' loads are in flight together.
-template <int D, bool F16>
-__global__ void __launch_bounds__(kFewJoinThreads) few_join_kernel(const __grid_constant__ AttnE4m3Args a) {
+// Block w: the item that begins in worker w's range and is cut; a thread has four
+// columns of a row.  Latency, of its loads kFewJoinParts at a time: a request of 16000
+// keys may have 70 parts (four at a time and 128 threads took 40 us of a call of 8
+// requests).  Blocks for 32 columns each cost one row's token 2 us: most have nothing
+// to do.
+template <int D, bool F16, int ROWS>
+__global__ void __launch_bounds__(ROWS * D / 4) few_join_kernel(const __grid_constant__ AttnE4m3Args a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const FewJoin j = reinterpret_cast<const FewJoin *>(a.joins)[blockIdx.x];
     if (j.c0 == j.c1 || __ldcg(a.status) != 0u) return;
-    for (int i = threadIdx.x; i < j.rows * (D / 4); i += kFewJoinThreads) {
-        const int r = i / (D / 4), k = i % (D / 4);
-        float M = -INFINITY, L = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int b0 = j.c0; b0 <= j.c1; b0 += 4 * j.step) {
-            float pm[4], pl[4], mn = M;
-            float4 y[4];
+    const int r = threadIdx.x / (D / 4), k = threadIdx.x % (D / 4);
+    if (r >= j.rows) return;
+    float M = -INFINITY, L = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int b0 = j.c0; b0 <= j.c1; b0 += kFewJoinParts * j.step) {
+        float pm[kFewJoinParts], pl[kFewJoinParts], mn = M;
+        float4 y[kFewJoinParts];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                pm[e] = -INFINITY;
-                pl[e] = 0.0f;
-                const int b = b0 + e * j.step;
-                if (b > j.c1) continue;
-                const float *p = few_part<D>(a, b, b == j.c0);
-                pm[e] = __ldcg(p + 16 * D + r);
-                pl[e] = __ldcg(p + 16 * D + 16 + r);
-                y[e] = __ldcg(reinterpret_cast<const float4 *>(p + r * D) + k);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mn = fmaxf(mn, pm[e]);
-            const float f = M == -INFINITY ? 0.0f : ex2(M - mn);
-            M = mn;
-            L *= f;
-            o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (b0 + e * j.step > j.c1 || pm[e] == -INFINITY) continue;
-                const float w = ex2(pm[e] - M);
-                L = fmaf(pl[e], w, L);
-                o = make_float4(fmaf(y[e].x, w, o.x), fmaf(y[e].y, w, o.y), fmaf(y[e].z, w, o.z), fmaf(y[e].w, w, o.w));
-            }
+        for (int e = 0; e < kFewJoinParts; ++e) {
+            pm[e] = -INFINITY;
+            pl[e] = 0.0f;
+            const int b = b0 + e * j.step;
+            if (b > j.c1) continue;
+            const float *p = few_part<D>(a, b, b == j.c0);
+            pm[e] = __ldcg(p + 16 * D + r);
+            pl[e] = __ldcg(p + 16 * D + 16 + r);
+            y[e] = __ldcg(reinterpret_cast<const float4 *>(p + r * D) + k);
         }
-        const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
-        const int sr = j.row0 + r, tok = sr / a.group, head = j.head0 + sr - tok * a.group;
-        const int64_t token = j.qs + tok;
-        uint2 v = make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
-        if (L == 0.0f) v = make_uint2(0u, 0u);
-        *reinterpret_cast<uint2 *>(a.out + token * a.out_s0 + head * a.out_s1 + 4 * k) = v;
-        if (k == 0 && a.lse)
-            a.lse[token * a.q_heads + head] = L == 0.0f ? -INFINITY : (M - kShiftE4 + __log2f(L)) * 0.69314718055994531f;
+#pragma unroll
+        for (int e = 0; e < kFewJoinParts; ++e) mn = fmaxf(mn, pm[e]);
+        const float f = M == -INFINITY ? 0.0f : ex2(M - mn);
+        M = mn;
+        L *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+        for (int e = 0; e < kFewJoinParts; ++e) {
+            if (pm[e] == -INFINITY) continue;
+            const float w = ex2(pm[e] - M);
+            L = fmaf(pl[e], w, L);
+            o = make_float4(fmaf(y[e].x, w, o.x), fmaf(y[e].y, w, o.y), fmaf(y[e].z, w, o.z), fmaf(y[e].w, w, o.w));
+        }
     }
+    const float inv = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, L);
+    const int sr = j.row0 + r, tok = sr / a.group, head = j.head0 + sr - tok * a.group;
+    const int64_t token = j.qs + tok;
+    uint2 v = make_uint2(pack2<F16>(o.x * inv, o.y * inv), pack2<F16>(o.z * inv, o.w * inv));
+    if (L == 0.0f) v = make_uint2(0u, 0u);
+    *reinterpret_cast<uint2 *>(a.out + token * a.out_s0 + head * a.out_s1 + 4 * k) = v;
+    if (k == 0 && a.lse)
+        a.lse[token * a.q_heads + head] = L == 0.0f ? -INFINITY : (M - kShiftE4 + __log2f(L)) * 0.69314718055994531f;
 }
 
 template <int D, bool F16, bool HALF>
@@ -620,11 +622,12 @@ static cudaError_t launch_few_typed(const AttnE4m3Args &a, const CUtensorMap &k,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks * kFewWarps);
-    cfg.blockDim = dim3(kFewJoinThreads);
+    constexpr int kRows = HALF ? 8 : 16;
+    cfg.blockDim = dim3(kRows * D / 4);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, few_join_kernel<D, F16>, a);
+    return cudaLaunchKernelEx(&cfg, few_join_kernel<D, F16, kRows>, a);
 }
 
 template <int D>
