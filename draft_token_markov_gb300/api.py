@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import threading
 from typing import NamedTuple
 
@@ -814,30 +815,30 @@ def markov_rotary(plan: RotaryPlan, q, k, positions, q_out=None, k_out=None, str
     return q_out, k_out
 
 
+# a view's fields in one store (setting them one by one costs a call 2 us)
+_pack_view = struct.Struct("@PqqqqPqqqi").pack_into
+assert struct.calcsize("@PqqqqPqqqi") <= ctypes.sizeof(_E4m3View)
+
+
 def _e4m3_view(plan: PagedPlan, view: _E4m3View, t, scales, name: str):
     """Describe an e4m3 cache and its scales in `view`, one of the thread's."""
-    view.data = _dev(t, torch.float8_e4m3fn, f"{name}_cache")
-    if t.dim() != 4 or t.shape[1:] != plan._cache_shape:
-        raise ValueError(f"{name}_cache must be [pages, {plan.page_size}, {plan.kv_heads}, {plan.head_dim}], "
-                         f"got {tuple(t.shape)}")
-    view.scales = _dev(scales, torch.float32, f"{name}_scales")
-    pages = t.shape[0]
-    if (scales.dim() != 3 or scales.shape[0] != pages or scales.shape[2] != plan.kv_heads or
-            scales.shape[1] < 1 or plan.page_size % scales.shape[1]):
-        raise ValueError(f"{name}_scales must be [{pages}, blocks of a page, {plan.kv_heads}], got {tuple(scales.shape)}")
+    data, scale_data = _dev(t, torch.float8_e4m3fn, f"{name}_cache"), _dev(scales, torch.float32, f"{name}_scales")
+    shape, blocks_shape = t.shape, scales.shape
+    heads = plan.kv_heads
+    if len(shape) != 4 or shape[1:] != plan._cache_shape:
+        raise ValueError(f"{name}_cache must be [pages, {plan.page_size}, {heads}, {plan.head_dim}], got {tuple(shape)}")
+    pages = shape[0]
+    if (len(blocks_shape) != 3 or blocks_shape[0] != pages or blocks_shape[2] != heads or blocks_shape[1] < 1 or
+            plan.page_size % blocks_shape[1]):
+        raise ValueError(f"{name}_scales must be [{pages}, blocks of a page, {heads}], got {tuple(blocks_shape)}")
     s0, s1, s2, s3 = t.stride()
     if s3 != 1:
         raise ValueError(f"the last dimension of {name}_cache must be contiguous")
-    # the stride of a dimension of one element says nothing
-    blocks = scales.shape[1]
-    view.num_pages = pages
-    view.s_page, view.s_slot = s0 if pages > 1 else 0, s1
-    view.s_head = s2 if plan.kv_heads > 1 else plan.head_dim
     c0, c1, c2 = scales.stride()
-    view.ss_page = c0 if pages > 1 else 0
-    view.ss_block = c1 if blocks > 1 else 0
-    view.ss_head = c2 if plan.kv_heads > 1 else 0
-    view.block = plan.page_size // blocks
+    blocks = blocks_shape[1]
+    # the stride of a dimension of one element says nothing
+    _pack_view(view, 0, data, pages, s0 if pages > 1 else 0, s1, s2 if heads > 1 else plan.head_dim, scale_data,
+               c0 if pages > 1 else 0, c1 if blocks > 1 else 0, c2 if heads > 1 else 0, plan.page_size // blocks)
 
 
 def _e4m3_views(plan: PagedPlan, k_cache, v_cache, k_scales, v_scales):
@@ -950,7 +951,7 @@ def markov_logprobs(logits, tokens=None, temperature=None, top: int = 0, logprob
         raise ValueError("logprobs and ranks need tokens")
     if stream is None:
         # of the logits' device, whichever is current
-        stream = torch.cuda.current_stream(dev)
+        stream = _raw_stream(dev.index) if _raw_stream is not None else torch.cuda.current_stream(dev)
         new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
     else:
         new = lambda shape, dtype: _new(stream, shape, dtype, dev)  # noqa: E731
