@@ -145,13 +145,13 @@ __device__ __forceinline__ void convert_row(uint32_t raw, uint32_t operand, int 
     constexpr int kVec = D / 16;
     const int x = row & 7;
     const uint32_t from = raw + row * D, to = operand + row * 128;
+#pragma unroll 1
+    for (int v0 = 0; v0 < kVec; v0 += 2) {
+        uint4 w[2];
 #pragma unroll
-    for (int v0 = 0; v0 < kVec; v0 += 4) {
-        uint4 w[4];
+        for (int i = 0; i < 2; ++i) w[i] = lds128(from + (((v0 + i) ^ (D == 128 ? x : x >> 1)) << 4));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = lds128(from + (((v0 + i) ^ (D == 128 ? x : x >> 1)) << 4));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             uint32_t h[8];
             if (zero) w[i] = make_uint4(0, 0, 0, 0);
             f16x4_of_e4m3(w[i].x, h[0], h[1]);
@@ -159,20 +159,29 @@ __device__ __forceinline__ void convert_row(uint32_t raw, uint32_t operand, int 
             f16x4_of_e4m3(w[i].z, h[4], h[5]);
             f16x4_of_e4m3(w[i].w, h[6], h[7]);
             const uint32_t half = to + (v0 >> 2) * (kTileRows * 128);
-            sts128(half + (((2 * i) ^ x) << 4), h[0], h[1], h[2], h[3]);
-            sts128(half + (((2 * i + 1) ^ x) << 4), h[4], h[5], h[6], h[7]);
+            sts128(half + (((2 * (v0 + i) & 7) ^ x) << 4), h[0], h[1], h[2], h[3]);
+            sts128(half + (((2 * (v0 + i) + 1 & 7) ^ x) << 4), h[4], h[5], h[6], h[7]);
         }
     }
 }
 
-// A row of BF16 queries times 2^k as fp16, in place; returns k.
-template <int D>
-__device__ __forceinline__ int convert_query(uint32_t tile, int row) {
+// A row of BF16 queries times 2^k as fp16, in place, with `sign` (of a negative scale)
+// in each half's sign bit; returns k.  fp16 queries get the sign alone.
+template <int D, bool F16>
+__device__ __forceinline__ int convert_query(uint32_t tile, int row, uint32_t sign) {
     constexpr int kVec = D / 8;
     const uint32_t at = tile + row * 128;
     const auto place = [&](int v) { return at + (v >> 3) * (kTileRows * 128) + (((v & 7) ^ (row & 7)) << 4); };
+    if (F16) {
+#pragma unroll 2
+        for (int v = 0; v < kVec; ++v) {
+            const uint4 w = lds128(place(v));
+            sts128(place(v), w.x ^ sign, w.y ^ sign, w.z ^ sign, w.w ^ sign);
+        }
+        return 0;
+    }
     uint32_t top = 0;
-#pragma unroll 4
+#pragma unroll 2
     for (int v = 0; v < kVec; ++v) {
         const uint4 w = lds128(place(v));
         const uint32_t a[4] = {w.x, w.y, w.z, w.w};
@@ -182,14 +191,14 @@ __device__ __forceinline__ int convert_query(uint32_t tile, int row) {
     // NaN counts as the largest
     const int k = row_exponent(__uint_as_float(min(top, 0x7f800000u)));
     const float power = power_of_two(k);
-#pragma unroll 4
+#pragma unroll 2
     for (int v = 0; v < kVec; ++v) {
         const uint4 w = lds128(place(v));
         uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             a[i] = pack2<true>(__uint_as_float(a[i] << 16) * power, __uint_as_float(a[i] & 0xffff0000u) * power);
-        sts128(place(v), a[0], a[1], a[2], a[3]);
+        sts128(place(v), a[0] ^ sign, a[1] ^ sign, a[2] ^ sign, a[3] ^ sign);
     }
     return k;
 }
@@ -486,7 +495,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
                 __syncwarp();
                 // the whole warp goes through the boxes, an elected lane issues
                 uint32_t dst = raws + stage * S::kRaw;
-#pragma unroll 2
+#pragma unroll 1
                 for (int b = 0; b < boxes; ++b, dst += box * D)
                     tma_load_4d_elect(dst, map, 0, slot0, h, __shfl_sync(0xffffffffu, pid, b), full);
                 pid = pid_next;
@@ -534,7 +543,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
         };
         auto release = [&](Place k) { tc::commit_elect(op_empty + 8 * k.stage); };
         auto queries = [&](uint32_t tile) {
-            return step_wait((F16 ? q_full : q_ready) + 8 * (tile & 1), tile >> 1 & 1, 0x210 + (tile & 1));
+            return step_wait((F16 && a.scale2 >= 0.0f ? q_full : q_ready) + 8 * (tile & 1), tile >> 1 & 1, 0x210 + (tile & 1));
         };
         Place k{0, 0};                               // the next key tile for scores
         for (uint32_t n = 0; ok; ++n) {
@@ -648,23 +657,23 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
             const int j0 = it.j0, sinks = it.sink_tiles, w0 = it.w0, end = it.end, first = it.first, kept = it.kept;
             item_done(n);
             if (steps <= 0) continue;
-            if (!F16) {
+            if (!F16 || a.scale2 < 0.0f) {
 #pragma unroll 1
                 for (int s = 0; s < tiles; ++s, ++qt) {
                     ok = step_wait(q_full + 8 * (qt & 1), qt >> 1 & 1, 0x840);
                     if (!ok) break;
-                    const int k = convert_query<D>(smem + (qt & 1) * S::kOperand, row);
+                    const int k = convert_query<D, F16>(smem + (qt & 1) * S::kOperand, row, a.scale2 < 0.0f ? 0x80008000u : 0u);
                     row_exp[(qt & 3) * kTileRows + row] = (uint8_t)(k + 127);
                     tc::fence_proxy_async_smem();
                     arrive(q_ready + 8 * (qt & 1));
                 }
             }
+            // keys and values in turn, by the same code
+            const int tiles2 = 2 * steps;
 #pragma unroll 1
-            for (int j = j0; ok && j < j0 + steps; ++j) {
-                convert(false);
-                if (!ok) break;
-                const int key = (j < sinks ? j : w0 + j - sinks) * kTileRows + row;
-                convert(key >= end || (key < first && key >= kept));
+            for (int i = 0; ok && i < tiles2; ++i) {
+                const int j = j0 + (i >> 1), key = (j < sinks ? j : w0 + j - sinks) * kTileRows + row;
+                convert((i & 1) && (key >= end || (key < first && key >= kept)));
             }
         }
     } else {
@@ -673,7 +682,6 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
         const int slot = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;    // TMEM lane of the warp
         const uint32_t t_s = tmem + slot * kTileRows + lanes, t_o = tmem + 2 * kTileRows + slot * D + lanes;
-        const bool negate = a.scale2 < 0.0f;
         uint32_t s_phase = 0, pv_phase = 0, merge_phase = 0, qt = 0, tile = 0;
         bool ok = true, owed = false;                 // owed: slot 0 may not have read what slot 1 left
         for (uint32_t n = 0; ok; ++n) {
@@ -720,10 +728,6 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
 #pragma unroll
                     for (int k = 0; k < 4; ++k) ld_32x32b_x32(t_s + 32 * k, s + 32 * k);
                     tc::wait_ld();
-                    if (negate) {
-#pragma unroll
-                        for (int k = 0; k < kTileRows; ++k) s[k] = -s[k];
-                    }
                     if (key0 + kTileRows > whole_end || (key0 < whole_first && key0 + kTileRows > a.sinks)) {
                         const int hi = min(pos + 1, a.r.room) - key0, sk = min(a.sinks - key0, hi);
                         const int lo = window_start(a.window, pos) - key0;
