@@ -522,11 +522,11 @@ markov_status markov_paged_attention_e4m3(
     const bool f16 = p->d.dtype == MARKOV_F16;
     const cudaStream_t s = (cudaStream_t)stream;
     // Few rows of query heads a request on average: bound by the cache's bytes.  In us,
-    // few against many, 8 query heads a key head: 32 requests of 500-16000 keys with 16
-    // rows each 63 and 107, 24 rows 86 and 108, 32 rows 89 and 107, 48 rows 129 and 109; 8
-    // requests with 16 rows 37 and 41, 32 rows 41 and 42, 72 rows 68 and 43
+    // few against many: 64 requests of 500-16000 keys with 16 rows for each of 4 key heads
+    // 70 and 95; 32 of them with 16 rows for each of 8 key heads 68 and 87, 24 rows 88 and
+    // 87, 32 rows 92 and 88; 8 of 1000-16000 keys with 16 rows 39 and 37, 32 rows 44 and 37
     const int64_t query_rows = (int64_t)num_tokens * group;
-    const bool few = query_rows <= 32 * (int64_t)rows;
+    const bool few = query_rows <= 16 * (int64_t)rows;
     CUtensorMap qmap, kmap, vmap;
     const int slots = few ? 32 : 128;
     if (!encode_e4m3_map(&kmap, *k_cache, *p, slots) || !encode_e4m3_map(&vmap, *v_cache, *p, slots) ||

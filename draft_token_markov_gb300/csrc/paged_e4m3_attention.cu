@@ -38,7 +38,7 @@ constexpr int kRing = 4;                     // items that are known ahead
 constexpr int kTileRows = 128, kTileShift = 7;   // keys of a tile, and rows
 constexpr int kGrains = kTileRows / 16;          // groups of 16 keys of a tile, a scale each
 constexpr int kScaleRing = 8;                // tiles whose scales are kept; five at most are in use
-constexpr int kWeightOne = 3, kWeightTwo = 7;    // an item's start and end, in tiles
+constexpr int kWeightOne = 3, kWeightTwo = 10;    // an item's start and end, in tiles
 constexpr uint64_t kUnitNs = 20000;          // what a unit of work may take at most
 constexpr uint32_t kReaders = 15;            // warps that read an item
 
