@@ -394,23 +394,26 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     }
     if (a.top > 0 && warp == 0) {
         // the top-th largest of the threads' maxima, eight a lane
+        static_assert(kWarps == 8, "the network");
         uint32_t g[kWarps], key = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) g[w] = thread_key[w * 32 + lane];
+        // a lane's in falling order (a network of 19 exchanges), then the first of all
+        constexpr uint8_t kNetwork[19][2] = {{0, 2}, {1, 3}, {4, 6}, {5, 7}, {0, 4}, {1, 5}, {2, 6}, {3, 7}, {0, 1}, {2, 3},
+                                             {4, 5}, {6, 7}, {2, 4}, {3, 5}, {1, 4}, {3, 6}, {1, 2}, {3, 4}, {5, 6}};
+#pragma unroll
+        for (int e = 0; e < 19; ++e) {
+            const uint32_t hi = max(g[kNetwork[e][0]], g[kNetwork[e][1]]), lo = min(g[kNetwork[e][0]], g[kNetwork[e][1]]);
+            g[kNetwork[e][0]] = hi;
+            g[kNetwork[e][1]] = lo;
+        }
         for (int i = 0; i < a.top; ++i) {
-            uint32_t mine = g[0];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) mine = max(mine, g[w]);
-            key = __reduce_max_sync(0xffffffffu, mine);
-            const uint32_t who = __ballot_sync(0xffffffffu, mine == key);
+            key = __reduce_max_sync(0xffffffffu, g[0]);
+            const uint32_t who = __ballot_sync(0xffffffffu, g[0] == key);
             if (lane == __ffs(who) - 1) {
-                bool gone = false;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w)
-                    if (!gone && g[w] == key) {
-                        g[w] = 0;
-                        gone = true;
-                    }
+                for (int w = 0; w + 1 < kWarps; ++w) g[w] = g[w + 1];
+                g[kWarps - 1] = 0;
             }
         }
         if (lane == 0) bound_s = key;
