@@ -132,7 +132,7 @@ struct Vec<float> {
 
 template <typename T, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-    extern __shared__ float2 turn[];              // [tile][pairs] cosine and sine
+    extern __shared__ __align__(16) float2 turn[];    // [tile][pairs] cosine and sine
     const int t0 = blockIdx.x * a.tile, tokens = min(a.tile, a.tokens - t0);
     for (int i = threadIdx.x; i < tokens * a.pairs; i += kThreads) {
         const int t = i / a.pairs;
@@ -175,15 +175,18 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                 x[e][0].store(dst[e]);
                 continue;
             }
-            const float2 *cs = turn + tok[e] * a.pairs + vec[e] * (INTERLEAVED ? 4 : 8);
+            // two pairs' cosines and sines in each
+            const float4 *cs = reinterpret_cast<const float4 *>(turn + tok[e] * a.pairs + vec[e] * (INTERLEAVED ? 4 : 8));
             if (INTERLEAVED) {
                 float y[8], z[8];
                 x[e][0].get(y);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 w = cs[j];
+                for (int j = 0; j < 4; j += 2) {
+                    const float4 w = cs[j / 2];
                     z[2 * j] = y[2 * j] * w.x - y[2 * j + 1] * w.y;
                     z[2 * j + 1] = y[2 * j + 1] * w.x + y[2 * j] * w.y;
+                    z[2 * j + 2] = y[2 * j + 2] * w.z - y[2 * j + 3] * w.w;
+                    z[2 * j + 3] = y[2 * j + 3] * w.z + y[2 * j + 2] * w.w;
                 }
                 x[e][0].put(z);
                 x[e][0].store(dst[e]);
@@ -192,10 +195,12 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
                 x[e][0].get(y);
                 x[e][kPartner].get(z);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 r = cs[j];
+                for (int j = 0; j < 8; j += 2) {
+                    const float4 r = cs[j / 2];
                     u[j] = y[j] * r.x - z[j] * r.y;
                     w[j] = z[j] * r.x + y[j] * r.y;
+                    u[j + 1] = y[j + 1] * r.z - z[j + 1] * r.w;
+                    w[j + 1] = z[j + 1] * r.z + y[j + 1] * r.w;
                 }
                 x[e][0].put(u);
                 x[e][kPartner].put(w);
