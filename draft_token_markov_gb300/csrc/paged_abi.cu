@@ -423,8 +423,11 @@ markov_status markov_paged_write_e4m3(markov_paged_plan *p, const void *key, int
     a.T = num_tokens;
     a.heads = p->d.kv_heads;
     a.page_shift = p->page_shift;
-    // a token a block while all of them are resident, else a cache block's worth
-    a.chunk = (int64_t)num_tokens * p->d.kv_heads <= 2048 ? 1 : std::max(k_cache->block, v_cache->block);
+    // a token a block while those find a place at once, then more: of single tokens of a
+    // batch a warp takes one after the other, of a prompt a block a cache block
+    a.chunk = 1;
+    while (a.chunk < 64 && (int64_t)(num_tokens + a.chunk - 1) / a.chunk * p->d.kv_heads * 2 > 16 * p->sm_count) a.chunk *= 4;
+    if (a.chunk == 64) a.chunk = std::max({64, (int)k_cache->block, (int)v_cache->block});
     a.status = p->ctrl;
     if (launch_store_e4m3(a, p->d.head_dim, p->d.dtype == MARKOV_F16, keep_scales != 0, (cudaStream_t)stream) != cudaSuccess) {
         cudaGetLastError();

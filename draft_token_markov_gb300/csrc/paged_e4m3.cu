@@ -32,12 +32,15 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
 // rescaled: a thread block (chunk of tokens, head, side) takes the cache blocks
 // whose first token of the call lies in its chunk, one after the other, with all
 // of their tokens, also those past the chunk.  Where the runs of a cache block's
-// tokens begin and end is found once, from the slots: a bit a token.
+// tokens begin and end is found once, from the slots: a bit a token.  Where many begin
+// in a chunk (single tokens of a batch) its warps take one each.
 // Up to kHeld * 128 vectors of a run stay in registers between the maximum and the
 // rounding, the rest is read again.  Rescaling comes before the new values, so that
 // it need not know which entries they replace.  Bound by latency (slots, values,
-// maximum one after the other) where a call is small, then by memory: the elements
-// are read once and written as bytes.
+// maximum one after the other) where a call is small, then by instructions as much as
+// by memory: 8192 tokens of 8 heads of 128 (50 MB, scales of 64 tokens) take 14.8 us
+// (51% of the copy rate), 72 tokens 4.2 us in a graph, 1000 single tokens 14.5 us.  With
+// the maximum in fp32 and divisions in the loop the first took 27 us.
 constexpr int kStoreThreads = 128;
 constexpr int kHeld = 8;
 constexpr int kMostChunk = 256;              // tokens of a chunk: a cache block at most
@@ -65,7 +68,106 @@ __device__ __forceinline__ uint32_t larger_magnitudes(uint32_t a, uint32_t b) {
     return __vmaxu2(a, b & 0x7fff7fffu);
 }
 
-template <int D, bool F16, bool KEEP>
+// The run [t0, t1) of one cache block's tokens, by a block or a warp (TEAM threads).
+// slot_at, place: a token's slot and its place in its cache block; begins_anew: whether
+// the cache block's first place is among tokens.
+template <int D, bool F16, int TEAM, class SlotAt, class Place, class Anew>
+__device__ __forceinline__ void store_run(const StoreArgs &a, const StoreSide &side, int head, int t0, int t1, const SlotAt &slot_at,
+                                          const Place &place, const Anew &begins_anew, uint32_t *top_s) {
+    constexpr int kLanes = D / 8, kTokens = TEAM / kLanes;              // threads of a token, tokens of a turn
+    const E4m3Side &c = side.cache;
+    const int tid = threadIdx.x % TEAM, sub = tid / kLanes, vec = tid % kLanes;
+    const auto sync = [] {
+        if (TEAM == 32) __syncwarp(); else __syncthreads();
+    };
+    const uint4 *src = side.src + head * side.src_s1 + vec;
+    const auto load = [&](int t) { return __ldcs(src + t * side.src_s0); };
+    uint4 held[kHeld];
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        const int t = t0 + k * kTokens + sub;
+        held[k] = t < t1 ? load(t) : make_uint4(0, 0, 0, 0);
+    }
+    const int64_t slot0 = slot_at(t0), in_page = slot0 & ((1 << a.page_shift) - 1);
+    float *scale = c.scales + (slot0 >> a.page_shift) * c.ss_page + (in_page >> c.block_shift) * c.ss_block + head * c.ss_head;
+    const float old = __ldcg(scale);
+    const bool anew = begins_anew(t0, t1);
+    // magnitudes as bits; infinities and NaN, which are the largest, do not count
+    constexpr uint32_t kInfinity = F16 ? 0x7c00u : 0x7f80u;
+    uint32_t top2 = 0;
+    const auto look = [&](const uint4 &v) {
+        top2 = larger_magnitudes(larger_magnitudes(larger_magnitudes(larger_magnitudes(top2, v.x), v.y), v.z), v.w);
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) look(held[k]);
+    for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) look(load(t));
+    uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
+    if (top >= kInfinity) {
+        top = 0;
+#pragma unroll 1
+        for (int t = t0 + sub; t < t1; t += kTokens) {
+            const uint4 v = load(t);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
+                top = max(top, max(lo < kInfinity ? lo : 0u, hi < kInfinity ? hi : 0u));
+            }
+        }
+        __syncwarp();
+        top = __reduce_max_sync(0xffffffffu, top);
+    }
+    if (TEAM > 32) {
+        if ((tid & 31) == 0) top_s[tid >> 5] = top;
+        __syncthreads();                              // every thread has read the old scale
+        top = top_s[0];
+#pragma unroll
+        for (int w = 1; w < TEAM / 32; ++w) top = max(top, top_s[w]);
+    }
+    float s = scale_of(F16 ? __half2float(__ushort_as_half((unsigned short)top)) : __uint_as_float(top << 16));
+    // the block's first entry of the head
+    uint8_t *at = c.data + (slot0 >> a.page_shift) * c.s_page + head * c.s_head + (in_page >> c.block_shift << c.block_shift) * c.s_slot;
+    if (!anew && usable_scale(old)) {
+        if (s > old) {
+            // the block's entries so far, 16 bytes a thread
+            const float ratio = __fdiv_rn(old, s);
+            constexpr int kVec = D / 16;
+            for (int i = tid; i < kVec << c.block_shift; i += TEAM) {
+                uint4 *p = reinterpret_cast<uint4 *>(at + (i / kVec) * c.s_slot + i % kVec * 16);
+                uint4 v = *p;
+                uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 lo = f32x2_of_e4m3(w[j]), hi = f32x2_of_e4m3(w[j] >> 16);
+                    w[j] = e4m3_of_f32(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
+                }
+                *p = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            sync();
+        } else {
+            s = old;
+        }
+    }
+    const float inv = exact_inverse(s);
+    at += 8 * vec;
+    const auto store = [&](int t, const uint4 &v) {
+        float x[8];
+        unpack8<F16>(v, x);
+        *reinterpret_cast<uint2 *>(at + place(t) * c.s_slot) = round8(x, s, inv);
+    };
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+        const int t = t0 + k * kTokens + sub;
+        if (t < t1) store(t, held[k]);
+    }
+    for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) store(t, load(t));
+    if (tid == 0) *scale = s;
+    sync();                                           // top_s is free
+}
+
+// MANY: a chunk may have several runs (in us, without and with: 72 tokens, a token a
+// chunk, 4.0 and 4.5; 1000 single tokens, 16 a chunk, 38 and 14).
+template <int D, bool F16, bool KEEP, bool MANY>
 __global__ void __launch_bounds__(kStoreThreads, 7) store_e4m3_kernel(const __grid_constant__ StoreArgs a) {
     constexpr int kLanes = D / 8, kTokens = kStoreThreads / kLanes;     // threads of a token, tokens of a turn
     const uint32_t pending = __ldcg(a.status);                          // nothing is written then
@@ -79,8 +181,6 @@ __global__ void __launch_bounds__(kStoreThreads, 7) store_e4m3_kernel(const __gr
         const int64_t s = t >= 0 && t < a.T ? __ldg(a.slots + t) : -1;
         return s >= 0 && s < a.num_slots ? s : (int64_t)-1;
     };
-    const uint4 *src = side.src + head * side.src_s1 + vec;
-    const auto load = [&](int t) { return __ldcs(src + t * side.src_s0); };
     const auto scale_at = [&](int64_t slot) {
         return c.scales + (slot >> a.page_shift) * c.ss_page + ((slot & in_page) >> c.block_shift) * c.ss_block +
                head * c.ss_head;
@@ -91,7 +191,7 @@ __global__ void __launch_bounds__(kStoreThreads, 7) store_e4m3_kernel(const __gr
             if (slot < 0 || pending) continue;
             const float s = __ldg(scale_at(slot));
             float x[8];
-            unpack8<F16>(load(t), x);
+            unpack8<F16>(__ldcs(side.src + t * side.src_s0 + head * side.src_s1 + vec), x);
             uint8_t *to = c.data + (slot >> a.page_shift) * c.s_page + (slot & in_page) * c.s_slot + head * c.s_head + 8 * vec;
             *reinterpret_cast<uint2 *>(to) = round8(x, s, exact_inverse(s));
         }
@@ -135,27 +235,10 @@ __global__ void __launch_bounds__(kStoreThreads, 7) store_e4m3_kernel(const __gr
     const auto place = [&](int t) {
         return t - t_first < window ? (int)place_s[t - t_first] : (int)(slot_at(t) & in_block);
     };
-    for (int i0 = 0; i0 < t_last - t_first; ++i0) {
-        // the tokens [t0, t1) of one cache block
-        const uint32_t begins = begins_s[i0 >> 5] >> (i0 & 31);
-        if (begins == 0) {
-            i0 |= 31;
-            continue;
-        }
-        i0 += __ffs(begins) - 1;
-        if (i0 >= t_last - t_first) break;
-        const int t0 = t_first + i0, t1 = run_end(i0 + 1);
-        uint4 held[kHeld];
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
-            const int t = t0 + k * kTokens + sub;
-            held[k] = t < t1 ? load(t) : make_uint4(0, 0, 0, 0);
-        }
-        const int64_t slot0 = slot_at(t0);
-        float *scale = scale_at(slot0);
-        const float old = __ldcg(scale);
+    // whether a place 0 is among tokens [t0, t1)
+    const auto begins_anew = [&](int t0, int t1) {
         bool anew = false;
-        for (int i = i0; i < t1 - t_first;) {
+        for (int i = t0 - t_first; i < t1 - t_first;) {
             if (i >= window) {
                 anew |= place(t_first + i++) == 0;
                 continue;
@@ -166,76 +249,23 @@ __global__ void __launch_bounds__(kStoreThreads, 7) store_e4m3_kernel(const __gr
             anew |= f != 0;
             i = next;
         }
-        // magnitudes as bits; infinities and NaN, which are the largest, do not count
-        constexpr uint32_t kInfinity = F16 ? 0x7c00u : 0x7f80u;
-        uint32_t top2 = 0;
-        const auto look = [&](const uint4 &v) {
-            top2 = larger_magnitudes(larger_magnitudes(larger_magnitudes(larger_magnitudes(top2, v.x), v.y), v.z), v.w);
-        };
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k) look(held[k]);
-        for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) look(load(t));
-        uint32_t top = __reduce_max_sync(0xffffffffu, max(top2 & 0xffffu, top2 >> 16));
-        if (top >= kInfinity) {
-            top = 0;
-#pragma unroll 1
-            for (int t = t0 + sub; t < t1; t += kTokens) {
-                const uint4 v = load(t);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t lo = w[i] & 0x7fffu, hi = w[i] >> 16 & 0x7fffu;
-                    top = max(top, max(lo < kInfinity ? lo : 0u, hi < kInfinity ? hi : 0u));
-                }
-            }
-            top = __reduce_max_sync(0xffffffffu, top);
+        return anew;
+    };
+    // short runs: a warp each; long ones: the block together
+    const int tokens = t_last - t_first;
+    int runs = 0;
+    for (int i = 0; i < tokens; i += 32) runs += __popc(begins_s[i >> 5] & (tokens - i < 32 ? (1u << (tokens - i)) - 1u : ~0u));
+    const bool by_warp = MANY && runs > 1 && tokens <= 16 * runs;
+    int n = 0;
+    for (int i = 0; i < tokens; i = (i | 31) + 1) {
+        for (uint32_t b = begins_s[i >> 5] & (tokens - i < 32 ? (1u << (tokens - i)) - 1u : ~0u); b; b &= b - 1, ++n) {
+            if (by_warp && n % (kStoreThreads / 32) != tid >> 5) continue;
+            const int i0 = i + __ffs(b) - 1, t0 = t_first + i0, t1 = run_end(i0 + 1);
+            if (MANY && by_warp)
+                store_run<D, F16, 32>(a, side, head, t0, t1, slot_at, place, begins_anew, top_s);
+            else
+                store_run<D, F16, kStoreThreads>(a, side, head, t0, t1, slot_at, place, begins_anew, top_s);
         }
-        if (lane == 0) top_s[tid >> 5] = top;
-        __syncthreads();                              // every thread has read the old scale
-        top = top_s[0];
-#pragma unroll
-        for (int w = 1; w < kStoreThreads / 32; ++w) top = max(top, top_s[w]);
-        float s = scale_of(F16 ? __half2float(__ushort_as_half((unsigned short)top)) : __uint_as_float(top << 16));
-        // the block's first entry of the head
-        uint8_t *at = c.data + (slot0 >> a.page_shift) * c.s_page + head * c.s_head +
-                      ((slot0 & in_page) >> c.block_shift << c.block_shift) * c.s_slot;
-        if (!anew && usable_scale(old)) {
-            if (s > old) {
-                // the block's entries so far, 16 bytes a thread
-                const float ratio = __fdiv_rn(old, s);
-                constexpr int kVec = D / 16;
-                for (int i = tid; i < kVec << c.block_shift; i += kStoreThreads) {
-                    uint4 *p = reinterpret_cast<uint4 *>(at + (i / kVec) * c.s_slot + i % kVec * 16);
-                    uint4 v = *p;
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 lo = f32x2_of_e4m3(w[j]), hi = f32x2_of_e4m3(w[j] >> 16);
-                        w[j] = e4m3_of_f32(lo.x * ratio, lo.y * ratio, hi.x * ratio, hi.y * ratio);
-                    }
-                    *p = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-                __syncthreads();
-            } else {
-                s = old;
-            }
-        }
-        const float inv = exact_inverse(s);
-        at += 8 * vec;
-        const auto store = [&](int t, const uint4 &v) {
-            float x[8];
-            unpack8<F16>(v, x);
-            *reinterpret_cast<uint2 *>(at + place(t) * c.s_slot) = round8(x, s, inv);
-        };
-#pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
-            const int t = t0 + k * kTokens + sub;
-            if (t < t1) store(t, held[k]);
-        }
-        for (int t = t0 + kHeld * kTokens + sub; t < t1; t += kTokens) store(t, load(t));
-        if (tid == 0) *scale = s;
-        __syncthreads();                              // top_s is free
-        i0 = t1 - t_first - 1;
     }
 }
 
@@ -243,9 +273,11 @@ template <int D, bool F16>
 static cudaError_t launch_store_typed(const StoreArgs &a, bool keep, cudaStream_t s) {
     const dim3 grid((a.T + a.chunk - 1) / a.chunk, a.heads, 2);
     if (keep)
-        store_e4m3_kernel<D, F16, true><<<grid, kStoreThreads, 0, s>>>(a);
+        store_e4m3_kernel<D, F16, true, false><<<grid, kStoreThreads, 0, s>>>(a);
+    else if (a.chunk == 1)
+        store_e4m3_kernel<D, F16, false, false><<<grid, kStoreThreads, 0, s>>>(a);
     else
-        store_e4m3_kernel<D, F16, false><<<grid, kStoreThreads, 0, s>>>(a);
+        store_e4m3_kernel<D, F16, false, true><<<grid, kStoreThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -259,7 +291,9 @@ cudaError_t launch_store_e4m3(const StoreArgs &a, int head_dim, bool f16, bool k
 //
 // A thread block finds the slots of its tokens (a binary search over the rows, a
 // thread a token), then copies their vectors of 16 bytes, each to 32.  Bound by
-// memory.
+// memory: 16 requests of up to 8000 tokens (429 MB moved) take 74 us, 86% of the copy
+// rate (77 us without the streaming hint on its stores), one of 500 tokens 3.7 us in a
+// graph.
 constexpr int kFetchThreads = 256;
 constexpr int kFetchTokens = 32;
 

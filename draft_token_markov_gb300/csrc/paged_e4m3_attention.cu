@@ -18,6 +18,18 @@
 // Roles.  Warps 0-3 and 4-7: softmax and output of the two slots, a thread a row;
 // 8-11: conversion; 12: MMAs; 13 and 14: loads of keys and values, with their
 // scales; 15: walks the block's items and loads queries.
+//
+// Bounds.  4096 tokens over 16384 keys (32 / 8 heads of 128) take 722 us, 1332 TFLOP/s
+// (68% of the GEMM rate; 660 us over a cache of BF16): a turn of two row tiles over 128
+// keys takes some 3600 cycles, of which the MMAs are 2048; a slot's softmax and its
+// hand-overs are most of the rest, and shared memory is busy with operands, conversion
+// and loads (about 2900 cycles of 128 bytes).  Without conversion and scales it took
+// 729 us of what were then 840.  Instructions to fetch counted most: with the conversion
+// loops rolled, one body for keys and values, and negative scales put into the queries,
+// 840 us became 722, and 32 rows of 9 tokens over 500 to 16000 keys 117 us 90.  8 rows of
+// 9 tokens over 1000 to 16000 keys take 38.5 us in a graph (74 MB, 11 us at the copy
+// rate): start, conversion of every tile by one warpgroup (some 1300 cycles for keys and
+// values), ends, the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -38,7 +50,10 @@ constexpr int kRing = 4;                     // items that are known ahead
 constexpr int kTileRows = 128, kTileShift = 7;   // keys of a tile, and rows
 constexpr int kGrains = kTileRows / 16;          // groups of 16 keys of a tile, a scale each
 constexpr int kScaleRing = 8;                // tiles whose scales are kept; five at most are in use
-constexpr int kWeightOne = 3, kWeightTwo = 10;    // an item's start and end, in tiles
+// an item's start and end, in tiles of one and of two row tiles.  In us, for 16 rows of
+// 1-500 tokens (7 query heads a key head), 24 rows of 1-300 (8) and 32 rows of 9 tokens:
+// 3 and 10 109, 123, 90; 3 and 7 108, 131, 90; 4 and 9 105, 127, 93; 6 and 12 112, 124, 97
+constexpr int kWeightOne = 3, kWeightTwo = 10;
 constexpr uint64_t kUnitNs = 20000;          // what a unit of work may take at most
 constexpr uint32_t kReaders = 15;            // warps that read an item
 

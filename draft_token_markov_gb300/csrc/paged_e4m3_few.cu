@@ -10,15 +10,16 @@
 //   O += P V     the scores' registers are P's fragment
 // The scale of a value enters its weight, as an addition in the exponent, and is
 // taken out of the sum again; m is the maximum of y, which is what bounds p.  So a
-// block's scales cost a few instructions for 16 keys, a scale's half step.  Keys and values go from
-// shared memory to registers once and become fp16 there (exact: e4m3 is a subset);
-// values in pairs of keys by byte permutes.  (Through tcgen05 they would be written
-// to shared memory as fp16 and read from there: 7 bytes of its traffic for each of
-// the cache, more than it has to give at the memory's rate.)
+// block's scales cost a few instructions for half a step's 16 keys.  Keys and values go
+// from shared memory to registers once and become fp16 there (exact: e4m3 is a
+// subset); values in pairs of keys by byte permutes.  (Through tcgen05 they would be
+// written to shared memory as fp16 and read from there: 7 bytes of its traffic for each
+// of the cache, more than it has to give at the memory's rate; 64 requests with 16 rows
+// took 95 us that way and 70 here.)
 //
 // The maximum that p is taken against moves when a row's grows by more than 2^8
-// (kLazy), so that most steps need no exchange between lanes; weights are at most
-// 2^(kShift + kLazy) = 2^15.
+// (kLazyE4), so that most steps need no exchange between lanes; weights are at most
+// 2^(kShiftE4 + kLazyE4) = 2^15.
 //
 // Work.  An item weighs one for each of its steps of 32 keys and kEnds for its
 // start and end.  Neighbouring warps have neighbouring key heads (as many as the
@@ -27,6 +28,14 @@
 // heads has the items of the call end to end, in order of request, group of heads and
 // rows, cut into ranges of equal weight, one a warp.  A cut item leaves its parts in
 // the plan's scratch, which a second launch joins.
+//
+// Bounds.  64 single tokens over 500 to 32000 keys (64 / 8 heads of 128, 0.91 GB) take
+// 150 us, 90% of the copy rate; 163 us with a head's warps on keys of their own, 231 us
+// with lines of 256 bytes, which fetch a neighbouring head's too.  One row's token over
+// 1000 keys takes 11.5 us in a graph: the start, four steps, the join.  With 16 rows the
+// arithmetic counts: 32 requests of two tokens with 8 heads each 68 us for 37 us of
+// bytes.  8 warps of 250 registers and steps of 32 keys; 12 warps of 168 and steps of 16
+// took 186 us where these took 166.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -44,8 +53,11 @@ constexpr int kFewWarps = 8;
 constexpr int kFewThreads = kFewWarps * 32;
 constexpr int kStep = 32;                    // keys of a step, in two halves of 16
 constexpr int kStepShift = 5;
-constexpr int kEnds = 2;                     // an item's start and end, in steps
-constexpr int kLeast = 2;                    // units of a range
+// an item's start and end, in steps, and the least units of a range.  One row's token and
+// the 64 of above in us: 2 and 2 12.2 and 150.3; 3 and 3 14.5 and 151.1; 3 and 1 12.6 and
+// 150.9; 1 and 1 12.9 and 155.2
+constexpr int kEnds = 2;
+constexpr int kLeast = 2;
 
 template <int D>
 struct FewShape {

@@ -10,7 +10,9 @@
 // A block takes the sines and cosines of its tokens to shared memory, amplitude
 // included, then walks their heads in 16-byte vectors (half layout: the vector
 // and its partner rot_dim / 2 further on).  Bound by memory: each element is
-// read and written once.
+// read and written once; 8191 tokens of 40 heads of 128 (168 MB) take 30 us, 84% of the
+// copy rate, with 8 tokens a block and 4 vectors in flight a thread (31 us with 4
+// tokens, 33 with 2; 35 with 2 vectors); 72 tokens 2.9 us in a graph.
 #include <cmath>
 #include <cstdint>
 #include <new>
