@@ -73,7 +73,7 @@ def _runs(page, pages, rng, rows, most):
 @pytest.mark.parametrize("heads,d,page,blocks,order,rows,most", [
     (1, 64, 16, 1, "nhd", 1, 1), (3, 128, 16, 1, "hnd", 8, 9), (8, 64, 64, 4, "nhd", 5, 40),
     (2, 128, 256, 1, "nhd", 2, 300), (5, 128, 32, 2, "hnd", 60, 100), (8, 128, 64, 1, "nhd", 4, 700),
-    (2, 64, 256, 16, "hnd", 3, 500)])
+    (2, 64, 256, 16, "hnd", 3, 500), (4, 128, 64, 1, "nhd", 700, 1), (8, 64, 32, 2, "hnd", 300, 9), (2, 128, 128, 1, "nhd", 1500, 3)])
 def test_store(gpu_lib, dtype, heads, d, page, blocks, order, rows, most):
     rng = np.random.default_rng(page + rows)
     g = torch.Generator().manual_seed(page * rows)
