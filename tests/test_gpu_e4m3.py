@@ -88,6 +88,19 @@ def test_store(gpu_lib, dtype, heads, d, page, blocks, order, rows, most):
     _store(gpu_lib, new.to(dtype), value.to(dtype), *caches, *scales, slots, keep=True)
 
 
+@pytest.mark.parametrize("rows,most", [(3, 9), (300, 1), (2, 700)])
+def test_store_blocks_of_keys_and_values_differ(gpu_lib, rows, most):
+    rng = np.random.default_rng(rows)
+    g = torch.Generator().manual_seed(rows)
+    page, heads, d = 128, 8, 128
+    pages = rows * (most // page + 3) + 2
+    slots = _runs(page, pages, rng, rows, most)
+    new, value = (torch.randn((len(slots), heads, d), generator=g).bfloat16() for _ in range(2))
+    caches = [_bytes((pages, page, heads, d), "nhd", g) for _ in range(2)]
+    for k, v in ((1, 8), (8, 1), (2, 4)):
+        _store(gpu_lib, new, value, *caches, _scales(pages, k, heads, g), _scales(pages, v, heads, g), slots)
+
+
 def test_store_skips_and_strides(gpu_lib):
     g = torch.Generator().manual_seed(2)
     heads, d, page, pages = 3, 64, 32, 6
@@ -541,6 +554,28 @@ def test_many_rows_and_long_ones(gpu_lib, hq, hkv, rows, hi):
         assert int(live.sum()) >= min(12, rows) * hq
         assert float(((out.double() - want).abs() - tol)[live].max()) <= 0
         assert float(((lse.double() - wl).abs() - tl)[live].max()) <= 0
+
+
+def test_two_plans_at_once(gpu_lib):
+    """Calls that may overlap, each on a plan and a stream of its own."""
+    api = gpu_lib
+    for reqs in ([(3000, 1)] * 20, [(700, 60)] * 5):
+        cases = [Case(reqs, 8, 2, 128, 64, 32, seed=s) for s in (21, 22)]
+        want = [run(api, c) for c in cases]
+        plans, devs = [c.plan(api) for c in cases], [c.dev() for c in cases]
+        streams = [torch.cuda.Stream() for _ in cases]
+        torch.cuda.synchronize()
+        got = []
+        for _ in range(5):
+            for plan, d, s in zip(plans, devs, streams):
+                got.append(api.markov_paged_attention_e4m3(plan, d["q"], d["kc"], d["vc"], d["ks"], d["vs"], d["table"], d["idx"],
+                                                           d["start"], d["lens"], lse=True, stream=s))
+        torch.cuda.synchronize()
+        for i, (out, lse) in enumerate(got):
+            assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+        for p in plans:
+            assert api.markov_paged_plan_status(p) == 0
+            p.close()
 
 
 def test_a_pending_status_computes_nothing(gpu_lib):

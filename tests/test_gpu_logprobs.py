@@ -1,6 +1,9 @@
 """Log probabilities, ranks, entropies and alternatives on the GPU against their
 plain 64-bit form."""
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -9,6 +12,7 @@ import torch
 from tests import serving_ref as ref
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _compare(api, logits, tokens, temperature, top, stream=None):
@@ -157,6 +161,28 @@ def test_streams_graphs_and_two_calls_at_once(gpu_lib):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(out[n], getattr(want, n)) for n in out)
+
+
+def test_the_first_call_may_be_captured():
+    """In a process of its own: nothing has to be called before a capture."""
+    code = """
+import torch
+from draft_token_markov_gb300 import api
+l = torch.randn((3, 5000), device="cuda")
+t = torch.tensor([1, 2, 3], device="cuda")
+out = [torch.zeros(3, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda"), torch.zeros(3, device="cuda")]
+api.lib()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    api.markov_logprobs(l, t, None, 0, logprobs=out[0], ranks=out[1], entropy=out[2])
+g.replay()
+torch.cuda.synchronize()
+want = torch.log_softmax(l.double(), -1).gather(1, t[:, None])[:, 0]
+assert (out[0].double() - want).abs().max() < 1e-5
+"""
+    done = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_many_rows(gpu_lib):

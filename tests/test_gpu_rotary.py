@@ -118,6 +118,25 @@ def test_strides_streams_and_graphs(gpu_lib):
     plan.close()
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_wide_strides_of_each_type(gpu_lib, interleaved):
+    """Keys of another number of heads and other strides than the queries, one of them in place."""
+    api = gpu_lib
+    g = torch.Generator(device="cuda").manual_seed(2)
+    plan = api.RotaryPlan(96, 64, interleaved=interleaved)
+    f = ref.frequencies(64)
+    for dtype in (torch.float32, torch.float16, torch.bfloat16):
+        wide = torch.randn((33, 7, 120), generator=g, device="cuda").to(dtype)
+        q, k = wide[:, :4, :96], torch.randn((3, 33, 96), generator=g, device="cuda").to(dtype).transpose(0, 1)
+        pos = torch.randint(0, 10 ** 6, (33,), generator=g, device="cuda").int()
+        q0, k0, rest = q.clone(), k.clone(), wide[..., 96:].clone()
+        _, ko = api.markov_rotary(plan, q, k, pos, q_out=q)
+        _check(q, q0, pos, f, interleaved)
+        _check(ko, k0, pos, f, interleaved)
+        assert torch.equal(k, k0) and torch.equal(wide[..., 96:], rest)
+    plan.close()
+
+
 def test_nothing_to_do_and_special_values(gpu_lib):
     api = gpu_lib
     plan = api.RotaryPlan(16)
