@@ -93,6 +93,12 @@ struct Logits {
     }
 };
 
+template <bool F32>
+__device__ __forceinline__ float vector_max(const uint4 &v) {
+    const uint32_t w = word_max<F32>(word_max<F32>(v.x, v.y), word_max<F32>(v.z, v.w));
+    return F32 ? __uint_as_float(w) : __uint_as_float(word_max<true>(w << 16, w & 0xffff0000u));
+}
+
 __device__ __forceinline__ float nan_max(float a, float b) {
     return __uint_as_float(word_max<true>(__float_as_uint(a), __float_as_uint(b)));
 }
@@ -435,21 +441,22 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         bool slow = m != m || m == INFINITY;                           // NaN and infinities: by their keys
         int listed = 0;
         if (!slow) {
-            if (r.m >= bound && r.m > -INFINITY) {
+            const float least = fmaxf(bound, -3.402823466e38f);        // masked logits are not listed
+            if (r.m >= least) {
 #pragma unroll 1
                 for (int turn = 0; turn < turns; ++turn) {
-                    const float most = turn_max[turn * kThreads + tid];
-                    if (!(most >= bound) || most == -INFINITY) continue;
-                    load(x, turn);
-#pragma unroll
+                    if (!(turn_max[turn * kThreads + tid] >= least)) continue;
+#pragma unroll 1
                     for (int k = 0; k < kTurn; ++k) {
-                        const Logits<F32> l(x[k]);
+                        const uint4 v = load1(turn * kTurnVectors + k * kThreads + tid);
+                        if (!(vector_max<F32>(v) >= least)) continue;
+                        const int id = first_id + (turn * kTurnVectors + k * kThreads + tid) * kN;
+                        const Logits<F32> l(v);
 #pragma unroll
                         for (int e = 0; e < kN; ++e)
-                            if (l.x[e] >= bound && l.x[e] > -INFINITY) {
+                            if (l.x[e] >= least) {
                                 const int at = atomicAdd(&listed_s, 1);
-                                if (at < kList)
-                                    list[at] = pack_key(l.x[e], (uint32_t)(first_id + (turn * kTurnVectors + k * kThreads + tid) * kN + e));
+                                if (at < kList) list[at] = pack_key(l.x[e], (uint32_t)(id + e));
                             }
                     }
                 }
