@@ -18,10 +18,11 @@
 // ln p = (d - log2 Z) ln 2, entropy = (log2 Z - S / Z) ln 2.
 //
 // Bound by instructions: some 60 for 256 logits in the stream.  576 rows of 129280 BF16
-// logits, an eighth of them left out, with 20 alternatives (130 MB) take 45 us, 43% of
-// the copy rate; 9 rows in clusters of 8 blocks 11.4 us.  (Slices in shared memory and
-// read three times took 111 us, slices in registers with a bound for the cluster 86;
-// the latter 9.0 us for 9 rows.)
+// logits, an eighth of them left out, with 20 alternatives (130 MB) take 44 us, 44% of
+// the copy rate; 9 rows in clusters of 8 blocks 11.3 us.  (Slices in shared memory and
+// read three times took 111 us, slices in registers with a bound for the cluster 86,
+// 9 rows 9.0; the stream without the next turn on its way 45.4, one logit an
+// instruction 44.8 to 45.9; against the maximum of the turn before it takes no less.)
 #include <atomic>
 #include <cmath>
 #include <cstddef>

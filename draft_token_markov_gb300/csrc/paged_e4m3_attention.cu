@@ -49,7 +49,7 @@ constexpr int kManyThreads = 512;
 constexpr int kRing = 4;                     // items that are known ahead
 constexpr int kTileRows = 128, kTileShift = 7;   // keys of a tile, and rows
 constexpr int kGrains = kTileRows / 16;          // groups of 16 keys of a tile, a scale each
-constexpr int kScaleRing = 8;                // tiles whose scales are kept; five at most are in use
+constexpr int kScaleRing = 8;                // tiles whose scales are kept; seven at most are in use (four with D = 128)
 // an item's start and end, in tiles of one and of two row tiles.  In us, for 16 rows of
 // 1-500 tokens (7 query heads a key head), 24 rows of 1-300 (8) and 32 rows of 9 tokens:
 // 3 and 10 109, 123, 90; 3 and 7 108, 131, 90; 4 and 9 105, 127, 93; 6 and 12 112, 124, 97
@@ -296,7 +296,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
         uint32_t stage, phase;
     };
 
-    // 256 x 184 + 256 x 72 registers of the 512 x 128 at launch
+    // 256 x 192 + 256 x 64 registers of the 512 x 128 at launch
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 15) {
         // ------------------------------------------- the walk, query loads

@@ -666,8 +666,9 @@ markov_status markov_rotary(markov_rotary_plan *plan, const void *q, int64_t q_s
  * (page, slot / block, head).  Elements lie at page * s_page + slot * s_slot +
  * head * s_head + d bytes, all three multiples of 16, base 16-byte aligned; scales
  * at page * ss_page + (slot / block) * ss_block + head * ss_head floats, any
- * strides of at least 0 (0 shares a scale, where it is only read).  block is a
- * power of two, 16 .. page_size, so pages have 16 slots at least. */
+ * strides of at least 0 (0 shares a scale, where it is only read); scales are
+ * positive and finite where an element is read.  block is a power of two, 16 ..
+ * page_size, so pages have 16 slots at least. */
 typedef struct markov_e4m3_view {
     void *data;
     int64_t num_pages;
@@ -721,7 +722,8 @@ markov_status markov_paged_read_e4m3(markov_paged_plan *plan, const markov_e4m3_
  * scale.  The 8-bit values enter the tensor cores exactly, as fp16; queries
  * exactly too (BF16 ones times a power of two for each row, which leaves what is
  * below 2^-29 of a row's largest element without some bits); scores, scales,
- * softmax sums and outputs are fp32, the weights are rounded to fp16.  Scales of
+ * softmax sums and outputs are fp32; the weights, times their values' scales, are
+ * rounded to fp16 (what is below 2^-21 of a row's largest loses bits).  Scales of
  * values below 2^-60 count as 2^-60.  Two launches. */
 markov_status markov_paged_attention_e4m3(
     markov_paged_plan *plan, const void *q, int64_t q_s0, int64_t q_s1,
