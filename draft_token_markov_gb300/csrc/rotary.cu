@@ -331,8 +331,9 @@ markov_status markov_rotary(markov_rotary_plan *p, const void *q, int64_t q_s0, 
                             void *k_out, int64_t ko_s0, int64_t ko_s1, void *stream) {
     if (!p || num_tokens < 0 || q_heads < 0 || k_heads < 0 || (int64_t)q_heads + k_heads < 1) return MARKOV_EINVAL;
     if (dtype != MARKOV_BF16 && dtype != MARKOV_F16 && dtype != MARKOV_F32) return MARKOV_EINVAL;
+    if ((int64_t)q_heads + k_heads > 4096) return MARKOV_EINVAL;
     const int heads = q_heads + k_heads;
-    if (heads > 4096 || (int64_t)num_tokens * heads > INT32_MAX) return MARKOV_EINVAL;
+    if ((int64_t)num_tokens * heads > INT32_MAX) return MARKOV_EINVAL;
     if (num_tokens == 0) return MARKOV_OK;
     if (!positions) return MARKOV_EINVAL;
     const int size = dtype == MARKOV_F32 ? 4 : 2, per16 = 16 / size;

@@ -652,8 +652,8 @@ void markov_rotary_plan_destroy(markov_rotary_plan *plan);
  *                 they must not overlap them.
  *   positions     int32 [num_tokens] (as markov_paged_layout gives them;
  *                 negative ones turn the other way).
- * EINVAL for a bad shape, stride, alignment or dtype, or 2^31 and more tokens
- * times heads. */
+ * EINVAL for a bad shape, stride, alignment or dtype, more than 4096 heads
+ * together, or 2^31 and more tokens times heads. */
 markov_status markov_rotary(markov_rotary_plan *plan, const void *q, int64_t q_s0, int64_t q_s1,
                             int32_t q_heads, const void *k, int64_t k_s0, int64_t k_s1,
                             int32_t k_heads, markov_dtype dtype, const int32_t *positions,

@@ -183,3 +183,16 @@ def test_refusals(gpu_lib):
     with pytest.raises(ValueError):
         api.RotaryPlan(64, scaling="given")
     plan.close()
+
+
+def test_head_counts_are_refused(gpu_lib):
+    """More heads than 4096 together, and counts whose sum leaves 32 bits."""
+    api = gpu_lib
+    plan = api.RotaryPlan(64)
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.zeros(64, dtype=torch.bfloat16, device="cuda")
+    p, n = x.data_ptr(), pos.data_ptr()
+    for hq, hk in ((4097, 0), (2048, 2049), (2 ** 31 - 1, 0), (2 ** 31 - 1, 1), (2 ** 31 - 1, 2 ** 31 - 1)):
+        code = api.lib().markov_rotary(plan.handle, p, 64, 64, hq, p, 64, 64, hk, api.MARKOV_BF16, n, 1, p, 64, 64, p, 64, 64, None)
+        assert code == 1                                          # EINVAL
+    plan.close()
