@@ -183,7 +183,7 @@ size_t attention_e4m3_many_parts(int head_dim, int blocks);
 size_t attention_e4m3_many_joins(int blocks);
 // Other calls: k and v are maps of up to 128 slots, q one of 64 elements by a row tile's tokens.
 cudaError_t launch_attention_e4m3_many(const AttnE4m3Args &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                                       int head_dim, bool f16, int blocks, cudaStream_t s);
+                                       int head_dim, bool f16, bool one, int blocks, cudaStream_t s);
 cudaError_t paged_attention_prepare();
 size_t paged_attention_parts(int head_dim, int blocks);
 size_t paged_attention_joins(int blocks);

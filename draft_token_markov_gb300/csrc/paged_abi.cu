@@ -530,6 +530,12 @@ markov_status markov_paged_attention_e4m3(
     // 87, 32 rows 92 and 88; 8 of 1000-16000 keys with 16 rows 39 and 37, 32 rows 44 and 37
     const int64_t query_rows = (int64_t)num_tokens * group;
     const bool few = query_rows <= 16 * (int64_t)rows;
+    // and of many, items of one row tile while a request has no more on average: a place for
+    // another operand, work that spreads.  In us, a pair of row tiles an item and one: 8
+    // rows of 9 tokens (72 query rows a key head) 38.7 and 36.4; 64 of 8 tokens (32) 175 and
+    // 161; 16 of 16 tokens (128) 63 and 59; 24 of 1-40 tokens (164 on average) 98 and 88,
+    // but 16 of 24 tokens (192) 86 and 97, a prompt's 4096 tokens 726 and 955
+    const bool one = query_rows <= 128 * (int64_t)rows;
     CUtensorMap qmap, kmap, vmap;
     const int slots = few ? 32 : 128;
     if (!encode_e4m3_map(&kmap, *k_cache, *p, slots) || !encode_e4m3_map(&vmap, *v_cache, *p, slots) ||
@@ -537,7 +543,7 @@ markov_status markov_paged_attention_e4m3(
         return MARKOV_EINVAL;
     const cudaError_t e =
         few ? launch_attention_e4m3_few(a, kmap, vmap, p->d.head_dim, f16, query_rows <= 8 * (int64_t)rows, p->blocks, s)
-            : launch_attention_e4m3_many(a, qmap, kmap, vmap, p->d.head_dim, f16, p->blocks, s);
+            : launch_attention_e4m3_many(a, qmap, kmap, vmap, p->d.head_dim, f16, one, p->blocks, s);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return MARKOV_ECUDA;

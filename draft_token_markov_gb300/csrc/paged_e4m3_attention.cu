@@ -3,8 +3,8 @@
 //
 // Rows, items, the two slots that take turns on the tensor core and the cut of the
 // call's work into ranges are those of the attention over a 16-bit cache: an item
-// is (request, key head, up to two tiles of 128 stacked query rows), its keys go by
-// in tiles of 128.  Between the loads and the MMAs stands a warpgroup of its own:
+// is (request, key head, up to two tiles of 128 stacked query rows, or one where a
+// request has no more on average), its keys go by in tiles of 128.  Between the loads and the MMAs stands a warpgroup of its own:
 // it reads a tile as TMA brought it (bytes, a row a thread) and writes it as fp16
 // in the operand's swizzled layout, exactly; values that nobody sees become zeros
 // there.  BF16 queries become fp16 ones in place, each row times a power of two
@@ -27,9 +27,9 @@
 // 729 us of what were then 840.  Instructions to fetch counted most: with the conversion
 // loops rolled, one body for keys and values, and negative scales put into the queries,
 // 840 us became 722, and 32 rows of 9 tokens over 500 to 16000 keys 117 us 90.  8 rows of
-// 9 tokens over 1000 to 16000 keys take 38.5 us in a graph (74 MB, 11 us at the copy
-// rate): start, conversion of every tile by one warpgroup (some 1300 cycles for keys and
-// values), ends, the join.
+// 9 tokens over 1000 to 16000 keys take 36 us in a graph (74 MB, 11 us at the copy
+// rate; 38.7 us with pairs of row tiles): some 17 us for start, ends and the join, the
+// rest conversion of every tile by one warpgroup (some 1300 cycles for keys and values).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -49,7 +49,7 @@ constexpr int kManyThreads = 512;
 constexpr int kRing = 4;                     // items that are known ahead
 constexpr int kTileRows = 128, kTileShift = 7;   // keys of a tile, and rows
 constexpr int kGrains = kTileRows / 16;          // groups of 16 keys of a tile, a scale each
-constexpr int kScaleRing = 8;                // tiles whose scales are kept; seven at most are in use (four with D = 128)
+constexpr int kScaleRing = 8;                // tiles whose scales are kept; eight at most are in use (five with D = 128)
 // an item's start and end, in tiles of one and of two row tiles.  In us, for 16 rows of
 // 1-500 tokens (7 query heads a key head), 24 rows of 1-300 (8) and 32 rows of 9 tokens:
 // 3 and 10 109, 123, 90; 3 and 7 108, 131, 90; 4 and 9 105, 127, 93; 6 and 12 112, 124, 97
@@ -57,14 +57,17 @@ constexpr int kWeightOne = 3, kWeightTwo = 10;
 constexpr uint64_t kUnitNs = 20000;          // what a unit of work may take at most
 constexpr uint32_t kReaders = 15;            // warps that read an item
 
-template <int D>
+// ONE: items are of one row tile, whose queries take the place of one tile; the other's
+// is an operand's.
+template <int D, bool ONE>
 struct Shape {
+    static constexpr int kQueries = ONE ? 1 : 2;                 // tiles of queries
     static constexpr int kHalf = kTileRows * 128;                // 64 elements of every row
     static constexpr int kHalves = D / 64;
     static constexpr int kOperand = kTileRows * D * 2;           // a tile of queries, or of keys or values in fp16
     static constexpr int kRaw = kTileRows * D;                   // one of keys or values in e4m3
-    static constexpr int kOperands = D == 128 ? 3 : 5, kRaws = D == 128 ? 4 : 8;
-    static constexpr int kOperandAt = 2 * kOperand;
+    static constexpr int kOperands = (D == 128 ? 5 : 7) - kQueries, kRaws = D == 128 ? 4 : 8;
+    static constexpr int kOperandAt = kQueries * kOperand;
     static constexpr int kRawAt = kOperandAt + kOperands * kOperand;
     static constexpr int kExchange = kRawAt + kRaws * kRaw;
     static constexpr int kScales = kExchange + 2 * kTileRows * 4;
@@ -73,7 +76,8 @@ struct Shape {
     static constexpr int kMisc = kBars + 8 * (2 * kOperands + 2 * kRaws + 15 + 2 * kRing);
     static constexpr int kSmem = kMisc + 256;
 };
-static_assert(Shape<128>::kSmem <= 232448 && Shape<64>::kSmem <= 232448, "shared memory");
+static_assert(Shape<128, false>::kSmem <= 232448 && Shape<64, false>::kSmem <= 232448, "shared memory");
+static_assert(Shape<128, true>::kSmem <= 232448 && Shape<64, true>::kSmem <= 232448, "shared memory");
 
 struct Item {
     int tokens, t0;            // tokens of the item (0: no more items), the first within the request
@@ -98,10 +102,12 @@ struct Join {
     int token, tokens, head;   // its first token, its tokens, its first query head
 };
 
-// The m-th pair of row tiles of a request.
+// The m-th item of a request's key head: a pair of row tiles, or one.
+template <bool ONE>
 __device__ __forceinline__ void span(const AttnE4m3Args &a, const RowOfCall &q, int m, Item &it) {
-    it.t0 = m * 2 * a.tile_tokens;
-    it.tokens = min(q.np - it.t0, 2 * a.tile_tokens);
+    const int most = ONE ? a.tile_tokens : 2 * a.tile_tokens;
+    it.t0 = m * most;
+    it.tokens = min(q.np - it.t0, most);
     const int p0 = q.pos0 + it.t0;
     const KeySpan s = key_span<kTileShift>(a.r, a.window, a.sinks, q.state, p0, p0 + it.tokens - 1);
     it.end = s.end;
@@ -127,13 +133,16 @@ __device__ __forceinline__ int tile_at(const AttnE4m3Args &a, const Item &it, ui
     return past <= 0 ? 0 : min(past / tile_weight(a, it), max(it.steps, 1));
 }
 // The weight of an item and its key tiles.
+template <bool ONE>
 __device__ __noinline__ uint2 units_of(const AttnE4m3Args &a, RowOfCall q, int m) {
     Item it;
-    span(a, q, m, it);
+    span<ONE>(a, q, m, it);
     return make_uint2(weight(a, it), it.steps);
 }
-__device__ __forceinline__ int pairs_of(const AttnE4m3Args &a, const RowOfCall &q) {
-    return (q.np + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+template <bool ONE>
+__device__ __forceinline__ int items_of(const AttnE4m3Args &a, const RowOfCall &q) {
+    const int most = ONE ? a.tile_tokens : 2 * a.tile_tokens;
+    return (q.np + most - 1) / most;
 }
 
 // An item's part from a block, for one slot: [D / 4][128 rows] vectors of four
@@ -220,11 +229,12 @@ __device__ __forceinline__ int convert_query(uint32_t tile, int row, uint32_t si
 
 // ------------------------------------------------------------------ kernel
 
-template <int D, bool F16>
+template <int D, bool F16, bool ONE>
 __global__ void __launch_bounds__(kManyThreads, 1)
 attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_constant__ CUtensorMap qmap,
                       const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
-    using S = Shape<D>;
+    using S = Shape<D, ONE>;
+    constexpr uint32_t kQs = S::kQueries;
     extern __shared__ __align__(1024) uint8_t base[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t smem = tc::smem_u32(base), operands = smem + S::kOperandAt, raws = smem + S::kRawAt;
@@ -310,10 +320,10 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
             uint64_t x = 0, y = 0;
             if (r0 + lane < a.r.rows) {
                 const RowOfCall q = row_of_call(a.r, r0 + lane);
-                const int pairs = pairs_of(a, q);
+                const int pairs = items_of<ONE>(a, q);
 #pragma unroll 1
                 for (int m = 0; m < pairs; ++m) {
-                    const uint2 units = units_of(a, q, m);
+                    const uint2 units = units_of<ONE>(a, q, m);
                     x += units.x;
                     y += units.y;
                 }
@@ -355,13 +365,13 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
             }
             const uint64_t before = r ? units_to[r - 1] : 0, units = units_to[r] - before;
             q = row_of_call(a.r, r);
-            pairs = pairs_of(a, q);
+            pairs = items_of<ONE>(a, q);
             const uint64_t head = units / a.kv_heads;
             h = (int)((u0 - before) / head);
             u = before + h * head;
 #pragma unroll 1
             for (;; ++m) {
-                const uint32_t w = units_of(a, q, m).x;
+                const uint32_t w = units_of<ONE>(a, q, m).x;
                 if (u0 - u < w) break;
                 u += w;
             }
@@ -380,7 +390,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
             q_tiles = 0;
             bool more = false;
             while (!more && u < u_end) {
-                span(a, q, m, it);
+                span<ONE>(a, q, m, it);
                 const uint32_t units = weight(a, it), w = tile_weight(a, it);
                 const int all = max(it.steps, 1);
                 it.j0 = tile_at(a, it, skip);
@@ -414,7 +424,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
                             do {
                                 q = row_of_call(a.r, ++r);
                             } while (q.np <= 0);
-                            pairs = pairs_of(a, q);
+                            pairs = items_of<ONE>(a, q);
                         }
                     }
                 }
@@ -434,8 +444,8 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
             }
 #pragma unroll 1
             for (int s = 0; s < tiles; ++s, token += a.tile_tokens) {
-                const uint32_t buf = qt & 1, full = q_full + 8 * buf;
-                ok = all_wait(q_empty + 8 * buf, (qt >> 1 & 1) ^ 1, 0x300 + buf, limit_ns);
+                const uint32_t buf = qt % kQs, full = q_full + 8 * buf;
+                ok = all_wait(q_empty + 8 * buf, (qt / kQs & 1) ^ 1, 0x300 + buf, limit_ns);
                 if (!ok) break;
                 ++qt;
                 if (lane == 0) {
@@ -452,8 +462,8 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
         if (lane == 0 && sh.abort) {
             // gave up: no load may be in flight when the block leaves
             const uint64_t until = tc::now_ns() + a.timeout_ns;
-            for (uint32_t t = qt > 2 ? qt - 2 : 0; t < qt; ++t)
-                while (!tc::mbar_test(q_full + 8 * (t & 1), t >> 1 & 1) && tc::now_ns() < until) {}
+            for (uint32_t t = qt > kQs ? qt - kQs : 0; t < qt; ++t)
+                while (!tc::mbar_test(q_full + 8 * (t % kQs), t / kQs & 1) && tc::now_ns() < until) {}
         }
     } else if (warp == 13 || warp == 14) {
         // ------------------------------------------------ key / value loads
@@ -545,7 +555,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
         };
         auto loaded = [&](Place k) { return step_wait(op_full + 8 * k.stage, k.phase, 0x200); };
         auto scores = [&](int slot, uint32_t tile, Place k) {
-            mma_scores<D>(tmem + slot * kTileRows, q_desc + (tile & 1) * kStep, k_desc + k.stage * kStep, kIdescS);
+            mma_scores<D>(tmem + slot * kTileRows, q_desc + tile % kQs * kStep, k_desc + k.stage * kStep, kIdescS);
             tc::commit_elect(s_full + 8 * slot);
         };
         // O += P V, once the slot's P is there
@@ -558,7 +568,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
         };
         auto release = [&](Place k) { tc::commit_elect(op_empty + 8 * k.stage); };
         auto queries = [&](uint32_t tile) {
-            return step_wait((F16 && a.scale2 >= 0.0f ? q_full : q_ready) + 8 * (tile & 1), tile >> 1 & 1, 0x210 + (tile & 1));
+            return step_wait((F16 && a.scale2 >= 0.0f ? q_full : q_ready) + 8 * (tile % kQs), tile / kQs & 1, 0x210 + tile % kQs);
         };
         Place k{0, 0};                               // the next key tile for scores
         for (uint32_t n = 0; ok; ++n) {
@@ -570,7 +580,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
             // Either way a slot's turn is: its P comes, O += P V, the next scores
             // over P's place (MMAs run in the order of their issue).
             Place v = after(k, 1);
-            if (tokens > a.tile_tokens) {
+            if (!ONE && tokens > a.tile_tokens) {
                 // two row tiles, a slot each, every key tile for both
                 ok = queries(qt) && loaded(k);
                 if (!ok) break;
@@ -597,8 +607,8 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
                     k = after(k, 2);
                 }
                 if (!ok) break;
-                tc::commit_elect(q_empty + 8 * (qt & 1));
-                tc::commit_elect(q_empty + 8 * (qt + 1 & 1));
+                tc::commit_elect(q_empty + 8 * (qt % kQs));
+                tc::commit_elect(q_empty + 8 * ((qt + 1) % kQs));
                 qt += 2;
                 ok = loaded(v);
 #pragma unroll 1
@@ -619,7 +629,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
                     release(k);
                     k = after(k, 2);
                 }
-                if (steps <= 2) tc::commit_elect(q_empty + 8 * (qt & 1));
+                if (steps <= 2) tc::commit_elect(q_empty + 8 * (qt % kQs));
 #pragma unroll 1
                 for (int j = 0; ok && j < steps; ++j) {
                     ok = loaded(v) && values(j & 1, v, j > 1);
@@ -632,7 +642,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
                         tc::fence_after_sync();
                         scores(j & 1, qt, k);
                         release(k);
-                        if (j + 3 == steps) tc::commit_elect(q_empty + 8 * (qt & 1));
+                        if (j + 3 == steps) tc::commit_elect(q_empty + 8 * (qt % kQs));
                         k = after(k, 2);
                     } else {
                         tc::commit_elect(pv_done + 8 * (j & 1));
@@ -668,19 +678,19 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
             ok = item_wait(n);
             const volatile Item &it = item(n);
             if (!ok || it.tokens == 0) break;
-            const int tiles = it.tokens > a.tile_tokens ? 2 : 1, steps = it.steps;
+            const int tiles = !ONE && it.tokens > a.tile_tokens ? 2 : 1, steps = it.steps;
             const int j0 = it.j0, sinks = it.sink_tiles, w0 = it.w0, end = it.end, first = it.first, kept = it.kept;
             item_done(n);
             if (steps <= 0) continue;
             if (!F16 || a.scale2 < 0.0f) {
 #pragma unroll 1
                 for (int s = 0; s < tiles; ++s, ++qt) {
-                    ok = step_wait(q_full + 8 * (qt & 1), qt >> 1 & 1, 0x840);
+                    ok = step_wait(q_full + 8 * (qt % kQs), qt / kQs & 1, 0x840);
                     if (!ok) break;
-                    const int k = convert_query<D, F16>(smem + (qt & 1) * S::kOperand, row, a.scale2 < 0.0f ? 0x80008000u : 0u);
+                    const int k = convert_query<D, F16>(smem + qt % kQs * S::kOperand, row, a.scale2 < 0.0f ? 0x80008000u : 0u);
                     row_exp[(qt & 3) * kTileRows + row] = (uint8_t)(k + 127);
                     tc::fence_proxy_async_smem();
-                    arrive(q_ready + 8 * (qt & 1));
+                    arrive(q_ready + 8 * (qt % kQs));
                 }
             }
             // keys and values in turn, by the same code
@@ -703,7 +713,7 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
             ok = item_wait(n);
             const volatile Item &it = item(n);
             if (!ok || it.tokens == 0) break;
-            const bool two = it.tokens > a.tile_tokens;
+            const bool two = !ONE && it.tokens > a.tile_tokens;
             const int t0 = it.t0 + (two ? slot * a.tile_tokens : 0);
             const int tokens = min(it.tokens + it.t0 - t0, a.tile_tokens), rows = tokens * a.group;
             const int steps = it.steps, ahead = two ? 1 : 2;
@@ -1013,10 +1023,10 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (k0 == 0 && a.lse) a.lse[token * a.q_heads + head] = lse_of(M, L);
 }
 
-template <int D, bool F16>
+template <int D, bool F16, bool ONE>
 cudaError_t launch_typed(const AttnE4m3Args &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v, int blocks,
                          cudaStream_t s) {
-    attention_e4m3_kernel<D, F16><<<blocks, kManyThreads, Shape<D>::kSmem, s>>>(a, q, k, v);
+    attention_e4m3_kernel<D, F16, ONE><<<blocks, kManyThreads, Shape<D, ONE>::kSmem, s>>>(a, q, k, v);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
@@ -1034,21 +1044,31 @@ cudaError_t launch_typed(const AttnE4m3Args &a, const CUtensorMap &q, const CUte
 }  // namespace
 
 cudaError_t launch_attention_e4m3_many(const AttnE4m3Args &a, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                                       int head_dim, bool f16, int blocks, cudaStream_t s) {
-    if (head_dim == 64)
-        return f16 ? launch_typed<64, true>(a, q, k, v, blocks, s) : launch_typed<64, false>(a, q, k, v, blocks, s);
-    return f16 ? launch_typed<128, true>(a, q, k, v, blocks, s) : launch_typed<128, false>(a, q, k, v, blocks, s);
+                                       int head_dim, bool f16, bool one, int blocks, cudaStream_t s) {
+    const auto launch = head_dim == 64 ? f16 ? one ? launch_typed<64, true, true> : launch_typed<64, true, false>
+                                             : one ? launch_typed<64, false, true> : launch_typed<64, false, false>
+                                       : f16 ? one ? launch_typed<128, true, true> : launch_typed<128, true, false>
+                                             : one ? launch_typed<128, false, true> : launch_typed<128, false, false>;
+    return launch(a, q, k, v, blocks, s);
 }
 
+namespace {
+
+template <int D, bool ONE>
+cudaError_t prepare() {
+    for (const void *fn : {(const void *)attention_e4m3_kernel<D, false, ONE>, (const void *)attention_e4m3_kernel<D, true, ONE>}) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<D, ONE>::kSmem);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
 cudaError_t attention_e4m3_many_prepare() {
-    const auto set = [](const void *fn, int bytes) {
-        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    };
-    cudaError_t e = set((const void *)attention_e4m3_kernel<64, false>, Shape<64>::kSmem);
-    if (e == cudaSuccess) e = set((const void *)attention_e4m3_kernel<64, true>, Shape<64>::kSmem);
-    if (e == cudaSuccess) e = set((const void *)attention_e4m3_kernel<128, false>, Shape<128>::kSmem);
-    if (e == cudaSuccess) e = set((const void *)attention_e4m3_kernel<128, true>, Shape<128>::kSmem);
-    return e;
+    for (const cudaError_t e : {prepare<64, false>(), prepare<64, true>(), prepare<128, false>(), prepare<128, true>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 // Floats of the parts that `blocks` blocks may leave, bytes of their joins.

@@ -269,6 +269,31 @@ def both(api, case, **kw):
     check(case, out, lse, **kw)
 
 
+# requests of one and of several row tiles, around an average of 128 query rows a request
+_ROW_TILES = {
+    "one tile each": [(3000, 16), (0, 1), (700, 9), (64, 16), (5000, 11)],
+    "many rows, some alone": [(300, 100), (10, 1), (2000, 1), (0, 1), (129, 3), (127, 1), (40, 2), (900, 1)],
+    "above the average": [(3000, 17), (100, 40), (1500, 33)],
+    "a lone request of two tiles": [(9000, 32)],
+    "a lone request of one tile": [(9000, 16)],
+    "short ones": [(0, 16), (0, 5), (1, 12), (15, 16)],
+}
+
+
+@pytest.mark.parametrize("d,dtype,scale", [(128, torch.bfloat16, None), (128, torch.float16, -0.1), (64, torch.bfloat16, -0.2),
+                                           (64, torch.float16, None)])
+@pytest.mark.parametrize("reqs", list(_ROW_TILES.values()), ids=list(_ROW_TILES))
+def test_row_tiles_of_an_item(gpu_lib, reqs, d, dtype, scale):
+    both(gpu_lib, Case(reqs, 16, 2, d, 32, 16, dtype=dtype, seed=len(reqs)), scale=scale)
+
+
+def test_padding_rows_change_the_row_tiles_of_an_item(gpu_lib):
+    """40 tokens of 8 heads a request, alone and among rows of padding (no tokens)."""
+    for pad in (0, 1, 5):
+        reqs = [(500, 40), (2500, 40)] + [(0, 0)] * pad
+        both(gpu_lib, Case(reqs, 16, 2, 128, 64, 32, seed=3, padding=tuple(range(2, 2 + pad))), window=700, sinks=5)
+
+
 # ------------------------------------------------------------------- fetch
 
 def _fetch(api, case, T=None, key=None, value=None):
