@@ -526,8 +526,9 @@ markov_status markov_paged_attention_e4m3(
     const cudaStream_t s = (cudaStream_t)stream;
     // Few rows of query heads a request on average: bound by the cache's bytes.  In us,
     // few against many: 64 requests of 500-16000 keys with 16 rows for each of 4 key heads
-    // 70 and 95; 32 of them with 16 rows for each of 8 key heads 68 and 87, 24 rows 88 and
-    // 87, 32 rows 92 and 88; 8 of 1000-16000 keys with 16 rows 39 and 37, 32 rows 44 and 37
+    // 72 and 87; 32 of them with 16 rows for each of 8 key heads 69 and 80, 24 rows 92 and
+    // 81; 8 of 1000-16000 keys with 16 rows 38 and 34, of 32000 keys 106 and 141, 32 rows of
+    // 1000-16000 44 and 35
     const int64_t query_rows = (int64_t)num_tokens * group;
     const bool few = query_rows <= 16 * (int64_t)rows;
     // and of many, items of one row tile while a request has no more on average: a place for

@@ -15,7 +15,7 @@
 // subset); values in pairs of keys by byte permutes.  (Through tcgen05 they would be
 // written to shared memory as fp16 and read from there: 7 bytes of its traffic for each
 // of the cache, more than it has to give at the memory's rate; 64 requests with 16 rows
-// took 95 us that way and 70 here.)
+// take 87 us that way and 72 here.)
 //
 // The maximum that p is taken against moves when a row's grows by more than 2^8
 // (kLazyE4), so that most steps need no exchange between lanes; weights are at most
@@ -32,7 +32,7 @@
 // Bounds.  64 single tokens over 500 to 32000 keys (64 / 8 heads of 128, 0.91 GB) take
 // 150 us, 90% of the copy rate; 163 us with a head's warps on keys of their own, 231 us
 // with lines of 256 bytes, which fetch a neighbouring head's too.  One row's token over
-// 1000 keys takes 11.5 us in a graph: the start, four steps, the join.  With 16 rows the
+// 1000 keys takes 11.4 us in a graph: the start, four steps, the join; over 16000 31 us.  With 16 rows the
 // arithmetic counts: 32 requests of two tokens with 8 heads each 68 us for 37 us of
 // bytes.  8 warps of 250 registers and steps of 32 keys; 12 warps of 168 and steps of 16
 // took 186 us where these took 166.
@@ -58,6 +58,11 @@ constexpr int kStepShift = 5;
 // 150.9; 1 and 1 12.9 and 155.2
 constexpr int kEnds = 2;
 constexpr int kLeast = 2;
+// What a part costs the join, in a warp's steps: a range has sqrt(kPartCost * an item's
+// units) or more, where steps and joins cost the same.  0 and 0.25: a row's token over
+// 16000 keys (8 key heads) 39 and 31 us, 32 requests of 500-8000 keys with 16 rows (one
+// key head) 31 and 23 us, calls whose ranges are longer anyway the same.
+constexpr float kPartCost = 0.25f;
 
 template <int D>
 struct FewShape {
@@ -195,9 +200,17 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
     };
     FewJoin join{0, 0, 0, 0, 0, 0, 0};
     uint64_t total = 0;
+    uint32_t items = 0;                                      // of one key head
 #pragma unroll 1
     for (int r0 = 0; r0 < a.r.rows; r0 += 32) {
-        uint64_t x = r0 + lane < a.r.rows ? units_of(row_of_call(a.r, r0 + lane)) : 0;
+        uint64_t x = 0;
+        uint32_t n = 0;
+        if (r0 + lane < a.r.rows) {
+            const RowOfCall mine = row_of_call(a.r, r0 + lane);
+            x = units_of(mine);
+            n = tiles_of(mine);
+        }
+        items += __reduce_add_sync(0xffffffffu, n);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         total += x;
@@ -206,8 +219,11 @@ attention_e4m3_few_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_c
         if (tid == 0 && !pending) set_status(a.status, 2u /* MARKOV_EUNSUPPORTED */, 0x700);
         total = 0;
     }
+    // the parts of an item are joined one after the other: few of them where it is long
+    const float mean = (float)total / (float)max(items, 1u);
+    const uint32_t least = max(kLeast, (int)sqrtf(mean * kPartCost));
     UnitSplit split;
-    split.cut(pending ? 0 : total * head_groups, ranges, kLeast);
+    split.cut(pending ? 0 : total * head_groups, ranges, least);
     if (range >= split.ranges) {
         if (lane == 0) reinterpret_cast<FewJoin *>(a.joins)[worker] = join;
         return;
@@ -574,8 +590,9 @@ constexpr int kFewJoinParts = 8;             // loads in flight
 
 // Block w: the item that begins in worker w's range and is cut; a thread has four
 // columns of a row.  Latency, of its loads kFewJoinParts at a time: a request of 16000
-// keys may have 70 parts (four at a time and 128 threads took 40 us of a call of 8
-// requests).  Blocks for 32 columns each cost one row's token 2 us: most have nothing
+// keys may have 50 parts (sixteen at a time take one row's token over them in 29.4 us for
+// 30.8, but 32 rows' in 57.7 for 56.5; four at a time and 128 threads took 40 us of a call
+// of 8 requests).  Blocks for 32 columns each cost one row's token 2 us: most have nothing
 // to do.
 template <int D, bool F16, int ROWS>
 __global__ void __launch_bounds__(ROWS * D / 4) few_join_kernel(const __grid_constant__ AttnE4m3Args a) {

@@ -651,3 +651,10 @@ def test_refusals(gpu_lib):
     with pytest.raises(ValueError):
         api.markov_paged_read_e4m3(plan, d["kc"], d["vc"], d["ks"], d["vs"], *rest, 3, key=d["q"][:, :2])
     plan.close()
+
+
+@pytest.mark.parametrize("reqs,hq,hkv", [([(16000, 1)], 8, 1), ([(9000, 2)], 8, 8), ([(7000, 1), (30, 1), (0, 1)], 16, 2)])
+def test_long_items_of_few_rows_are_cut_into_few_parts(gpu_lib, reqs, hq, hkv):
+    """An item's parts are fewer than the warps there are: by the root of its length."""
+    for d in (64, 128):
+        both(gpu_lib, Case(reqs, hq, hkv, d, 64, 64, seed=hq))
