@@ -193,6 +193,15 @@ __device__ __noinline__ uint4 edge_vector(const uint8_t *from, int id, int vocab
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Rows whose largest |m c| is below this are summed in the fused form.  A thread's d of
+// its own maximum is what M's rounding left out, half a unit of M in its last place: 4
+// at most there, but 128 from |M| = 2^31 on, as for masked logits of -1e10, and then Z is
+// infinite.  M only moves by whole units, so from 2^31 - 128 on every step towards 0
+// has the factor 2^-128 or less, that is 0, and what was summed so far is dropped, not
+// multiplied: no such sum comes back below 2^31, or into a row's where the maximum is
+// below 2^27.
+constexpr float kFused = 134217728.0f;
+
 // A thread's logits so far.
 template <bool F32>
 struct Running {
@@ -209,9 +218,10 @@ struct Running {
         if (!(top <= m) && m == m) {                  // larger, or NaN, which stays
             const float next = top * c, back = M - next;
             if (m != -INFINITY) {
+                // not a product where the weight is 0: see kFused
                 const float f = ex2(back);
-                s = f * fmaf(back, z, s);
-                z *= f;
+                s = f > 0.0f ? f * fmaf(back, z, s) : 0.0f;
+                z = f > 0.0f ? f * z : 0.0f;
             }
             m = top;
             M = next;
@@ -221,7 +231,8 @@ struct Running {
         uint64_t z2[2] = {0, 0}, s2[2] = {0, 0};
 #pragma unroll
         for (int k = 0; k < kTurn; ++k) {
-            // a masked logit's 0 times -inf would be NaN: -1e30 times c weighs 0 too
+            // a masked logit's 0 times -inf would be NaN: -1e30 times c weighs 0 too where
+            // the row's maximum is below kFused / c, and other rows are summed again
             constexpr uint32_t kLow = F32 ? 0xf149f2cau : 0xf149f149u;
             const Logits<F32> l(make_uint4(word_max<F32>(x[k].x, kLow), word_max<F32>(x[k].y, kLow), word_max<F32>(x[k].z, kLow),
                                            word_max<F32>(x[k].w, kLow)));
@@ -359,13 +370,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) m = nan_max(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (lane == 0) warp_f[0][warp] = m;
-    // what the fused form cannot do: scales and logits that leave its range
-    const bool wild = r.m != -INFINITY && !(fabsf(r.M) < 1e30f);
-    const bool plain = __syncthreads_or(wild) || c < 1e-20f || c > 1e7f;
+    __syncthreads();
     m = warp_f[0][0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) m = nan_max(m, warp_f[0][w]);
     const bool odd = !(fabsf(m) < INFINITY);                           // NaN, an infinity, nothing
+    // what the fused form cannot do: scales and logits that leave its range
+    const bool plain = !(fabsf(m * c) < kFused) || c < 1e-20f || c > 1e7f;
     float z = 0.0f, s = 0.0f;
     uint64_t best = 0;
     if (!odd && !plain) {
@@ -373,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             // relative to the slice's maximum, and to m c instead of M
             const float off = fmaf(r.m, c, -r.M), d = fmaf(r.m - m, c, -off), f = ex2(d);
             s = f > 0.0f ? f * fmaf(d, r.z, r.s) : 0.0f;
-            z = f * r.z;
+            z = f > 0.0f ? f * r.z : 0.0f;
         }
     } else if (!odd) {
         each([&](float l, int) {
