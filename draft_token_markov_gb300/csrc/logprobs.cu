@@ -311,8 +311,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     };
     uint4 x[kTurn], y[kTurn];
     const int turns = (vectors + kTurnVectors - 1) / kTurnVectors;
-    if (turns > 0) load(x, 0);                                         // on its way while the token comes
-    if (token64 < 0 || token64 >= a.vocab) return;                     // the whole cluster
+    // the whole cluster, before the first load: a row that is left out is not read
+    if (token64 < 0 || token64 >= a.vocab) return;
+    if (turns > 0) load(x, 0);
     if (blocks > 1) cluster_arrive();                                  // every block runs
     const int token = (int)token64;
     float T = a.temperature ? __ldg(a.temperature + row) : 1.0f;
