@@ -16,8 +16,8 @@
 // weights.  m is the maximum of y and moves when a row's has grown by 2^8 or more.
 //
 // Roles.  Warps 0-3 and 4-7: softmax and output of the two slots, a thread a row;
-// 8-11: conversion; 12: MMAs; 13 and 14: loads of keys and values, with their
-// scales; 15: walks the block's items and loads queries.
+// 8-11: conversion; 12: MMAs; 13 and 14: loads of keys and values, the former with
+// the scales of both; 15: walks the block's items and loads queries.
 //
 // Bounds.  4096 tokens over 16384 keys (32 / 8 heads of 128) take 722 us, 1332 TFLOP/s
 // (68% of the GEMM rate; 660 us over a cache of BF16): a turn of two row tiles over 128
@@ -469,7 +469,6 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
         // ------------------------------------------------ key / value loads
         const bool values = warp == 14;
         const CUtensorMap *map = values ? &vmap : &kmap;
-        const E4m3Scales &sc = values ? a.vs : a.ks;
         const int page = 1 << a.r.page_shift;
         const int box = min(page, kTileRows), boxes = kTileRows / box;       // boxes of a tile
         uint32_t at = values ? 1 : 0;                // in the ring: K V K V ...
@@ -490,12 +489,15 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
                 const int id = __ldg(table + (key >> a.r.page_shift));
                 return id >= 0 && id < a.r.num_pages ? id : -1;
             };
-            // lane g: the scale of the tile's g-th 16 keys, 1 where nobody sees one
+            // lane g: the scale of the tile's g-th 16 keys, lane kGrains + g: of their
+            // values, 1 where nobody sees one.  Both are the keys' warp's: the softmax reads
+            // them once a tile's scores are done, which wait for its keys, not for its values
             auto scale_of = [&](int j, int pids) {
-                const int id = __shfl_sync(0xffffffffu, pids, (lane & (kGrains - 1)) * 16 / box);
-                if (j >= j1 || lane >= kGrains) return 1.0f;
-                const int key = key_of(j) + lane * 16;
+                const int g = lane & (kGrains - 1), id = __shfl_sync(0xffffffffu, pids, g * 16 / box);
+                if (values || j >= j1 || lane >= 2 * kGrains) return 1.0f;
+                const int key = key_of(j) + g * 16;
                 if (id < 0 || !seen(key, 16)) return 1.0f;
+                const E4m3Scales &sc = lane < kGrains ? a.ks : a.vs;
                 return __ldg(sc.p + id * sc.s_page + ((key & (page - 1)) >> sc.block_shift) * sc.s_block + h * sc.s_head);
             };
             int pid = page_of(j0), pid_next = page_of(j0 + 1);
@@ -505,17 +507,17 @@ attention_e4m3_kernel(const __grid_constant__ AttnE4m3Args a, const __grid_const
                 const uint32_t stage = at % S::kRaws, phase = at / S::kRaws & 1, full = raw_full + 8 * stage;
                 ok = step_wait(raw_empty + 8 * stage, phase ^ 1, 0x100 + stage);
                 if (!ok) break;
-                if (lane < kGrains) {
+                if (!values && lane < 2 * kGrains) {
                     float *to = scales + (at / 2 % kScaleRing) * 3 * kGrains + lane;
-                    if (values) {
-                        const float lv = scale_log2(scale);
-                        to[kGrains] = lv;
-                        to[2 * kGrains] = ex2(-lv);
-                    } else {
+                    if (lane < kGrains) {
                         to[0] = fmaxf(scale, 1e-30f);        // positive: a masked score stays -inf
+                    } else {
+                        const float lv = scale_log2(scale);
+                        to[0] = lv;
+                        to[kGrains] = ex2(-lv);
                     }
                 }
-                __syncwarp();
+                __syncwarp();                                // before the arrival that the scores wait for
                 if (lane == 0) tc::mbar_expect_tx(full, S::kRaw);
                 __syncwarp();
                 // the whole warp goes through the boxes, an elected lane issues

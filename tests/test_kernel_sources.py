@@ -18,3 +18,15 @@ def test_logits_of_a_row_that_is_left_out_are_not_read():
     body = _body("logprobs.cu", "uint4 x[kTurn], y[kTurn];", " the stream\n")
     leave = body.index("if (token64 < 0 || token64 >= a.vocab) return;")
     assert leave < body.index("load(x, 0)") and "load" not in body[:leave].replace("before the first load", "")
+
+
+def test_scales_of_a_tile_are_written_by_the_warp_whose_barrier_its_scores_wait_for():
+    """The softmax reads a tile's scales, of keys and of values, once its scores are done;
+    those wait for the keys' barrier alone, so the warp that arrives there after its
+    stores has to have made them all."""
+    body = _body("paged_e4m3_attention.cu", "key / value loads", "MMA issue")
+    guard = body.index("if (!values && ")
+    at, arrive = body.index("= scales + "), body.index("mbar_expect_tx(full")
+    assert guard < at < body.index("__syncwarp();", at) < arrive and body.count("= scales + ") == 1
+    text = open(os.path.join(CSRC, "paged_e4m3_attention.cu")).read()
+    assert text.count("= scales + ") == 2                # the other is the softmax's
