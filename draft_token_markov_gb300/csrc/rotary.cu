@@ -305,8 +305,11 @@ markov_status markov_rotary_plan_create(const markov_rotary_desc *desc, markov_r
     uint64_t turns[256];
     const int pairs = d.rot_dim / 2;
     for (int i = 0; i < pairs; ++i) turns[i] = turns_of(frequency(d, i));
+    // a copy from pageable memory may return before it has arrived, and the plan's calls run
+    // on streams that do not wait for the default one
     if (cudaMalloc(&p->turns, pairs * sizeof(uint64_t)) != cudaSuccess ||
-        cudaMemcpy(p->turns, turns, pairs * sizeof(uint64_t), cudaMemcpyHostToDevice) != cudaSuccess) {
+        cudaMemcpy(p->turns, turns, pairs * sizeof(uint64_t), cudaMemcpyHostToDevice) != cudaSuccess ||
+        cudaStreamSynchronize(nullptr) != cudaSuccess) {
         cudaGetLastError();
         if (p->turns) cudaFree(p->turns);
         delete p;

@@ -30,3 +30,10 @@ def test_scales_of_a_tile_are_written_by_the_warp_whose_barrier_its_scores_wait_
     assert guard < at < body.index("__syncwarp();", at) < arrive and body.count("= scales + ") == 1
     text = open(os.path.join(CSRC, "paged_e4m3_attention.cu")).read()
     assert text.count("= scales + ") == 2                # the other is the softmax's
+
+
+def test_a_rotary_plans_frequencies_have_arrived_when_it_is_there():
+    """A copy from pageable memory may return before it is done, and a call's stream need
+    not wait for the default one."""
+    body = _body("rotary.cu", "markov_status markov_rotary_plan_create", "markov_status markov_rotary(")
+    assert body.index("cudaMemcpy(p->turns") < body.index("cudaStreamSynchronize(nullptr)") < body.index("*out = p;")
