@@ -123,6 +123,8 @@ __device__ __forceinline__ void store_run(const StoreArgs &a, const StoreSide &s
         top = top_s[0];
 #pragma unroll
         for (int w = 1; w < TEAM / 32; ++w) top = max(top, top_s[w]);
+    } else {
+        __syncwarp();                                 // likewise: a reduction orders no memory
     }
     float s = scale_of(F16 ? __half2float(__ushort_as_half((unsigned short)top)) : __uint_as_float(top << 16));
     // the block's first entry of the head

@@ -37,3 +37,12 @@ def test_a_rotary_plans_frequencies_have_arrived_when_it_is_there():
     not wait for the default one."""
     body = _body("rotary.cu", "markov_status markov_rotary_plan_create", "markov_status markov_rotary(")
     assert body.index("cudaMemcpy(p->turns") < body.index("cudaStreamSynchronize(nullptr)") < body.index("*out = p;")
+
+
+def test_a_blocks_old_scale_is_read_before_a_thread_writes_the_new_one():
+    """By a thread block behind its barrier, by a warp behind its own."""
+    body = _body("paged_e4m3.cu", "__device__ __forceinline__ void store_run(", "if (tid == 0) *scale = s;")
+    read = body.index("old = __ldcg(scale)")
+    both = body[body.index("if (TEAM > 32) {", read):body.index("float s = scale_of(", read)]
+    block, warp = both.split("} else {")
+    assert "__syncthreads();" in block and "__syncwarp();" in warp
