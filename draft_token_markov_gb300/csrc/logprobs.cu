@@ -193,6 +193,13 @@ __device__ __noinline__ uint4 edge_vector(const uint8_t *from, int id, int vocab
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// (l - m) c.  The difference of a very negative logit to a large maximum may leave the
+// range of fp32 where its product with c does not; the products' signs differ then.
+__device__ __forceinline__ float scaled(float l, float m, float c) {
+    const float x = l - m;
+    return x > -INFINITY || l == -INFINITY ? x * c : __fmul_rn(l, c) - __fmul_rn(m, c);
+}
+
 // Rows whose largest |m c| is below this are summed in the fused form.  A thread's d of
 // its own maximum is what M's rounding left out, half a unit of M in its last place: 4
 // at most there, but 128 from |M| = 2^31 on, as for masked logits of -1e10, and then Z is
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         }
     } else if (!odd) {
         each([&](float l, int) {
-            const float d = (l - m) * c, p = ex2(d);
+            const float d = scaled(l, m, c), p = ex2(d);
             z += p;
             s += d > -1024.0f ? p * d : 0.0f;
         });
@@ -581,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
         before += p.before;
         best = p.best > best ? p.best : best;
         if (one_hot || p.m == -INFINITY) continue;
-        const float d = (p.m - all) * c, f = ex2(d);
+        const float d = scaled(p.m, all, c), f = ex2(d);
         z += p.z * f;
         s += f > 0.0f ? f * (p.s + d * p.z) : 0.0f;
     }
@@ -589,9 +596,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
     const auto log_p = [&](float l, int id) {
         if (one_hot) return id == (int)packed_id(best) ? 0.0f : -INFINITY;
         if (l == -INFINITY) return l;
-        const float d = (l - all) * c;
-        // a logit of the type's lowest value leaves the range of d
-        return d > -INFINITY ? (d - log_z) * kLn2 : __fdiv_rn(l - all, T);
+        const float x = l - all, d = scaled(l, all, c);
+        if (d > -INFINITY) return (d - log_z) * kLn2;
+        // a logit of the type's lowest value leaves the range of d (and of x: see scaled)
+        return x > -INFINITY ? __fdiv_rn(x, T) : __fdiv_rn(l, T) - __fdiv_rn(all, T);
     };
     if (tid == 0) {
         if (a.logprobs && a.tokens) a.logprobs[row] = log_p(own, (int)token);

@@ -108,3 +108,34 @@ def test_a_thread_may_meet_masks_first_or_last(gpu_lib):
         tokens = torch.randint(0, V, (len(l),), generator=g, device="cuda")
         for copies in (1, 60):
             _check(gpu_lib, l, tokens, T, copies=copies)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("top", [1e37, 3.3e38, -2e38])
+def test_differences_that_leave_the_range_of_fp32(gpu_lib, dtype, top):
+    """The lowest value's distance to the maximum need not be a float where the log
+    probability is one."""
+    lowest = torch.finfo(dtype).min
+    l = torch.full((6, 3000), lowest, dtype=dtype, device="cuda")
+    l[:, 7::500] = top
+    T = torch.tensor([1.0, 2.0, 5.5, 9.0, 0.5, 0.01], device="cuda")
+    for token in (0, 7, 2999):
+        _check(gpu_lib, l, torch.full((6,), token, device="cuda"), T, top=9, copies=1)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_uniform_over_finite_masks_too(gpu_lib, dtype):
+    """T = +inf: every logit but -inf counts alike, however far from the maximum; one block
+    of a cluster may have nothing but masks."""
+    l = torch.full((3, V), torch.finfo(dtype).min, dtype=dtype, device="cuda")
+    l[:, :100] = 3e38
+    l[1, 5000:] = -math.inf
+    l[2, 50:V - 7] = -math.inf
+    T = torch.full((3,), math.inf, device="cuda")
+    for copies in (1, 150):
+        got = gpu_lib.markov_logprobs(l.repeat(copies, 1), torch.full((3 * copies,), 49, device="cuda"), T.repeat(copies), 3)
+        for i, n in enumerate((V, 5000, 57)):
+            # the logarithm of a count: 2^-20 and two roundings of it
+            tol = 2.0 ** -20 + 2.0 ** -22 * math.log(n)
+            for x, want in ((got.logprobs, -math.log(n)), (got.entropy, math.log(n)), (got.top_logprobs[:, 2], -math.log(n))):
+                assert float((x[i::3].double() - want).abs().max()) <= tol, (i, n)
