@@ -395,10 +395,18 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const __grid_cons
             z = f > 0.0f ? f * r.z : 0.0f;
         }
     } else if (!odd) {
+        // a thread's terms one after the other, often equal ones: what a sum's rounding
+        // leaves out is kept and goes into the next
+        float z_off = 0.0f, s_off = 0.0f;
+        const auto add = [](float &sum, float &off, float x) {
+            const float y = __fadd_rn(x, -off), t = __fadd_rn(sum, y);
+            off = __fadd_rn(__fadd_rn(t, -sum), -y);
+            sum = t;
+        };
         each([&](float l, int) {
             const float d = scaled(l, m, c), p = ex2(d);
-            z += p;
-            s += d > -1024.0f ? p * d : 0.0f;
+            add(z, z_off, p);
+            add(s, s_off, d > -1024.0f ? p * d : 0.0f);
         });
     }
     const bool by_key = a.tokens && (odd || !ranked);                  // NaN or an infinity in the comparison

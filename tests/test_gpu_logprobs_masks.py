@@ -139,3 +139,15 @@ def test_uniform_over_finite_masks_too(gpu_lib, dtype):
             tol = 2.0 ** -20 + 2.0 ** -22 * math.log(n)
             for x, want in ((got.logprobs, -math.log(n)), (got.entropy, math.log(n)), (got.top_logprobs[:, 2], -math.log(n))):
                 assert float((x[i::3].double() - want).abs().max()) <= tol, (i, n)
+
+
+@pytest.mark.parametrize("base", [1e8, -1e8, 4e8])
+def test_many_equal_logits_far_from_zero(gpu_lib, base):
+    """fp32 logits a few units in the last place apart: sums of many equal terms."""
+    g = torch.Generator(device="cuda").manual_seed(14)
+    l = (torch.randn((8, V), generator=g, device="cuda").double() + base).float()
+    l[4:, ::7] = -1e9
+    T = torch.tensor([0.46, 0.55, 0.63, 0.68, 0.69, 0.91, 0.98, 0.5], device="cuda")
+    tokens = torch.randint(0, V, (8,), generator=g, device="cuda")
+    for copies in (1, 50):
+        _check(gpu_lib, l, tokens, T, copies=copies)
