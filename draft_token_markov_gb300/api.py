@@ -722,6 +722,8 @@ class RotaryPlan:
     """The frequencies of rotary positions, computed once.  scaling is one of
     "none", "linear", "base", "parts", "wavelength" (include/markov.h has their
     formulas) or "given", with frequencies [rot_dim / 2] in radians a position.
+    low and high are by default the numbers of turns that "parts" goes by; a model
+    that scales by "wavelength" has its own (often 1 and 4): give both.
     amplitude None: 0.1 ln(factor) + 1 with "parts", else 1."""
 
     def __init__(self, head_dim: int, rot_dim: int | None = None, theta: float = 10000.0,

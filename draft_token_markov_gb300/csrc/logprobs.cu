@@ -12,17 +12,23 @@
 // that reach it are read again (from L2; some 20 of 4000 for 20 alternatives of a row
 // of 129280), and what reaches it in them goes to a list, which is put in order by
 // counting.  Where the list is too short (many equal logits), the block takes its
-// maximum `top` times instead.  The cluster's first block joins sums and sorted
+// maximum `top` times instead, and a row whose maximum is too large for the fused form
+// (kFused) is read again for its sums.  The cluster's first block joins sums and sorted
 // lists, which the others write to its shared memory.
 //
 // ln p = (d - log2 Z) ln 2, entropy = (log2 Z - S / Z) ln 2.
 //
-// Bound by instructions: some 60 for 256 logits in the stream.  576 rows of 129280 BF16
-// logits, an eighth of them left out, with 20 alternatives (130 MB) take 44 us, 44% of
-// the copy rate; 9 rows in clusters of 8 blocks 11.3 us.  (Slices in shared memory and
-// read three times took 111 us, slices in registers with a bound for the cluster 86,
-// 9 rows 9.0; the stream without the next turn on its way 45.4, one logit an
-// instruction 44.8 to 45.9; against the maximum of the turn before it takes no less.)
+// At no unit's limit.  576 rows of 129280 BF16 logits with 20 alternatives (149 MB) take
+// 47 us, 47% of the copy rate, as long with every eighth left out; fp32 ones 65 us (298
+// MB, 69%); 9 rows in clusters of 8 blocks 11.2 and 13.1 us in a graph.  A multiprocessor that has
+// blocks issues 2.2 instructions of 4 a cycle (92 for 256 BF16 logits, all told), its
+// warps waiting for loads a third of the time and at the blocks' barriers a fifth; and
+// they have blocks 72% of the time, as rows are whole and some take four where others take
+// three.  The token is looked at before the first load, which costs 1.6 us of the 47.  (On
+// another card, with the load ahead of it, 44 us; there slices in shared memory and read
+// three times took 111 us, slices in registers with a bound for the cluster 86, 9 rows
+// 9.0; the stream without the next turn on its way 45.4, one logit an instruction 44.8 to
+// 45.9; against the maximum of the turn before it takes no less.)
 #include <atomic>
 #include <cmath>
 #include <cstddef>

@@ -528,7 +528,11 @@ markov_status markov_paged_attention_e4m3(
     // few against many: 64 requests of 500-16000 keys with 16 rows for each of 4 key heads
     // 72 and 87; 32 of them with 16 rows for each of 8 key heads 69 and 80, 24 rows 92 and
     // 81; 8 of 1000-16000 keys with 16 rows 38 and 34, of 32000 keys 106 and 141, 32 rows of
-    // 1000-16000 44 and 35
+    // 1000-16000 44 and 35.  These are of requests that are alike: of mixed ones one form
+    // takes all, and padding rows count.  64 single tokens and a chunk together and apart
+    // (8 key heads, 2000 keys and 500-8000): with 1 query head each and a chunk of 900 166
+    // and 98 + 32, of 2000 197 and 98 + 46 (430 with 400 padding rows), with 4 and 900 223 and
+    // 100 + 68 (382 with padding rows)
     const int64_t query_rows = (int64_t)num_tokens * group;
     const bool few = query_rows <= 16 * (int64_t)rows;
     // and of many, items of one row tile while a request has no more on average: a place for

@@ -36,11 +36,13 @@ __device__ __forceinline__ void unpack8(const uint4 &v, float (&x)[8]) {
 // in a chunk (single tokens of a batch) its warps take one each.
 // Up to kHeld * 128 vectors of a run stay in registers between the maximum and the
 // rounding, the rest is read again.  Rescaling comes before the new values, so that
-// it need not know which entries they replace.  Bound by latency (slots, values,
-// maximum one after the other) where a call is small, then by instructions as much as
-// by memory: 8192 tokens of 8 heads of 128 (50 MB, scales of 64 tokens) take 14.8 us
-// (51% of the copy rate), 72 tokens 4.2 us in a graph, 1000 single tokens 14.5 us.  With
-// the maximum in fp32 and divisions in the loop the first took 27 us.
+// it need not know which entries they replace.  Bound by latency: slots, scale, values and
+// maximum come one after the other.  8192 tokens of 8 heads of 128 (50 MB, scales of 64
+// tokens) take 15 us, 50% of the copy rate and 2.2 of 4 instructions a cycle, neither at
+// its limit, in two rounds of blocks; 72 tokens 3.7 us in a graph; 1000 single tokens 14.7
+// us for 1 us of bytes, as a warp takes its runs in turn.  With the maximum in fp32 and
+// divisions in the loop the first took 27 us.  With given scales, where every token is on
+// its own, the three take 15, 1.9 and 3.4 us.
 constexpr int kStoreThreads = 128;
 constexpr int kHeld = 8;
 constexpr int kMostChunk = 256;              // tokens of a chunk: a cache block at most
@@ -308,7 +310,8 @@ __global__ void __launch_bounds__(kFetchThreads) fetch_e4m3_kernel(const __grid_
     const int tid = threadIdx.x, t0 = blockIdx.x * a.tile, tokens = min(a.tile, a.r.T - t0);
     if (tid < tokens) {
         const int t = t0 + tid;
-        // the last row that begins at or before t, then back over empty ones
+        // the last row that begins at or before t: of those with the same start the last
+        // is the one that is not empty, or none is
         int lo = 0, hi = a.r.rows;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;

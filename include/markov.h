@@ -747,7 +747,10 @@ markov_status markov_paged_attention_e4m3(
  * fp32, the sums too; ln p of a masked id (a logit of -inf) is -inf.  T = +inf:
  * uniform over the ids whose logit is not -inf.  A row whose largest logit is NaN
  * or infinite is one-hot at the argmax, as in markov_verify: ln p is 0 there and
- * -inf elsewhere, the entropy 0.
+ * -inf elsewhere, the entropy 0.  Masks may be finite (the dtype's lowest value); ln p
+ * of an id that is below fp32's range is -inf.  Two kinds of row are right and slower:
+ * one where more than 512 logits reach the alternatives' bound (many equal ones) is
+ * read `top` times more, one whose |max / T| is 9e7 or more once.
  *   logits        [rows, vocab] of dtype (MARKOV_BF16 or MARKOV_F32), row stride
  *                 s0 >= vocab elements, aligned to its elements; vocab 1 .. 262144
  *   tokens        int64 [rows]; a row whose token is outside [0, vocab) (-1 past
